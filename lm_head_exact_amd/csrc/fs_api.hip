@@ -15,14 +15,15 @@
 #include <vector>
 
 #include "../../include/flashsample.h"
+#include "fs_host.hpp"
 #include "fs_internal.hpp"
 
 namespace {
-
 thread_local std::string g_last_error;
 std::atomic<int> g_forced_config{-1};
+}  // namespace
 
-fs_status fail(fs_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace fs {
 
 fs_status fail(fs_status s, const char* fmt, ...) {
   char buf[512];
@@ -38,14 +39,7 @@ fs_status hip_fail(hipError_t e, const char* what) {
   return fail(FS_ERR_HIP, "%s: %s (%d)", what, hipGetErrorString(e), static_cast<int>(e));
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Testing hook for failure handling: with FS_FAULT_INJECT=launch in the
-// environment, every entry point that would launch device work returns
-// FS_ERR_HIP once its arguments have passed the checks, before its first
-// launch, with the reason in fs_last_error(): the path a failed launch
-// takes, without a device and without launching anything.
-bool launch_fault_injected() {
+static bool launch_fault_injected() {
   const char* f = getenv("FS_FAULT_INJECT");
   return f != nullptr && std::strcmp(f, "launch") == 0;
 }
@@ -54,19 +48,21 @@ fs_status injected_failure(const char* who) {
   return fail(FS_ERR_HIP, "%s: launch failure injected (FS_FAULT_INJECT=launch)", who);
 }
 
-// Called by every launching entry point once its arguments have passed the
-// checks, just before its first HIP call; true when a failure is to be
-// injected (and then no HIP call is made).  HIP keeps one pending error per
-// host thread: any failed runtime call sets it, and the next hipGetLastError()
-// returns and clears it.  The launchers read it right after each launch, so an
-// error left pending by an earlier call (the caller's, or one of this
-// library's that has already returned its own status) is discarded here
-// rather than reported again against this call's launches.
 bool start_launches() {
   if (launch_fault_injected()) return true;
   (void)hipGetLastError();
   return false;
 }
+
+}  // namespace fs
+
+namespace {
+
+using fs::aligned;
+using fs::fail;
+using fs::hip_fail;
+using fs::injected_failure;
+using fs::start_launches;
 
 // Name of a configuration for messages (never a null pointer).
 const char* config_label(int cfg) {
