@@ -336,6 +336,167 @@ FS_API fs_status fs_sample_unfused(const void* h, const void* W, int32_t B, int3
                             float* out_maxval, void* workspace, size_t workspace_bytes,
                             void* stream);
 
+/* ---- training on sampled tokens ----
+ *
+ * What a user does with the tokens that the samplers above return: score them
+ * under a model (fs_token_logprobs), turn the scores into a loss and its
+ * gradient (fs_policy_loss, fs_preference_loss), take that gradient back
+ * through the LM head (fs_token_logprobs_backward) and clip gradients by
+ * their global norm (fs_clip_grad_norm).  All calls are asynchronous on
+ * `stream`, allocate nothing, take no atomics (equal calls give equal bits)
+ * and may be captured into graphs; calls that overlap need distinct
+ * workspaces and outputs.
+ */
+
+/* Log-probabilities of given tokens under softmax(z_b / T_b), z_b = W h_b, with
+ * no logits in memory.
+ *   h, W, B, D, V, vocab_offset  as fs_sample (D up to 2^20, B up to 2^24,
+ *                FS_ERR_UNSUPPORTED beyond); the _packed form reads W in
+ *                fragment order (fs_pack_weights, D % 32 == 0)
+ *   temperature  fp32 [B], device, or NULL (all 1).  As in the samplers the
+ *                logits are scaled by fp32(1/T), and a row whose temperature
+ *                is not a positive number is scored unscaled
+ *   token_ids    int32 [B], device: GLOBAL ids; negative: the row has none
+ *   out_logprob  fp32 [B]: log p(token); 0 for rows without a token; -inf for
+ *                a token outside [vocab_offset, vocab_offset + V)
+ *   out_lse      fp32 [B]: log sum_v exp(z_v / T) over these V rows
+ *   workspace    >= fs_token_logprobs_workspace_bytes(B, D, V) bytes (0 for
+ *                invalid sizes); contents on entry ignored
+ * On a vocabulary shard logprob + lse is the token's scaled logit on the rank
+ * that holds it and -inf elsewhere, and the log-sum-exp of the ranks' lse is
+ * the whole vocabulary's.  NaN entries of h or W give NaN in their rows. */
+FS_API size_t fs_token_logprobs_workspace_bytes(int32_t B, int32_t D, int32_t V);
+FS_API fs_status fs_token_logprobs(const void* h, const void* W, int32_t B, int32_t D, int32_t V,
+                                   int32_t vocab_offset, const float* temperature,
+                                   const int32_t* token_ids, float* out_logprob, float* out_lse,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+FS_API fs_status fs_token_logprobs_packed(const void* h, const void* W_packed, int32_t B, int32_t D,
+                                          int32_t V, int32_t vocab_offset, const float* temperature,
+                                          const int32_t* token_ids, float* out_logprob,
+                                          float* out_lse, void* workspace, size_t workspace_bytes,
+                                          void* stream);
+
+/* Gradients through fs_token_logprobs: with g = grad_logprob, p = exp(z / T -
+ * lse) and [.] 1 or 0,
+ *   dz_v = g / T ([v = token] (1 - exp(logprob)) - [v != token] p_v)
+ *   grad_h = dz W,  grad_W = dz^T h
+ * Rows without a token (negative id) have no gradient: their grad_h is 0 and
+ * their h, logprob, lse and grad_logprob are not used (they may be NaN).
+ *   h, W, B, D, V, vocab_offset, temperature, token_ids  as in the forward
+ *                call (row-major W; B up to 2^22)
+ *   logprob, lse fp32 [B]: the forward call's outputs; on a vocabulary shard
+ *                the whole vocabulary's (logprob is read only for the tokens
+ *                of this shard): grad_h is then this shard's share, to be
+ *                summed over the ranks, and grad_W its own rows
+ *   grad_h       bf16 [B][D], grad_W bf16 [V][D]; either may be NULL (not
+ *                wanted).  dz is rounded to bf16 between the products, sums
+ *                are fp32, results are rounded once
+ *   workspace    >= fs_token_logprobs_backward_workspace_bytes(B, D, V) bytes
+ *                (0 for invalid sizes; dz of up to 1 GiB of the vocabulary at
+ *                a time is held in it); contents on entry ignored
+ * B == 0 sets grad_W to 0. */
+FS_API size_t fs_token_logprobs_backward_workspace_bytes(int32_t B, int32_t D, int32_t V);
+FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_t B, int32_t D,
+                                            int32_t V, int32_t vocab_offset,
+                                            const float* temperature, const int32_t* token_ids,
+                                            const float* logprob, const float* lse,
+                                            const float* grad_logprob, void* grad_h, void* grad_W,
+                                            void* workspace, size_t workspace_bytes,
+                                            void* stream);
+
+/* Losses over a packed batch: sequence s holds tokens [cu_seqlens[s],
+ * cu_seqlens[s+1]) of the flat token arrays (int32 [n_sequences + 1], device,
+ * non-decreasing; offsets outside [0, n_tokens] are clamped to it).  Sequences
+ * may be empty.  mask is uint8 [n_tokens], device, or NULL: a token counts
+ * where it is nonzero.  Tokens that do not count get gradient 0 and their
+ * other entries are not used (they may be NaN); entries of out_grad outside
+ * every sequence are left as they were.  Sums are held in fp64.
+ * Up to 2^24 sequences (FS_ERR_UNSUPPORTED beyond).
+ *   workspace  >= fs_loss_workspace_bytes(n_sequences, n_tokens) bytes (for
+ *              the preference loss n_sequences = 2 * n_pairs), 0 for invalid
+ *              sizes; contents on entry ignored */
+FS_API size_t fs_loss_workspace_bytes(int32_t n_sequences, int32_t n_tokens);
+
+typedef enum { FS_KL_K1 = 1, FS_KL_K2 = 2, FS_KL_K3 = 3 } fs_kl_kind;
+typedef enum { FS_TOKEN_MEAN = 0, FS_SEQUENCE_MEAN = 1 } fs_loss_reduction;
+
+/* Clipped policy loss with a KL penalty, and its gradient.  Per token, with
+ * r = exp(logprob - old_logprob), q = ref_logprob - logprob and advantage A:
+ *   surrogate  -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A); with
+ *              dual_clip = c > 1 and A < 0 no larger than -c A (0: off)
+ *   kl         K1: -q;  K2: q^2 / 2;  K3: exp(q) - q - 1  (0 without a
+ *              reference)
+ *   loss       surrogate + kl_coef * kl
+ * averaged over the tokens that count (FS_TOKEN_MEAN) or, per sequence and
+ * then over the sequences that have such tokens (FS_SEQUENCE_MEAN).  Without
+ * any token that counts everything is 0.  A token has a surrogate gradient
+ * where r A attains the minimum and, with dual_clip, r is not above c.
+ *   logprob, old_logprob  fp32 [n_tokens];  ref_logprob fp32 [n_tokens] or NULL
+ *   advantages  fp32 [n_tokens] if advantage_per_token, else [n_sequences]
+ *   clip_low in [0, 1); clip_high >= 0; kl_coef, grad_scale finite
+ *   out_stats   fp32 [4]: loss, mean surrogate, mean kl, share of the tokens
+ *               that count whose surrogate is clipped
+ *   out_grad    fp32 [n_tokens]: grad_scale * d loss / d logprob */
+FS_API fs_status fs_policy_loss(const float* logprob, const float* old_logprob,
+                                const float* ref_logprob, const float* advantages,
+                                const uint8_t* mask, const int32_t* cu_seqlens,
+                                int32_t n_sequences, int32_t n_tokens,
+                                int32_t advantage_per_token, double clip_low, double clip_high,
+                                double dual_clip, double kl_coef, fs_kl_kind kl_kind,
+                                fs_loss_reduction reduction, double grad_scale, float* out_stats,
+                                float* out_grad, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+typedef enum {
+  FS_PREFERENCE_SIGMOID = 0,
+  FS_PREFERENCE_HINGE = 1,
+  FS_PREFERENCE_IPO = 2
+} fs_preference_kind;
+
+/* Preference loss of paired answers, and its gradient.  Sequences 0 ..
+ * n_pairs - 1 are the chosen answers, n_pairs .. 2 n_pairs - 1 the rejected
+ * ones (cu_seqlens int32 [2 n_pairs + 1]).  With S the sum over an answer's
+ * tokens that count (length_normalised: the mean) of logprob - ref_logprob
+ * (logprob alone without a reference), D = S_chosen - S_rejected and
+ * x = beta D - margin, a pair's loss is
+ *   SIGMOID  -(1 - e) log sigmoid(x) - e log sigmoid(-x), e = label_smoothing
+ *            in [0, 0.5]
+ *   HINGE    max(0, 1 - x)
+ *   IPO      (D - 1 / (2 beta))^2      (margin must be 0)
+ * averaged over the pairs both of whose answers have a token that counts; the
+ * other pairs have no loss and gradient 0.
+ *   beta        positive and finite
+ *   out_stats   fp32 [3]: loss, share of those pairs with D > 0, mean beta D
+ *   out_rewards fp32 [2 n_pairs]: beta S of every answer (0 for empty ones)
+ *   out_grad    fp32 [n_tokens]: grad_scale * d loss / d logprob */
+FS_API fs_status fs_preference_loss(const float* logprob, const float* ref_logprob,
+                                    const uint8_t* mask, const int32_t* cu_seqlens,
+                                    int32_t n_pairs, int32_t n_tokens, fs_preference_kind kind,
+                                    double beta, double margin, double label_smoothing,
+                                    int32_t length_normalised, double grad_scale, float* out_stats,
+                                    float* out_rewards, float* out_grad, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Clipping by the global norm: norm = sqrt(sum over all tensors of x^2), and
+ * every element times min(1, max_norm / (norm + 1e-6)).  A norm that is not
+ * finite scales nothing (out_norm tells it).
+ *   grads, out  HOST arrays of n device pointers; out[i] receives tensor i
+ *               and may equal grads[i]; out == NULL: in place.  Otherwise
+ *               tensors must not overlap one another.
+ *   numel       HOST int64 [n], each >= 0;  dtypes HOST fs_dtype [n]
+ *   (pointers aligned to their type; 16-byte aligned ones are read faster)
+ *   max_norm    >= 0, or infinity: the norm alone
+ *   out_norm    fp32 [1], device: the norm before clipping, summed in fp64
+ *   workspace   >= fs_clip_grad_norm_workspace_bytes(numel, n) bytes (0 for
+ *               invalid sizes)
+ * 0 <= n <= 65536.  The host arrays may be reused once the call returns. */
+typedef enum { FS_BF16 = 0, FS_FP16 = 1, FS_FP32 = 2 } fs_dtype;
+FS_API size_t fs_clip_grad_norm_workspace_bytes(const int64_t* numel, int32_t n);
+FS_API fs_status fs_clip_grad_norm(const void* const* grads, void* const* out,
+                                   const int64_t* numel, const fs_dtype* dtypes, int32_t n,
+                                   float max_norm, float* out_norm, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
 /* Diagnostics: the device noise field, from the same device functions the
  * samplers use.  Writes, for gv = gv0 .. gv0 + n - 1 of one (seed, step,
  * row), the raw Philox word (out_bits, may be NULL) and the Gumbel value g

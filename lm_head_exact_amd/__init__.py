@@ -12,7 +12,10 @@ _BINDING_NAMES = ("sample", "sample_partial", "merge", "sample_partial_lse", "me
                   "FlashSampleError", "alloc_workspace", "online_bounds", "sample_online",
                   "online_workspace_bytes", "pack_weights", "sample_packed",
                   "packed_weights_bytes", "device_info", "sample_packed_noalloc",
-                  "sample_groups_lse", "groups_workspace_bytes")
+                  "sample_groups_lse", "groups_workspace_bytes",
+                  "token_logprobs", "token_logprobs_workspace_bytes", "token_logprobs_backward",
+                  "token_logprobs_backward_workspace_bytes", "policy_loss", "preference_loss",
+                  "loss_workspace_bytes", "clip_grad_norm")
 __all__ = list(_BINDING_NAMES)
 
 

@@ -50,6 +50,7 @@ def lib():
     L = ctypes.CDLL(_LIB_PATH)
     vp, i32, u32, i64, u64, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32,
                                   ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t)
+    f64 = ctypes.c_double
     sample_args = [vp, vp, i32, i32, i32, i32, vp, u64, u64, vp, vp, vp, sz, vp]
     for name, args, res in [
         ("fs_workspace_bytes", [i32, i32, i32], sz),
@@ -81,6 +82,21 @@ def lib():
                               vp, vp, sz, vp], ctypes.c_int),
         ("fs_sample_online_packed", [vp, vp, i32, i32, i32, i32, vp, u64, u64, vp, i32, vp, vp,
                                      vp, vp, vp, sz, vp], ctypes.c_int),
+        ("fs_token_logprobs_workspace_bytes", [i32, i32, i32], sz),
+        ("fs_token_logprobs", [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp],
+         ctypes.c_int),
+        ("fs_token_logprobs_packed", [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp],
+         ctypes.c_int),
+        ("fs_token_logprobs_backward_workspace_bytes", [i32, i32, i32], sz),
+        ("fs_token_logprobs_backward", [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp,
+                                        sz, vp], ctypes.c_int),
+        ("fs_loss_workspace_bytes", [i32, i32], sz),
+        ("fs_policy_loss", [vp, vp, vp, vp, vp, vp, i32, i32, i32, f64, f64, f64, f64, ctypes.c_int,
+                            ctypes.c_int, f64, vp, vp, vp, sz, vp], ctypes.c_int),
+        ("fs_preference_loss", [vp, vp, vp, vp, i32, i32, ctypes.c_int, f64, f64, f64, i32, f64, vp,
+                                vp, vp, vp, sz, vp], ctypes.c_int),
+        ("fs_clip_grad_norm_workspace_bytes", [vp, i32], sz),
+        ("fs_clip_grad_norm", [vp, vp, vp, vp, i32, ctypes.c_float, vp, vp, sz, vp], ctypes.c_int),
         ("fs_debug_noise", [u64, u64, u32, u32, i64, vp, vp, vp], ctypes.c_int),
         ("fs_debug_gumbel", [vp, i64, vp, vp], ctypes.c_int),
         ("fs_device_info", [i32, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)],
@@ -554,3 +570,258 @@ def selected_config(B: int, D: int, V: int, packed: bool = False, grouped: bool 
         return int(lib().fs_selected_config_groups(B, D, V, int(packed)))
     fn = lib().fs_selected_config_packed if packed else lib().fs_selected_config
     return int(fn(B, D, V))
+
+
+# ---- training on sampled tokens ----
+# These calls run on the device of their tensors, whatever the current device
+# is, and on torch's current stream of that device.
+
+def _out(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _req(t, name, dtype, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if t.device != device:
+        raise ValueError("all tensors must be on one device")
+    return t
+
+
+def _workspace(t: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
+    if t is None:
+        return alloc_workspace(nbytes, device)
+    if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return t
+
+
+def _nbytes(t: torch.Tensor) -> int:
+    return t.numel() * t.element_size()
+
+
+def _row(t: Optional[torch.Tensor], name: str, dtype, n: int, device):
+    if t is None:
+        return
+    _req(t, name, dtype, 1)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries (got {t.shape[0]})")
+    if t.device != device:
+        raise ValueError("all tensors must be on one device")
+
+
+def token_logprobs_workspace_bytes(B: int, D: int, V: int) -> int:
+    return int(lib().fs_token_logprobs_workspace_bytes(B, D, V))
+
+
+def token_logprobs(h: torch.Tensor, W: torch.Tensor, temperature: Optional[torch.Tensor],
+                   token_ids: torch.Tensor, vocab_offset: int = 0, out=None,
+                   workspace: Optional[torch.Tensor] = None, V: Optional[int] = None):
+    """fs_token_logprobs: (log-probability fp32 [B] of each row's token under
+    softmax(W h / T), log-sum-exp fp32 [B]), with no logits in memory.
+    token_ids are global ids (int32); rows with a negative id have none and get
+    log-probability 0, ids outside this W's rows get -inf.  temperature None
+    means 1.  W is row-major V x D, or (1-D, with V given) its fragment-order
+    copy from pack_weights at the same vocab_offset."""
+    _req(h, "h", torch.bfloat16, 2)
+    packed = isinstance(W, torch.Tensor) and W.dim() == 1
+    _req(W, "W", torch.bfloat16, 1 if packed else 2)
+    B, D = h.shape
+    if packed:
+        if V is None:
+            raise ValueError("V is required with fragment-order W")
+        need = packed_weights_bytes(V, D, vocab_offset)
+        if need == 0 or W.numel() * 2 < need:
+            raise ValueError(f"W_packed holds {W.numel() * 2} bytes; {need} needed")
+    else:
+        if V is not None and V != W.shape[0]:
+            raise ValueError(f"V is {V} but W has {W.shape[0]} rows")
+        V = W.shape[0]
+        if W.shape[1] != D:
+            raise ValueError(f"h is B x {D} but W is V x {W.shape[1]}")
+    dev = h.device
+    if W.device != dev:
+        raise ValueError("all tensors must be on one device")
+    _row(temperature, "temperature", torch.float32, B, dev)
+    _row(token_ids, "token_ids", torch.int32, B, dev)
+    lp, lse = (None, None) if out is None else out
+    lp = _out(lp, "logprob", (B,), torch.float32, dev)
+    lse = _out(lse, "lse", (B,), torch.float32, dev)
+    ws = _workspace(workspace, token_logprobs_workspace_bytes(B, D, V), dev)
+    fn = lib().fs_token_logprobs_packed if packed else lib().fs_token_logprobs
+    with torch.cuda.device(dev):
+        _check(fn(_ptr(h), _ptr(W), B, D, V, int(vocab_offset), _ptr(temperature), _ptr(token_ids),
+                  _ptr(lp), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(dev)))
+    return lp, lse
+
+
+def token_logprobs_backward_workspace_bytes(B: int, D: int, V: int) -> int:
+    return int(lib().fs_token_logprobs_backward_workspace_bytes(B, D, V))
+
+
+def token_logprobs_backward(h: torch.Tensor, W: torch.Tensor, temperature: Optional[torch.Tensor],
+                            token_ids: torch.Tensor, logprob: torch.Tensor, lse: torch.Tensor,
+                            grad_logprob: torch.Tensor, vocab_offset: int = 0, need_h: bool = True,
+                            need_W: bool = True, out=None,
+                            workspace: Optional[torch.Tensor] = None):
+    """fs_token_logprobs_backward: (grad_h bf16 [B][D], grad_W bf16 [V][D]) from
+    the gradient of the log-probabilities; logprob and lse are the forward
+    call's.  need_h / need_W false: that product is skipped and None returned.
+    out: (grad_h, grad_W) to write into, either None."""
+    _req(h, "h", torch.bfloat16, 2)
+    _req(W, "W", torch.bfloat16, 2)
+    B, D = h.shape
+    V = W.shape[0]
+    if W.shape[1] != D:
+        raise ValueError(f"h is B x {D} but W is V x {W.shape[1]}")
+    dev = h.device
+    if W.device != dev:
+        raise ValueError("all tensors must be on one device")
+    _row(temperature, "temperature", torch.float32, B, dev)
+    _row(token_ids, "token_ids", torch.int32, B, dev)
+    for t, name in ((logprob, "logprob"), (lse, "lse"), (grad_logprob, "grad_logprob")):
+        _row(t, name, torch.float32, B, dev)
+    gh, gw = (None, None) if out is None else out
+    gh = _out(gh, "grad_h", (B, D), torch.bfloat16, dev) if need_h else None
+    gw = _out(gw, "grad_W", (V, D), torch.bfloat16, dev) if need_W else None
+    ws = _workspace(workspace, token_logprobs_backward_workspace_bytes(B, D, V), dev)
+    with torch.cuda.device(dev):
+        _check(lib().fs_token_logprobs_backward(
+            _ptr(h), _ptr(W), B, D, V, int(vocab_offset), _ptr(temperature), _ptr(token_ids),
+            _ptr(logprob), _ptr(lse), _ptr(grad_logprob), _ptr(gh), _ptr(gw), _ptr(ws), _nbytes(ws),
+            _stream(dev)))
+    return gh, gw
+
+
+def loss_workspace_bytes(n_sequences: int, n_tokens: int) -> int:
+    return int(lib().fs_loss_workspace_bytes(n_sequences, n_tokens))
+
+
+def _sequences(logprob, cu_seqlens, mask, **rows):
+    """Common checks of the losses; returns (device, tokens, mask as uint8)."""
+    _req(logprob, "logprob", torch.float32, 1)
+    dev, N = logprob.device, logprob.shape[0]
+    _req(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    if cu_seqlens.device != dev:
+        raise ValueError("all tensors must be on one device")
+    if cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must have at least one entry")
+    for name, t in rows.items():
+        _row(t, name, torch.float32, N, dev)
+    if mask is not None:
+        if mask.dtype == torch.bool:
+            mask = mask.view(torch.uint8)
+        _row(mask, "mask", torch.uint8, N, dev)
+    return dev, N, mask
+
+
+_KL = {"k1": 1, "k2": 2, "k3": 3}
+_REDUCTIONS = {"token": 0, "sequence": 1}
+_PREFERENCES = {"sigmoid": 0, "hinge": 1, "ipo": 2}
+
+
+def _choice(table, value, name):
+    if value not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)} (got {value!r})")
+    return table[value]
+
+
+def policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages: torch.Tensor,
+                cu_seqlens: torch.Tensor, ref_logprob: Optional[torch.Tensor] = None,
+                mask: Optional[torch.Tensor] = None, per_token: bool = False,
+                clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0,
+                kl_coef: float = 0.0, kl: str = "k3", reduction: str = "token",
+                grad_scale: float = 1.0, out=None, workspace: Optional[torch.Tensor] = None):
+    """fs_policy_loss over packed sequences (tokens cu_seqlens[s] to
+    cu_seqlens[s + 1] of the flat fp32 arrays): returns (stats fp32 [4], grad
+    fp32 [tokens]); stats are the loss, the mean surrogate, the mean KL and
+    the clipped share, grad is grad_scale * d loss / d logprob.  advantages
+    holds one value per sequence, or with per_token one per token.  mask (bool
+    or uint8): the tokens that count.  With `out` = (stats, grad) the entries
+    of grad outside every sequence are left as they were."""
+    dev, N, m = _sequences(logprob, cu_seqlens, mask, old_logprob=old_logprob,
+                           ref_logprob=ref_logprob)
+    S = cu_seqlens.shape[0] - 1
+    _row(advantages, "advantages", torch.float32, N if per_token else S, dev)
+    stats, grad = (None, None) if out is None else out
+    stats = _out(stats, "stats", (4,), torch.float32, dev)
+    grad = _out(grad, "grad", (N,), torch.float32, dev)
+    ws = _workspace(workspace, loss_workspace_bytes(S, N), dev)
+    with torch.cuda.device(dev):
+        _check(lib().fs_policy_loss(
+            _ptr(logprob), _ptr(old_logprob), _ptr(ref_logprob), _ptr(advantages), _ptr(m),
+            _ptr(cu_seqlens), S, N, int(per_token), clip_low, clip_high, dual_clip, kl_coef,
+            _choice(_KL, kl, "kl"), _choice(_REDUCTIONS, reduction, "reduction"), grad_scale,
+            _ptr(stats), _ptr(grad), _ptr(ws), _nbytes(ws), _stream(dev)))
+    return stats, grad
+
+
+def preference_loss(logprob: torch.Tensor, cu_seqlens: torch.Tensor,
+                    ref_logprob: Optional[torch.Tensor] = None,
+                    mask: Optional[torch.Tensor] = None, kind: str = "sigmoid", beta: float = 0.1,
+                    margin: float = 0.0, label_smoothing: float = 0.0,
+                    length_normalised: bool = False, grad_scale: float = 1.0, out=None,
+                    workspace: Optional[torch.Tensor] = None):
+    """fs_preference_loss over packed sequences, the chosen answers first and
+    then the rejected ones in the same order (cu_seqlens has 2 P + 1 entries):
+    returns (stats fp32 [3], rewards fp32 [2 P], grad fp32 [tokens]); stats are
+    the loss, the share of pairs that prefer the chosen answer and the mean
+    margin of rewards.  With `out` = (stats, rewards, grad) the entries of grad
+    outside every sequence are left as they were."""
+    dev, N, m = _sequences(logprob, cu_seqlens, mask, ref_logprob=ref_logprob)
+    S = cu_seqlens.shape[0] - 1
+    if S % 2:
+        raise ValueError("cu_seqlens must describe chosen and rejected answers: 2 P + 1 entries")
+    stats, rewards, grad = (None, None, None) if out is None else out
+    stats = _out(stats, "stats", (3,), torch.float32, dev)
+    rewards = _out(rewards, "rewards", (S,), torch.float32, dev)
+    grad = _out(grad, "grad", (N,), torch.float32, dev)
+    ws = _workspace(workspace, loss_workspace_bytes(S, N), dev)
+    with torch.cuda.device(dev):
+        _check(lib().fs_preference_loss(
+            _ptr(logprob), _ptr(ref_logprob), _ptr(m), _ptr(cu_seqlens), S // 2, N,
+            _choice(_PREFERENCES, kind, "kind"), beta, margin, label_smoothing,
+            int(length_normalised), grad_scale, _ptr(stats), _ptr(rewards), _ptr(grad), _ptr(ws),
+            _nbytes(ws), _stream(dev)))
+    return stats, rewards, grad
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, norm: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """fs_clip_grad_norm: scales the gradients (a list of contiguous bf16, fp16
+    or fp32 device tensors) in place, or into the tensors of `out`, by min(1,
+    max_norm / (norm + 1e-6)) and returns their global norm before that (fp32
+    [1], on the device).  A norm that is not finite scales nothing."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads must hold at least one tensor")
+    dev = grads[0].device
+    n = len(grads)
+    outs = grads if out is None else list(out)
+    if len(outs) != n:
+        raise ValueError(f"out must hold {n} tensors (got {len(outs)})")
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        for t, name in ((g, "grads"), (o, "out")):
+            if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
+                raise TypeError(f"{name}[{i}] must be a bf16, fp16 or fp32 tensor")
+            if t.device.type != "cuda" or t.device != dev:
+                raise ValueError(f"{name}[{i}] must be on the first gradient's device")
+            if not t.is_contiguous():
+                raise ValueError(f"{name}[{i}] must be contiguous")
+        if o.dtype != g.dtype or o.shape != g.shape:
+            raise ValueError(f"out[{i}] must have the type and shape of grads[{i}]")
+    spans = sorted((t.data_ptr(), t.data_ptr() + _nbytes(t)) for t in outs if t.numel())
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+        raise ValueError("the tensors written must not overlap")
+    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    types = (ctypes.c_int * n)(*[_DTYPES[g.dtype] for g in grads])
+    src = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+    dst = None if out is None else (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs])
+    norm = _out(norm, "norm", (1,), torch.float32, dev)
+    ws = _workspace(workspace, int(lib().fs_clip_grad_norm_workspace_bytes(sizes, n)), dev)
+    with torch.cuda.device(dev):
+        _check(lib().fs_clip_grad_norm(src, dst, sizes, types, n, max_norm, _ptr(norm), _ptr(ws),
+                                       _nbytes(ws), _stream(dev)))
+    return norm

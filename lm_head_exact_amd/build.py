@@ -16,7 +16,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libflashsample.so")
 SOURCES = ["fs_configs_dma_a.hip", "fs_configs_dma_b.hip", "fs_configs_dma_ntl.hip", "fs_configs_lds.hip",
            "fs_configs_small.hip", "fs_fused.hip", "fs_api.hip", "fs_unfused.hip",
-           "fs_online.hip", "fs_pack.hip"]
+           "fs_online.hip", "fs_pack.hip", "fs_loss.hip", "fs_clip.hip",
+           "fs_logprob.hip", "fs_logprob_grad.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,308 @@
+// fs_clip.hip -- the global norm of many gradient tensors, and clipping by it.
+//
+//   norm  = sqrt(sum_i sum_j x_ij^2),   y_ij = x_ij * min(1, max / (norm + 1e-6))
+//
+// Three steps: each block sums the squares of one chunk (fp64 throughout: no
+// gradient's square overflows, and a sum of 10^9 terms loses nothing), one
+// block adds the chunks in order and closes the norm, and each block scales
+// its chunk; where nothing is to be scaled in place the last step's blocks
+// return at once.  Bound by HBM: one read for the norm, one read and one
+// write for the scaling, since the scale is known only after the last element.
+// Tensors go to the device as tables in kernel arguments, kTable to a launch,
+// so that nothing is copied or kept.
+#include <cmath>
+
+#include "fs_host.hpp"
+#include "fs_device.hpp"
+#include "fs_internal.hpp"
+
+namespace fs {
+namespace {
+
+constexpr int kClipThreads = 256;
+constexpr int kTable = 96;              // 96 * 32 + ... bytes: below the 4 KB of kernel arguments
+constexpr int kVec = 16;                // bytes a lane loads at once
+constexpr int kUnroll = 4;
+// Bytes of input per block.
+constexpr int64_t kChunkBytes = 64 << 10;
+constexpr int32_t kMaxTensors = 65536;
+
+struct ClipTable {
+  const void* in[kTable];
+  void* out[kTable];
+  int64_t numel[kTable];
+  int32_t first[kTable + 1];  // first block of each tensor in this launch
+  uint8_t dtype[kTable];
+  int32_t n;
+  int32_t base;               // chunk index of the launch's first block
+};
+
+struct ClipItem {
+  const void* in;
+  void* out;
+  int64_t beg, end;  // elements
+  int32_t dtype;
+};
+
+__host__ __device__ constexpr int type_bytes(int dtype) { return dtype == FS_FP32 ? 4 : 2; }
+__host__ __device__ constexpr int64_t chunk_elems(int dtype) { return kChunkBytes / type_bytes(dtype); }
+
+// The block's tensor and elements.  Thread k looks at entry k; the one whose
+// blocks hold this one publishes the entry.
+__device__ __forceinline__ ClipItem clip_item(const ClipTable& t) {
+  __shared__ ClipItem item;
+  const int k = threadIdx.x, b = blockIdx.x;
+  if (k < t.n && t.first[k] <= b && b < t.first[k + 1]) {
+    const int d = t.dtype[k];
+    const int64_t beg = static_cast<int64_t>(b - t.first[k]) * chunk_elems(d);
+    const int64_t end = beg + chunk_elems(d);
+    item = {t.in[k], t.out[k], beg, end < t.numel[k] ? end : t.numel[k], d};
+  }
+  __syncthreads();
+  return item;
+}
+
+template <int DT>
+struct Elem;
+template <>
+struct Elem<FS_FP32> {
+  using T = float;
+  __device__ __forceinline__ static float get(T x) { return x; }
+  __device__ __forceinline__ static T put(float x) { return x; }
+};
+template <>
+struct Elem<FS_BF16> {
+  using T = __bf16;
+  __device__ __forceinline__ static float get(T x) { return static_cast<float>(x); }
+  __device__ __forceinline__ static T put(float x) { return static_cast<__bf16>(x); }
+};
+template <>
+struct Elem<FS_FP16> {
+  using T = _Float16;
+  __device__ __forceinline__ static float get(T x) { return static_cast<float>(x); }
+  __device__ __forceinline__ static T put(float x) { return static_cast<_Float16>(x); }
+};
+
+template <int DT>
+__device__ __forceinline__ double sum_squares(const ClipItem& it) {
+  using E = Elem<DT>;
+  using T = typename E::T;
+  constexpr int N = kVec / sizeof(T);
+  const T* p = static_cast<const T*>(it.in);
+  double s[kUnroll] = {};
+  int64_t i = it.beg;
+  if ((reinterpret_cast<uintptr_t>(p + it.beg) & (kVec - 1)) == 0) {
+    typedef T V __attribute__((ext_vector_type(N)));
+    constexpr int64_t kStep = static_cast<int64_t>(kClipThreads) * N;
+    for (; i + kUnroll * kStep <= it.end; i += kUnroll * kStep) {
+      V v[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        v[u] = *reinterpret_cast<const V*>(p + i + u * kStep + threadIdx.x * N);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const double x = E::get(v[u][j]);
+          s[u] = __builtin_fma(x, x, s[u]);
+        }
+    }
+  }
+  for (i += threadIdx.x; i < it.end; i += kClipThreads) {
+    const double x = E::get(p[i]);
+    s[0] = __builtin_fma(x, x, s[0]);
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+template <int THREADS>
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double s[THREADS / kWave];
+#pragma unroll
+  for (int m = kWave / 2; m >= 1; m >>= 1) v += __shfl_xor(v, m, kWave);
+  if ((threadIdx.x & (kWave - 1)) == 0) s[threadIdx.x / kWave] = v;
+  __syncthreads();
+  double r = s[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / kWave; ++w) r += s[w];
+  return r;
+}
+
+__global__ __launch_bounds__(kClipThreads) void squares_kernel(ClipTable t, double* part) {
+  const ClipItem it = clip_item(t);
+  const double s = it.dtype == FS_FP32   ? sum_squares<FS_FP32>(it)
+                   : it.dtype == FS_BF16 ? sum_squares<FS_BF16>(it)
+                                         : sum_squares<FS_FP16>(it);
+  const double all = block_sum<kClipThreads>(s);
+  if (threadIdx.x == 0) part[t.base + static_cast<int>(blockIdx.x)] = all;
+}
+
+constexpr int kCloseThreads = 1024;
+
+__global__ __launch_bounds__(kCloseThreads) void norm_kernel(const double* part, int32_t n,
+                                                             float max_norm, float* out_norm,
+                                                             float* scale) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += kCloseThreads) s += part[i];
+  const double norm = sqrt(block_sum<kCloseThreads>(s));
+  if (threadIdx.x == 0) {
+    *out_norm = static_cast<float>(norm);
+    const double c = static_cast<double>(max_norm) / (norm + 1e-6);
+    *scale = isfinite(norm) && c < 1.0 ? static_cast<float>(c) : 1.0f;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void scale_chunk(const ClipItem& it, float c) {
+  using E = Elem<DT>;
+  using T = typename E::T;
+  constexpr int N = kVec / sizeof(T);
+  const T* p = static_cast<const T*>(it.in);
+  T* q = static_cast<T*>(it.out);
+  int64_t i = it.beg;
+  if (((reinterpret_cast<uintptr_t>(p + it.beg) | reinterpret_cast<uintptr_t>(q + it.beg)) &
+       (kVec - 1)) == 0) {
+    typedef T V __attribute__((ext_vector_type(N)));
+    constexpr int64_t kStep = static_cast<int64_t>(kClipThreads) * N;
+    for (; i + kUnroll * kStep <= it.end; i += kUnroll * kStep) {
+      V v[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        v[u] = *reinterpret_cast<const V*>(p + i + u * kStep + threadIdx.x * N);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[u][j] = E::put(E::get(v[u][j]) * c);
+        *reinterpret_cast<V*>(q + i + u * kStep + threadIdx.x * N) = v[u];
+      }
+    }
+  }
+  for (i += threadIdx.x; i < it.end; i += kClipThreads) q[i] = E::put(E::get(p[i]) * c);
+}
+
+__global__ __launch_bounds__(kClipThreads) void scale_kernel(ClipTable t, const float* scale) {
+  const float c = *scale;
+  const ClipItem it = clip_item(t);
+  if (c == 1.0f && it.in == it.out) return;  // nothing to change (uniform)
+  if (it.dtype == FS_FP32) scale_chunk<FS_FP32>(it, c);
+  else if (it.dtype == FS_BF16) scale_chunk<FS_BF16>(it, c);
+  else scale_chunk<FS_FP16>(it, c);
+}
+
+int64_t tensor_blocks(int64_t numel, int dtype) {
+  return (numel + chunk_elems(dtype) - 1) / chunk_elems(dtype);
+}
+
+// Fills tables and calls launch(table, blocks) for each, in order.
+template <class F>
+hipError_t for_each_table(const void* const* grads, void* const* out, const int64_t* numel,
+                          const fs_dtype* dtypes, int32_t n, F launch) {
+  ClipTable t;
+  t.n = 0;
+  t.base = 0;
+  int64_t blocks = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (numel[i] > 0) {
+      t.in[t.n] = grads[i];
+      t.out[t.n] = out ? out[i] : const_cast<void*>(grads[i]);
+      t.numel[t.n] = numel[i];
+      t.dtype[t.n] = static_cast<uint8_t>(dtypes[i]);
+      t.first[t.n] = static_cast<int32_t>(blocks);
+      blocks += tensor_blocks(numel[i], dtypes[i]);
+      t.first[++t.n] = static_cast<int32_t>(blocks);
+    }
+    if (t.n > 0 && (t.n == kTable || i == n - 1)) {
+      const hipError_t e = launch(t, static_cast<unsigned>(blocks));
+      if (e != hipSuccess) return e;
+      t.base += static_cast<int32_t>(blocks);
+      t.n = 0;
+      blocks = 0;
+    }
+  }
+  return hipSuccess;
+}
+
+// Chunks of all tensors at the finest type's chunk (an upper bound), or -1.
+int64_t max_chunks(const int64_t* numel, int32_t n) {
+  if (n < 0 || n > kMaxTensors || (n > 0 && !numel)) return -1;
+  int64_t c = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (numel[i] < 0 || numel[i] > (int64_t{1} << 44)) return -1;
+    c += tensor_blocks(numel[i], FS_FP32);
+    if (c > 0x7FFFFFFF) return -1;
+  }
+  return c;
+}
+
+constexpr size_t kScaleBytes = 256;
+
+size_t clip_workspace(int64_t chunks) {
+  return kScaleBytes + round_up(sizeof(double) * static_cast<size_t>(chunks), 256);
+}
+
+}  // namespace
+}  // namespace fs
+
+extern "C" {
+
+FS_API size_t fs_clip_grad_norm_workspace_bytes(const int64_t* numel, int32_t n) {
+  const int64_t c = fs::max_chunks(numel, n);
+  return c < 0 ? 0 : fs::clip_workspace(c);
+}
+
+FS_API fs_status fs_clip_grad_norm(const void* const* grads, void* const* out,
+                                   const int64_t* numel, const fs_dtype* dtypes, int32_t n,
+                                   float max_norm, float* out_norm, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  using namespace fs;
+  const char* who = "fs_clip_grad_norm";
+  if (n < 0 || n > kMaxTensors)
+    return fail(FS_ERR_INVALID_ARG, "%s: n must be in [0, %d] (got %d)", who, kMaxTensors, n);
+  if (n > 0 && (!grads || !numel || !dtypes))
+    return fail(FS_ERR_INVALID_ARG, "%s: null host array", who);
+  for (int32_t i = 0; i < n; ++i) {
+    if (dtypes[i] != FS_BF16 && dtypes[i] != FS_FP16 && dtypes[i] != FS_FP32)
+      return fail(FS_ERR_INVALID_ARG, "%s: unknown dtype %d of tensor %d", who,
+                  static_cast<int>(dtypes[i]), i);
+    if (numel[i] < 0)
+      return fail(FS_ERR_INVALID_ARG, "%s: numel of tensor %d is negative", who, i);
+    if (numel[i] == 0) continue;
+    const size_t a = type_bytes(dtypes[i]);
+    if (!grads[i] || !aligned(grads[i], a) || (out && (!out[i] || !aligned(out[i], a))))
+      return fail(FS_ERR_INVALID_ARG, "%s: pointer of tensor %d is null or misaligned", who, i);
+  }
+  const int64_t chunks = max_chunks(numel, n);
+  if (chunks < 0) return fail(FS_ERR_UNSUPPORTED, "%s: more elements than one call can take", who);
+  if (!(max_norm >= 0.0f))
+    return fail(FS_ERR_INVALID_ARG, "%s: max_norm must be >= 0 (got %g)", who, max_norm);
+  if (!out_norm || !aligned(out_norm, 4))
+    return fail(FS_ERR_INVALID_ARG, "%s: out_norm must be a 4-byte aligned device pointer", who);
+  if (!workspace || !aligned(workspace, 256))
+    return fail(FS_ERR_INVALID_ARG, "%s: workspace must be a 256-byte aligned device pointer", who);
+  const size_t need = clip_workspace(chunks);
+  if (workspace_bytes < need)
+    return fail(FS_ERR_WORKSPACE, "%s: workspace of %zu bytes is below the %zu required", who,
+                workspace_bytes, need);
+  if (start_launches()) return injected_failure(who);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  float* scale = static_cast<float*>(workspace);
+  double* part = reinterpret_cast<double*>(static_cast<char*>(workspace) + kScaleBytes);
+  int64_t used = 0;
+  hipError_t e = for_each_table(grads, out, numel, dtypes, n, [&](const ClipTable& t, unsigned b) {
+    squares_kernel<<<b, kClipThreads, 0, st>>>(t, part);
+    used += b;
+    return hipGetLastError();
+  });
+  if (e != hipSuccess) return hip_fail(e, "gradient norm launch");
+  norm_kernel<<<1, kCloseThreads, 0, st>>>(part, static_cast<int32_t>(used), max_norm, out_norm,
+                                           scale);
+  if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "gradient norm launch");
+  if (out == nullptr && std::isinf(max_norm)) return FS_OK;
+  e = for_each_table(grads, out, numel, dtypes, n, [&](const ClipTable& t, unsigned b) {
+    scale_kernel<<<b, kClipThreads, 0, st>>>(t, scale);
+    return hipGetLastError();
+  });
+  return e == hipSuccess ? FS_OK : hip_fail(e, "gradient scaling launch");
+}
+
+}  // extern "C"

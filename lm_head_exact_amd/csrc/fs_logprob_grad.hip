@@ -1,0 +1,486 @@
+// fs_logprob_grad.hip -- gradients of token log-probabilities with respect to
+// the hidden states and the LM head (fs_token_logprobs_backward).
+//
+// With t = z * fp32(1/T) the scaled logits, p_v = exp(t_v - lse) and g the
+// incoming gradient of a row's log-probability,
+//   dz_v = g/T * ( [v = target] (1 - p_target) - [v != target] p_v )
+//   dh = dz W,   dW = dz^T h
+// 1 - p_target is -expm1(logprob) of the forward pass: from p itself it would
+// be noise where the target is nearly certain.  Rows without a target (prompt
+// or padding tokens) have no gradient: they are dropped before the products,
+// so they cost nothing and NaN in their hidden states stays there.
+//
+// dz (B x V) is made in bf16, one slice of the vocabulary at a time, from the
+// logits recomputed on chip; both products read it back from the workspace
+// (MFMA takes bf16 operands: every dz is rounded once, 2^-9 relative, as are
+// the two results).  Three matrix products of 2 B V D operations each bound
+// the call for batches of training; a batch of a few rows is bound by reading
+// W twice and writing dW.
+#include <cmath>
+
+#include "fs_host.hpp"
+#include "fs_score.hpp"
+#include "fs_sampler.hpp"
+
+namespace fs {
+namespace {
+
+// Per row that has a target, in order.
+struct RowTerm {
+  float c;       // log2(e) / T
+  float lse2;    // log2(e) * lse
+  float coef;    // -g / T
+  float target;  // g / T * (1 - p_target)
+};
+
+struct GradArgs {
+  const __bf16 *h, *W;
+  int32_t B, D, V, vocab_offset;
+  const float *temperature, *logprob, *lse, *grad;
+  const int32_t* ids;
+  __bf16 *dh, *dW;    // either may be null
+  // workspace
+  int32_t* count;     // rows with a target
+  int32_t* slot;      // [B]: their place among them, or -1
+  int32_t* row;       // [Bp]: the inverse
+  int32_t* loc;       // [Bp]: target's row of W, or -1
+  RowTerm* term;      // [Bp]
+  __bf16* hz;         // [Bp][Dp]: their hidden states, zeros behind them
+  __bf16* dz;         // [Bp][ldz]
+  float* slab;        // [splits][Bp][D] or null
+  int32_t Dp, Bp, ldz;
+  int32_t v0, nv;     // the slice: rows v0 .. v0 + nv of W
+  int32_t splits, first_slice;
+};
+
+// A row counts where it has a token; a token of another shard still gives
+// every row of this one a gradient.
+__device__ __forceinline__ bool has_token(int32_t id) { return id >= 0; }
+
+constexpr int kScanThreads = 1024;
+
+// Places of the rows that have a token, in order (one block).
+__global__ __launch_bounds__(kScanThreads) void grad_rows_kernel(GradArgs a) {
+  constexpr int kWaves = kScanThreads / kWave;
+  __shared__ int32_t s[kWaves];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  int base = 0;
+  for (int64_t b0 = 0; b0 < a.B; b0 += kScanThreads) {
+    const int64_t b = b0 + threadIdx.x;
+    const bool on = b < a.B && has_token(a.ids[b]);
+    const uint64_t votes = __ballot(on);
+    if (lane == 0) s[wave] = __popcll(votes);
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      before += w < wave ? s[w] : 0;
+      all += s[w];
+    }
+    const int at = base + before + __popcll(votes & ((uint64_t{1} << lane) - 1));
+    if (b < a.B) {
+      a.slot[b] = on ? at : -1;
+      if (on) a.row[at] = static_cast<int32_t>(b);
+    }
+    base += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *a.count = base;
+}
+
+// Row b < B: its terms and a copy of its hidden state at its place, or a zero
+// gradient.  Rows B .. B + 255: zeros up to the next multiple of 256 places.
+__global__ __launch_bounds__(256) void grad_gather_kernel(GradArgs a) {
+  const int b = blockIdx.x;
+  const int n = *a.count;
+  int at;
+  if (b < a.B) {
+    at = a.slot[b];
+    if (at < 0) {
+      if (a.dh != nullptr)
+        for (int k = threadIdx.x * 8; k < a.D; k += 256 * 8)
+          *reinterpret_cast<bf16x8*>(a.dh + static_cast<size_t>(b) * a.D + k) = zero_frag();
+      return;
+    }
+    for (int k = threadIdx.x * 8; k < a.Dp; k += 256 * 8)
+      *reinterpret_cast<bf16x8*>(a.hz + static_cast<size_t>(at) * a.Dp + k) =
+          k < a.D ? load_frag(a.h + static_cast<size_t>(b) * a.D + k) : zero_frag();
+  } else {
+    at = n + (b - a.B);
+    if (at >= (n + 255) / 256 * 256) return;
+    for (int k = threadIdx.x * 8; k < a.Dp; k += 256 * 8)
+      *reinterpret_cast<bf16x8*>(a.hz + static_cast<size_t>(at) * a.Dp + k) = zero_frag();
+  }
+  if (threadIdx.x != 0) return;
+  RowTerm t = {0.0f, 0.0f, 0.0f, 0.0f};
+  int loc = -1;
+  if (b < a.B) {
+    const float inv_t = score_inv_t(a.temperature, b);
+    const float g = a.grad[b] * inv_t;
+    t.c = inv_t * 1.44269504088896341f;
+    t.lse2 = a.lse[b] * 1.44269504088896341f;
+    t.coef = -g;
+    loc = target_row(a.ids[b], a.vocab_offset, a.V);
+    t.target = loc >= 0 ? -expm1f(a.logprob[b]) * g : 0.0f;
+  }
+  a.term[at] = t;
+  a.loc[at] = loc;
+}
+
+__device__ __forceinline__ uint64_t pack_bf16(float x0, float x1, float x2, float x3) {
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  const bf16x4 v = {static_cast<__bf16>(x0), static_cast<__bf16>(x1), static_cast<__bf16>(x2),
+                    static_cast<__bf16>(x3)};
+  return __builtin_bit_cast(uint64_t, v);
+}
+
+// dz of one slice: logits of a tile of vocabulary rows by rows with a target,
+// turned into dz in registers.
+template <class T>
+__global__ __launch_bounds__(T::kThreads) __attribute__((amdgpu_waves_per_eu(2)))
+void grad_logits_kernel(GradArgs a) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char dyn_smem[];
+  const int n = *a.count;
+  int tile, btile;
+  if (!xcd_tile(blockIdx.x, (a.nv + T::TA - 1) / T::TA, (n + T::TB - 1) / T::TB, tile, btile))
+    return;
+  const int a0 = tile * T::TA, b0 = btile * T::TB;
+  const Operand w = {a.W + static_cast<size_t>(a.v0) * a.D, a.D, a.nv, a.D};
+  const Operand h = {a.hz, a.Dp, a.Bp, a.Dp};
+  f32x4 acc[T::MR][T::NT];
+  T::run(w, h, a0, b0, 0, a.Dp / T::BK, acc, dyn_smem);
+  const int lane = threadIdx.x & (kWave - 1), li = lane & 15, kb = lane >> 4;
+  const int row0 = a0 + T::wave_a() + 4 * kb;  // in the slice
+  const bool whole = a0 + T::TA <= a.nv;
+  static_for<T::NT>([&](auto nc) FS_INLINE {
+    const int b = b0 + T::wave_b() + 16 * static_cast<int>(nc) + li;
+    const RowTerm t = a.term[b];
+    const int loc = a.loc[b] - a.v0;
+    __bf16* out = a.dz + static_cast<size_t>(b) * a.ldz + row0;
+    static_for<T::MR>([&](auto m) FS_INLINE {
+      const f32x4 z = acc[m][nc];
+      float d[4];
+      static_for<4>([&](auto rc) FS_INLINE {
+        constexpr int r = decltype(rc)::value;
+        const int v = row0 + 16 * static_cast<int>(m) + r;
+        d[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[r], t.c, -t.lse2)) * t.coef;
+        d[r] = v == loc ? t.target : d[r];
+        if (!whole) d[r] = v < a.nv ? d[r] : 0.0f;
+      });
+      *reinterpret_cast<uint64_t*>(out + 16 * static_cast<int>(m)) =
+          pack_bf16(d[0], d[1], d[2], d[3]);
+    });
+  });
+}
+
+// dW of one slice: rows v of W, columns d, summed over the rows with a target.
+template <class T>
+__global__ __launch_bounds__(T::kThreads) __attribute__((amdgpu_waves_per_eu(2)))
+void grad_weights_kernel(GradArgs a) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char dyn_smem[];
+  const int n = *a.count;
+  int tile, dtile;
+  if (!xcd_tile(blockIdx.x, (a.nv + T::TB - 1) / T::TB, (a.D + T::TA - 1) / T::TA, tile, dtile))
+    return;
+  const int a0 = dtile * T::TA, b0 = tile * T::TB;
+  const Operand h = {a.hz, a.Dp, a.D, a.Bp};
+  const Operand z = {a.dz, a.ldz, a.ldz, a.Bp};
+  f32x4 acc[T::MR][T::NT];
+  if (n > 0) T::run(h, z, a0, b0, 0, (n + T::BK - 1) / T::BK, acc, dyn_smem);
+  else zero_acc(acc);
+  const int lane = threadIdx.x & (kWave - 1), li = lane & 15, kb = lane >> 4;
+  const int d0 = a0 + T::wave_a() + 4 * kb;
+  static_for<T::NT>([&](auto nc) FS_INLINE {
+    const int v = b0 + T::wave_b() + 16 * static_cast<int>(nc) + li;
+    __bf16* out = a.dW + (static_cast<size_t>(a.v0) + v) * a.D + d0;
+    static_for<T::MR>([&](auto m) FS_INLINE {
+      const f32x4 x = acc[m][nc];
+      if (v < a.nv && d0 + 16 * static_cast<int>(m) < a.D)
+        *reinterpret_cast<uint64_t*>(out + 16 * static_cast<int>(m)) =
+            pack_bf16(x[0], x[1], x[2], x[3]);
+    });
+  });
+}
+
+// dh of one slice and one part of its vocabulary rows: straight to dh where
+// that is all there is, else into the part's slab (added up from slice to
+// slice in fp32).
+template <class T>
+__global__ __launch_bounds__(T::kThreads) __attribute__((amdgpu_waves_per_eu(2)))
+void grad_hidden_kernel(GradArgs a) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char dyn_smem[];
+  const int n = *a.count;
+  const int nb = (n + T::TB - 1) / T::TB, nd = (a.D + T::TA - 1) / T::TA;
+  int btile, at;
+  if (!xcd_tile(blockIdx.x, nb, static_cast<int64_t>(nd) * a.splits, btile, at)) return;
+  const int dtile = at % nd, split = at / nd;
+  const int a0 = dtile * T::TA, b0 = btile * T::TB;
+  const Operand w = {a.W + static_cast<size_t>(a.v0) * a.D, a.D, a.D, a.nv};
+  const Operand z = {a.dz, a.ldz, a.Bp, a.ldz};
+  const int64_t nk = (a.nv + T::BK - 1) / T::BK;
+  const int kt0 = static_cast<int>(nk * split / a.splits);
+  const int kt1 = static_cast<int>(nk * (split + 1) / a.splits);
+  f32x4 acc[T::MR][T::NT];
+  if (kt0 < kt1) T::run(w, z, a0, b0, kt0, kt1, acc, dyn_smem);
+  else zero_acc(acc);
+  const int lane = threadIdx.x & (kWave - 1), li = lane & 15, kb = lane >> 4;
+  const int d0 = a0 + T::wave_a() + 4 * kb;
+  static_for<T::NT>([&](auto nc) FS_INLINE {
+    const int b = b0 + T::wave_b() + 16 * static_cast<int>(nc) + li;
+    if (b < n) {
+      float* slab = a.slab + (static_cast<size_t>(split) * a.Bp + b) * a.D + d0;
+      __bf16* out = a.dh + static_cast<size_t>(a.slab ? 0 : a.row[b]) * a.D + d0;
+      static_for<T::MR>([&](auto m) FS_INLINE {
+        f32x4 x = acc[m][nc];
+        if (d0 + 16 * static_cast<int>(m) < a.D) {
+          if (a.slab != nullptr) {
+            f32x4* p = reinterpret_cast<f32x4*>(slab + 16 * static_cast<int>(m));
+            if (!a.first_slice) x += *p;
+            *p = x;
+          } else {
+            *reinterpret_cast<uint64_t*>(out + 16 * static_cast<int>(m)) =
+                pack_bf16(x[0], x[1], x[2], x[3]);
+          }
+        }
+      });
+    }
+  });
+}
+
+// The slabs of each row, added in order and rounded once.
+__global__ __launch_bounds__(256) void grad_slabs_kernel(GradArgs a) {
+  const int b = blockIdx.x;
+  if (b >= *a.count) return;
+  __bf16* out = a.dh + static_cast<size_t>(a.row[b]) * a.D;
+  for (int d = threadIdx.x * 4; d < a.D; d += 256 * 4) {
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < a.splits; ++s)
+      x += *reinterpret_cast<const f32x4*>(a.slab + (static_cast<size_t>(s) * a.Bp + b) * a.D + d);
+    *reinterpret_cast<uint64_t*>(out + d) = pack_bf16(x[0], x[1], x[2], x[3]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+constexpr int32_t kMaxGradB = 1 << 22;
+constexpr int32_t kMaxGradD = 1 << 20;
+// dz of one slice of the vocabulary.
+constexpr int64_t kSliceBytes = int64_t{1} << 30;
+constexpr int32_t kMaxSlice = 1 << 18;
+
+struct GradPlan {
+  int32_t Bp, Dp, slice, splits, TB;
+  bool slabs;
+  size_t count, slot, row, loc, term, hz, dz, slab, total;
+  GradPlan(int32_t B, int32_t D, int32_t V) {
+    TB = B <= 64 ? 64 : B <= 128 ? 128 : 256;
+    Bp = static_cast<int32_t>(round_up(B, 256));
+    Dp = static_cast<int32_t>(round_up(D, 64));
+    int64_t s = kSliceBytes / (2 * static_cast<int64_t>(Bp)) / 256 * 256;
+    s = s < 256 ? 256 : s > kMaxSlice ? kMaxSlice : s;
+    const int64_t whole = static_cast<int64_t>(round_up(V, 256));
+    if (s >= whole) {
+      s = whole;
+    } else {  // equal slices
+      const int64_t k = (whole + s - 1) / s;
+      s = static_cast<int64_t>(round_up((whole + k - 1) / k, 256));
+    }
+    slice = static_cast<int32_t>(s);
+    // Parts of the vocabulary for dh: its tiles alone are few, and rows without
+    // a target leave some of them empty, so that whole rounds of tiles would
+    // leave CUs idle; parts of at least 1024 vocabulary rows
+    const int64_t tiles = static_cast<int64_t>((B + TB - 1) / TB) * ((D + 255) / 256);
+    int64_t p = (1024 + tiles - 1) / tiles;
+    const int64_t most = (slice < V ? slice : V) / 1024;
+    p = p > most ? most : p;
+    splits = static_cast<int32_t>(p < 1 ? 1 : p);
+    slabs = splits > 1 || slice < V;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+      const size_t o = at;
+      at += round_up(bytes, 256);
+      return o;
+    };
+    count = take(4);
+    slot = take(4ull * B);
+    row = take(4ull * Bp);
+    loc = take(4ull * Bp);
+    term = take(sizeof(RowTerm) * Bp);
+    hz = take(2ull * Bp * Dp);
+    dz = take(2ull * Bp * slice);
+    slab = take(slabs ? 4ull * splits * Bp * D : 0);
+    total = at;
+  }
+};
+
+unsigned padded_grid(int64_t tiles) { return static_cast<unsigned>((tiles + 7) / 8 * 8); }
+
+template <int TB>
+struct Shapes;  // 8 waves over 256 x TB
+template <>
+struct Shapes<256> {
+  template <int LA, int LB> using tile = Tile<LA, LB, 2, 4, 8, 4, 2>;
+};
+template <>
+struct Shapes<128> {
+  template <int LA, int LB> using tile = Tile<LA, LB, 4, 2, 4, 4, 3>;
+};
+template <>
+struct Shapes<64> {
+  template <int LA, int LB> using tile = Tile<LA, LB, 8, 1, 2, 4, 4>;
+};
+
+template <class Kernel>
+hipError_t launch_tiles(Kernel kernel, const hipError_t& attr, int64_t tiles, int threads,
+                        size_t smem, const GradArgs& a, hipStream_t stream) {
+  if (attr != hipSuccess) return attr;
+  kernel<<<padded_grid(tiles), threads, smem, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <int TB>
+hipError_t launch_logits(const GradArgs& a, hipStream_t stream) {
+  using T = typename Shapes<TB>::template tile<kKC, kKC>;
+  static const hipError_t attr = allow_smem(&grad_logits_kernel<T>, T::kSmemBytes);
+  return launch_tiles(&grad_logits_kernel<T>, attr,
+                      static_cast<int64_t>((a.nv + T::TA - 1) / T::TA) * ((a.B + TB - 1) / TB),
+                      T::kThreads, T::kSmemBytes, a, stream);
+}
+
+template <int TB>
+hipError_t launch_hidden(const GradArgs& a, hipStream_t stream) {
+  using T = typename Shapes<TB>::template tile<kKM, kKC>;
+  static const hipError_t attr = allow_smem(&grad_hidden_kernel<T>, T::kSmemBytes);
+  return launch_tiles(&grad_hidden_kernel<T>, attr,
+                      static_cast<int64_t>((a.B + TB - 1) / TB) * ((a.D + T::TA - 1) / T::TA) *
+                          a.splits,
+                      T::kThreads, T::kSmemBytes, a, stream);
+}
+
+hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
+  using T = Shapes<256>::tile<kKM, kKM>;
+  static const hipError_t attr = allow_smem(&grad_weights_kernel<T>, T::kSmemBytes);
+  return launch_tiles(&grad_weights_kernel<T>, attr,
+                      static_cast<int64_t>((a.nv + T::TB - 1) / T::TB) * ((a.D + T::TA - 1) / T::TA),
+                      T::kThreads, T::kSmemBytes, a, stream);
+}
+
+hipError_t run_grad(GradArgs& a, const GradPlan& p, hipStream_t s) {
+  grad_rows_kernel<<<1, kScanThreads, 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  grad_gather_kernel<<<a.B + 256, 256, 0, s>>>(a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  for (int32_t v0 = 0; v0 < a.V; v0 += p.slice) {
+    a.v0 = v0;
+    a.nv = a.V - v0 < p.slice ? a.V - v0 : p.slice;
+    a.first_slice = v0 == 0;
+    if (a.B > 0)
+      e = p.TB == 64 ? launch_logits<64>(a, s)
+          : p.TB == 128 ? launch_logits<128>(a, s)
+                        : launch_logits<256>(a, s);
+    if (e != hipSuccess) return e;
+    if (a.dW != nullptr && (e = launch_weights(a, s)) != hipSuccess) return e;
+    if (a.dh != nullptr) {
+      e = p.TB == 64 ? launch_hidden<64>(a, s)
+          : p.TB == 128 ? launch_hidden<128>(a, s)
+                        : launch_hidden<256>(a, s);
+      if (e != hipSuccess) return e;
+    }
+    if (a.V - v0 <= p.slice) break;  // (v0 + slice may not fit in 32 bits)
+  }
+  if (a.dh != nullptr && p.slabs) {
+    grad_slabs_kernel<<<a.B, 256, 0, s>>>(a);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+bool grad_sizes_ok(int32_t B, int32_t D, int32_t V) {
+  return B >= 0 && D >= 8 && D % 8 == 0 && V >= 1 && B <= kMaxGradB && D <= kMaxGradD;
+}
+
+}  // namespace
+}  // namespace fs
+
+extern "C" {
+
+FS_API size_t fs_token_logprobs_backward_workspace_bytes(int32_t B, int32_t D, int32_t V) {
+  return fs::grad_sizes_ok(B, D, V) ? fs::GradPlan(B > 0 ? B : 1, D, V).total : 0;
+}
+
+FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_t B, int32_t D,
+                                            int32_t V, int32_t vocab_offset,
+                                            const float* temperature, const int32_t* token_ids,
+                                            const float* logprob, const float* lse,
+                                            const float* grad_logprob, void* grad_h, void* grad_W,
+                                            void* workspace, size_t workspace_bytes,
+                                            void* stream) {
+  using namespace fs;
+  const char* who = "fs_token_logprobs_backward";
+  if (B < 0) return fail(FS_ERR_INVALID_ARG, "%s: B must be >= 0 (got %d)", who, B);
+  if (D < 8 || D % 8 != 0)
+    return fail(FS_ERR_INVALID_ARG, "%s: D must be a positive multiple of 8 (got %d)", who, D);
+  if (V < 1) return fail(FS_ERR_INVALID_ARG, "%s: V must be >= 1 (got %d)", who, V);
+  if (vocab_offset < 0 || static_cast<int64_t>(vocab_offset) + V > 2147483647)
+    return fail(FS_ERR_INVALID_ARG, "%s: vocab_offset and vocab_offset + V must be in [0, 2^31 - 1]"
+                " (got %d, V = %d)", who, vocab_offset, V);
+  if (!grad_sizes_ok(B, D, V))
+    return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, D=%d exceed the %d rows or %d elements a call can "
+                "take", who, B, D, kMaxGradB, kMaxGradD);
+  if (!grad_h && !grad_W)
+    return fail(FS_ERR_INVALID_ARG, "%s: neither grad_h nor grad_W is asked for", who);
+  if (!grad_W && B == 0) return FS_OK;
+  if (!W || (B > 0 && (!h || !token_ids || !logprob || !lse || !grad_logprob)) || !workspace)
+    return fail(FS_ERR_INVALID_ARG, "%s: null pointer argument", who);
+  if (!aligned(h, 16) || !aligned(W, 16) || !aligned(grad_h, 16) || !aligned(grad_W, 16))
+    return fail(FS_ERR_INVALID_ARG, "%s: h, W and their gradients must be 16-byte aligned", who);
+  if (!aligned(token_ids, 4) || !aligned(logprob, 4) || !aligned(lse, 4) ||
+      !aligned(grad_logprob, 4) || !aligned(temperature, 4))
+    return fail(FS_ERR_INVALID_ARG, "%s: per-row arrays must be 4-byte aligned", who);
+  if (!aligned(workspace, 256))
+    return fail(FS_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
+  const GradPlan p(B > 0 ? B : 1, D, V);
+  if (workspace_bytes < p.total)
+    return fail(FS_ERR_WORKSPACE, "%s: workspace of %zu bytes is below the %zu required", who,
+                workspace_bytes, p.total);
+  const int64_t most_tiles = (static_cast<int64_t>(p.slice) / 256 + 1) *
+                             ((B + 63) / 64 > (D + 255) / 256 ? (B + 63) / 64 : (D + 255) / 256);
+  if (most_tiles > 0x7FFFFFFF - 8)
+    return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, D=%d, V=%d exceed the launch grid", who, B, D, V);
+  if (start_launches()) return injected_failure(who);
+  char* ws = static_cast<char*>(workspace);
+  GradArgs a;
+  a.h = static_cast<const __bf16*>(h);
+  a.W = static_cast<const __bf16*>(W);
+  a.B = B;
+  a.D = D;
+  a.V = V;
+  a.vocab_offset = vocab_offset;
+  a.temperature = temperature;
+  a.logprob = logprob;
+  a.lse = lse;
+  a.grad = grad_logprob;
+  a.ids = token_ids;
+  a.dh = B > 0 ? static_cast<__bf16*>(grad_h) : nullptr;
+  a.dW = static_cast<__bf16*>(grad_W);
+  a.count = reinterpret_cast<int32_t*>(ws + p.count);
+  a.slot = reinterpret_cast<int32_t*>(ws + p.slot);
+  a.row = reinterpret_cast<int32_t*>(ws + p.row);
+  a.loc = reinterpret_cast<int32_t*>(ws + p.loc);
+  a.term = reinterpret_cast<RowTerm*>(ws + p.term);
+  a.hz = reinterpret_cast<__bf16*>(ws + p.hz);
+  a.dz = reinterpret_cast<__bf16*>(ws + p.dz);
+  a.slab = p.slabs ? reinterpret_cast<float*>(ws + p.slab) : nullptr;
+  a.Dp = p.Dp;
+  a.Bp = p.Bp;
+  a.ldz = p.slice;
+  a.v0 = a.nv = 0;
+  a.splits = p.splits;
+  a.first_slice = 1;
+  const hipError_t e = run_grad(a, p, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? FS_OK : hip_fail(e, "log-probability gradient launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,103 @@
+// fs_score.hpp -- shared parts of the token log-probability operators: the
+// epilogue that turns a block's logits into one log-sum-exp partial per
+// token, and the arguments of its kernels.
+//
+// Scaled logits t_v = z_v * fp32(1/T) (rows whose T is not positive: t = z).
+// A token's partial over a block of vocabulary rows is the pair (m, s) with
+// sum exp(t_v) = s exp(m) over the rows that are not its target; the target's
+// own t goes to a separate array.  With L the log-sum-exp of the others,
+//   log p(target) = -log(1 + exp(L - t_target)),
+// which keeps its relative accuracy where the target is nearly certain;
+// t_target - logsumexp(all) would cancel there.
+#pragma once
+
+#include "fs_tile.hpp"
+
+namespace fs {
+
+struct ScoreArgs {
+  Operand w, h;             // W [V][D] (or fragment order), h [B][D]
+  int32_t B, D, V, vocab_offset, shift;  // shift: rows before row 0 in the grid (fragment order)
+  const float* temperature;  // [B] or null (all 1)
+  const int32_t* ids;        // [B]
+  float2* part;              // [S][B]
+  float* target;             // [B]: the target's scaled logit
+  int32_t S;
+};
+
+__device__ __forceinline__ float score_inv_t(const float* temperature, int b) {
+  return temperature != nullptr ? row_inv_temperature(temperature[b]) : 1.0f;
+}
+
+// The target's local vocabulary row, or -1 (no target, or another shard's).
+__device__ __forceinline__ int target_row(int32_t id, int32_t vocab_offset, int32_t V) {
+  if (id < vocab_offset) return -1;  // (vocab_offset >= 0, so negative ids too)
+  const int loc = id - vocab_offset;
+  return loc < V ? loc : -1;
+}
+
+// (m, s) of the union of two disjoint sets of rows.  m is -FLT_MAX where s is 0.
+__device__ __forceinline__ void pair_merge(float& m, float& s, float om, float os) {
+  const float nm = fmaxf(m, om);
+  s = s * LseAcc::ex(m - nm) + os * LseAcc::ex(om - nm);
+  m = nm;
+}
+__device__ __forceinline__ void pair_xor(float& m, float& s, int mask) {
+  const float om = __shfl_xor(m, mask, kWave), os = __shfl_xor(s, mask, kWave);
+  pair_merge(m, s, om, os);
+}
+
+// Folds the wave's logits of one token into (m, s): z[i][r] is vocabulary row
+// row0 + 16 i + r + 4 kb.  All values are in registers, so the maximum comes
+// first and each logit costs one multiply-add and one exp2.  `plain` (the
+// same on all lanes): no row of the wave is outside [0, V) or any of its
+// tokens' target, so nothing is excluded.
+template <int MR, class Z>
+__device__ __forceinline__ void fold_logits(const Z& z, int row0, int32_t V, int loc, bool plain,
+                                            float inv_t, float& m, float& s, float& zt,
+                                            bool& has_zt) {
+  const int kb = (threadIdx.x & (kWave - 1)) >> 4;
+  const float c = inv_t * 1.44269504088896341f;  // log2(e) / T
+  float mz = LseAcc::kMasked, sum = 0.0f;
+  if (plain) {
+    static_for<MR>([&](auto i) FS_INLINE {
+      const f32x4 x = z(i);
+      mz = fmaxf(fmaxf(mz, fmaxf(x[0], x[1])), fmaxf(x[2], x[3]));
+    });
+    const float off = mz * c;
+    static_for<MR>([&](auto i) FS_INLINE {
+      const f32x4 x = z(i);
+      static_for<4>([&](auto r) FS_INLINE {
+        sum += __builtin_amdgcn_exp2f(__builtin_fmaf(x[decltype(r)::value], c, -off));
+      });
+    });
+  } else {
+    auto keep = [&](int v) FS_INLINE {
+      return static_cast<uint32_t>(v) < static_cast<uint32_t>(V) && v != loc;
+    };
+    static_for<MR>([&](auto i) FS_INLINE {
+      const f32x4 x = z(i);
+      static_for<4>([&](auto r) FS_INLINE {
+        const int v = row0 + 16 * static_cast<int>(i) + 4 * kb + static_cast<int>(r);
+        if (v == loc && loc >= 0) {
+          zt = x[decltype(r)::value] * inv_t;
+          has_zt = true;
+        }
+        mz = keep(v) ? fmaxf(mz, x[decltype(r)::value]) : mz;
+      });
+    });
+    const float off = mz * c;
+    static_for<MR>([&](auto i) FS_INLINE {
+      const f32x4 x = z(i);
+      static_for<4>([&](auto r) FS_INLINE {
+        const int v = row0 + 16 * static_cast<int>(i) + 4 * kb + static_cast<int>(r);
+        // the exponential of an excluded row may be anything: not added
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[decltype(r)::value], c, -off));
+        sum += keep(v) ? e : 0.0f;
+      });
+    });
+  }
+  pair_merge(m, s, mz == LseAcc::kMasked ? mz : mz * inv_t, sum);
+}
+
+}  // namespace fs

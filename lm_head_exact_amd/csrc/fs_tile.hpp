@@ -1,0 +1,245 @@
+// fs_tile.hpp -- the block-tiled bf16 matrix product of the training operators
+// on gfx950: C[b][a] = sum_k A(a, k) B(b, k), fp32 accumulators.
+//
+// One block of 8 waves (two per SIMD, one block per CU) computes TA x TB
+// elements of C; wave w holds MR x NT tiles of 16 x 16
+// (v_mfma_f32_16x16x32_bf16, A as the MFMA's rows).  Both operands go through
+// LDS, staged by direct global->LDS loads in a ring of S slots of 64 k.  An
+// operand is either
+//   K-contiguous (KC)  element (i, k) at p[i * pitch + k]: 16-byte pieces
+//                      along k, read back as they are (ds_read_b128);
+//   K-major (KM)       element (i, k) at p[k * pitch + i]: 16-byte pieces
+//                      along i; the transposing LDS read
+//                      (ds_read_b64_tr_b16) hands every lane its k's, so no
+//                      operand is ever transposed in memory.
+//   fragment order     W as fs_pack_weights stores it (groups of 16 rows, one
+//                      contiguous KB per group and 32 k): staged and read as
+//                      it is (ds_read_b128, lanes in order).
+// The three products of the LM head are (KC or fragment order, KC) for logits,
+// (KM, KC) for the gradient of the hidden states and (KM, KM) for the gradient
+// of W.
+//
+// LDS layouts.  KC: rows of 64 k (128 bytes, 8 pieces), piece j of row i at
+// slot j ^ (i mod 8).  KM: rows of one k (T elements), the 32-byte unit u of
+// row k at unit u ^ g(k), g(k) = (k mod 4) + 4 (k / 8 mod 2): a transposing
+// read takes from each of its four 16-lane groups four rows of one unit; g
+// spreads the eight rows of 32 lanes over the eight 32-byte bank groups.  The
+// direct loads write LDS in lane order, so the permutation is applied to the
+// addresses they read.
+//
+// Bounds.  Rows, k's and columns past an operand's end are read at its last
+// one: no access leaves the operand.  What they contribute is masked by the
+// epilogue (rows of A and B) or multiplied by the other operand's zeros (k).
+#pragma once
+
+#include "fs_mma.hpp"
+
+namespace fs {
+
+enum Layout { kKC = 0, kKM = 1, kFrag = 2 };
+
+struct Operand {
+  const __bf16* p;
+  int64_t pitch;  // elements: between rows (KC), between k's (KM), between groups (fragment order)
+  int32_t n;      // rows (KM: a multiple of 8); fragment order: groups of 16 rows
+  int32_t k;      // k's; KC: a multiple of 8; fragment order: a multiple of 32
+};
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <int LA_, int LB_, int WA_, int WB_, int MR_, int NT_, int S_>
+struct Tile {
+  static constexpr int LA = LA_, LB = LB_;
+  static_assert(LB != kFrag, "W is operand A");
+  static constexpr int WA = WA_, WB = WB_, MR = MR_, NT = NT_, S = S_;
+  static constexpr int NW = WA * WB;
+  static constexpr int kThreads = NW * kWave;
+  static constexpr int TA = WA * MR * 16, TB = WB * NT * 16;
+  static constexpr int BK = 64;
+  static constexpr int kStageA = TA * BK * 2, kStageB = TB * BK * 2;  // bytes
+  static constexpr int kStage = kStageA + kStageB;
+  static constexpr size_t kSmemBytes = static_cast<size_t>(S) * kStage;
+  static constexpr int IA = kStageA / (NW * 1024), IB = kStageB / (NW * 1024);
+  static_assert(kStageA % (NW * 1024) == 0 && kStageB % (NW * 1024) == 0, "staging divides evenly");
+  static_assert((LA != kKM || TA % 128 == 0) && (LB != kKM || TB % 128 == 0), "KM swizzle needs 8 units a row");
+  static_assert(kSmemBytes <= 160 * 1024, "LDS");
+  static constexpr int kBufferFlags = 0x00020000;
+
+  __device__ __forceinline__ static int wave() {
+    return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  }
+  // First row of A and of B that this wave's accumulators cover, in the tile.
+  __device__ __forceinline__ static int wave_a() { return (wave() / WB) * MR * 16; }
+  __device__ __forceinline__ static int wave_b() { return (wave() % WB) * NT * 16; }
+
+  template <int N>
+  __device__ __forceinline__ static void wait_vm() {
+    static_assert(N >= 0 && N <= 63, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+  }
+  // Workgroup barrier without the fence of __syncthreads (which would wait
+  // for every load in flight); the callers wait for what they need.
+  __device__ __forceinline__ static void barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // The permutation of 32-byte units in a KM row.
+  __device__ __forceinline__ static int km_swizzle(int k) { return (k & 3) | ((k >> 1) & 4); }
+
+  // Byte offsets, from the operand tile's first element, of the pieces this
+  // lane stages (without the k step's part), and the k of the piece (KC).
+  template <int L, int T, int I>
+  struct Stager {
+    int off[I];
+    int kk[I];  // k of the piece in the tile
+    __device__ __forceinline__ void init(const Operand& o, int i0) {
+      const int lane = threadIdx.x & (kWave - 1);
+      static_for<I>([&](auto i) FS_INLINE {
+        const int q = (wave() * I + static_cast<int>(i)) * kWave + lane;  // 16-byte slot
+        if constexpr (L == kKM) {
+          constexpr int P = T / 8;  // pieces per row
+          const int k = q / P, slot = q % P;
+          const int piece = slot ^ (km_swizzle(k) << 1);
+          off[i] = min(piece * 8, o.n - 8 - i0) * 2;
+          kk[i] = k;
+        } else if constexpr (L == kFrag) {  // piece (group, k step of the tile), 1 KB each
+          const int piece = q / kWave;
+          off[i] = static_cast<int>(min(piece / 2, o.n - 1 - i0 / 16) * o.pitch) * 2 + lane * 16;
+          kk[i] = (piece % 2) * 32;
+        } else {
+          const int r = q / 8, piece = (q % 8) ^ (r & 7);
+          off[i] = static_cast<int>(min(r, o.n - 1 - i0) * o.pitch) * 2;
+          kk[i] = piece * 8;
+        }
+      });
+    }
+    // Tile kt of the operand whose row i0 starts at `base` (start(o, i0)), into
+    // LDS at `dst`.
+    __device__ __forceinline__ static const __bf16* start(const Operand& o, int i0) {
+      return o.p + (L == kKM ? static_cast<int64_t>(i0)
+                             : (L == kFrag ? i0 / 16 : i0) * o.pitch);
+    }
+    __device__ __forceinline__ void stage(const Operand& o, const __bf16* base, int kt,
+                                          unsigned char* dst) const {
+      if constexpr (L == kKM) {
+        const __bf16* b = base + static_cast<int64_t>(kt) * BK * o.pitch;
+        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<__bf16*>(b), 0, 0x7FFFFFFF, kBufferFlags);
+        const int kend = o.k - 1 - kt * BK;
+        static_for<I>([&](auto i) FS_INLINE {
+          const int k = min(kk[i], kend);
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+              rsrc, lds(dst + (wave() * I + static_cast<int>(i)) * 1024), 16,
+              off[i] + k * static_cast<int>(o.pitch * 2), 0, 0, 0);
+        });
+      } else {
+        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<__bf16*>(base), 0, 0x7FFFFFFF, kBufferFlags);
+        // KC: element k of a row; fragment order: k step k / 32 of a group, 512 elements each
+        const int kend = o.k - (L == kFrag ? 32 : 8);
+        static_for<I>([&](auto i) FS_INLINE {
+          const int k = min(kt * BK + kk[i], kend) * (L == kFrag ? 32 : 2);
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+              rsrc, lds(dst + (wave() * I + static_cast<int>(i)) * 1024), 16, off[i] + k, 0, 0, 0);
+        });
+      }
+    }
+    __device__ __forceinline__ static __attribute__((address_space(3))) void* lds(unsigned char* p) {
+      return (__attribute__((address_space(3))) void*)p;
+    }
+  };
+
+  // Fragment f (16 rows from f * 16 of the staged tile) of k step s of the
+  // operand at `buf`: lane (li, kb) gets row li, k = 32 s + 8 kb + 0..7.
+  template <int L, int T>
+  __device__ __forceinline__ static bf16x8 frag(const unsigned char* buf, int f, int s) {
+    const int lane = threadIdx.x & (kWave - 1);
+    if constexpr (L == kKM) {
+      const int g = lane >> 4, i = lane & 15;
+      // row k = 32 s + 8 g + 4 half + i / 4: its swizzle does not depend on s or half
+      const int c = (i >> 2) | ((g & 1) << 2);
+      const unsigned char* a =
+          buf + (8 * g + (i >> 2)) * (T * 2) + ((f ^ c) * 32 + (i & 3) * 8) + s * 32 * (T * 2);
+      const s16x4 lo = tr(a), hi = tr(a + 4 * (T * 2));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else if constexpr (L == kFrag) {
+      return __builtin_bit_cast(
+          bf16x8, *reinterpret_cast<const u32x4*>(buf + (f * 2 + s) * 1024 + lane * 16));
+    } else {
+      const int li = lane & 15, kb = lane >> 4;
+      const unsigned char* a = buf + (f * 16 + li) * 128 + (((s * 4 + kb) ^ (li & 7)) * 16);
+      return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(a));
+    }
+  }
+  __device__ __forceinline__ static s16x4 tr(const unsigned char* a) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4*)(const_cast<unsigned char*>(a)));
+  }
+
+  // acc[m][n] of C rows b0 + wave_b() + 16 n + li, columns a0 + wave_a() + 16 m
+  // + 4 kb + 0..3, over k tiles [kt0, kt1).  LDS is free for reuse (after a
+  // barrier) when it returns.
+  __device__ __forceinline__ static void run(const Operand& A, const Operand& B, int a0, int b0,
+                                             int kt0, int kt1, f32x4 (&acc)[MR][NT],
+                                             unsigned char* smem) {
+    zero_acc(acc);
+    Stager<LA, TA, IA> sa;
+    Stager<LB, TB, IB> sb;
+    sa.init(A, a0);
+    sb.init(B, b0);
+    const __bf16* pa = sa.start(A, a0);
+    const __bf16* pb = sb.start(B, b0);
+    auto stage = [&](int kt, int slot) FS_INLINE {
+      unsigned char* dst = smem + slot * kStage;
+      sa.stage(A, pa, kt, dst);
+      sb.stage(B, pb, kt, dst + kStageA);
+    };
+    static_for<S - 1>([&](auto i) FS_INLINE {
+      stage(min(kt0 + static_cast<int>(i), kt1 - 1), i);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    const int fa = wave_a() / 16, fb = wave_b() / 16;
+    int slot = 0;
+    for (int kt = kt0; kt < kt1; ++kt) {
+      wait_vm<(S - 2) * (IA + IB)>();  // this wave's share of tile kt has landed
+      barrier();                       // ... every wave's; the slot of tile kt - 1 is free
+      stage(min(kt + S - 1, kt1 - 1), slot == 0 ? S - 1 : slot - 1);
+      __builtin_amdgcn_sched_barrier(0);
+      const unsigned char* la = smem + slot * kStage;
+      const unsigned char* lb = la + kStageA;
+      static_for<BK / 32>([&](auto s) FS_INLINE {
+        bf16x8 a[MR], b[NT];
+        static_for<NT>([&](auto n) FS_INLINE { b[n] = frag<LB, TB>(lb, fb + n, s); });
+        static_for<MR>([&](auto m) FS_INLINE { a[m] = frag<LA, TA>(la, fa + m, s); });
+        mma_step(a, b, acc);
+      });
+      slot = slot == S - 1 ? 0 : slot + 1;
+    }
+    wait_vm<0>();  // the trailing (clamped) loads land before LDS is reused
+    barrier();
+  }
+};
+
+// Tile (slow, fast) of block `id` in a grid of at least nslow * nfast blocks;
+// false for the blocks beyond.  Blocks are dealt to the 8 XCDs round robin:
+// block id runs on XCD id mod 8, which takes one contiguous eighth of the
+// tiles in an order that walks four slow tiles by all fast ones, so that the
+// blocks resident on an XCD share their operands' tiles through its L2.
+__device__ __forceinline__ bool xcd_tile(int64_t id, int64_t nslow, int64_t nfast, int& slow,
+                                         int& fast) {
+  const int64_t total = nslow * nfast, per = (total + 7) / 8;
+  const int64_t at = id / 8;
+  const int64_t l = (id % 8) * per + at;
+  if (at >= per || l >= total) return false;
+  const int64_t g = l / (4 * nfast), w = l % (4 * nfast);
+  const int64_t rows = nslow - 4 * g < 4 ? nslow - 4 * g : 4;
+  slow = static_cast<int>(4 * g + w % rows);
+  fast = static_cast<int>(w / rows);
+  return true;
+}
+
+}  // namespace fs
