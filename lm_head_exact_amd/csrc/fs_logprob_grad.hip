@@ -316,11 +316,16 @@ struct GradPlan {
 
 unsigned padded_grid(int64_t tiles) { return static_cast<unsigned>((tiles + 7) / 8 * 8); }
 
+// 8 waves over 256 x TB.  K-major operands take ring slots of 32 k, four or
+// five deep (their rows are as long in memory as in slots of 64); K-contiguous
+// ones slots of 64, a whole 128-byte line per row.
 template <int TB>
-struct Shapes;  // 8 waves over 256 x TB
+struct Shapes;
 template <>
 struct Shapes<256> {
-  template <int LA, int LB> using tile = Tile<LA, LB, 2, 4, 8, 4, 2>;
+  template <int LA, int LB> using tile =
+      std::conditional_t<LA == kKM, Tile<LA, LB, 2, 4, 8, 4, LB == kKM ? 5 : 4, 32>,
+                         Tile<LA, LB, 2, 4, 8, 4, 2>>;
 };
 template <>
 struct Shapes<128> {

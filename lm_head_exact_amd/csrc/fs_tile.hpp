@@ -47,7 +47,7 @@ struct Operand {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-template <int LA_, int LB_, int WA_, int WB_, int MR_, int NT_, int S_>
+template <int LA_, int LB_, int WA_, int WB_, int MR_, int NT_, int S_, int BK_ = 64>
 struct Tile {
   static constexpr int LA = LA_, LB = LB_;
   static_assert(LB != kFrag, "W is operand A");
@@ -55,7 +55,8 @@ struct Tile {
   static constexpr int NW = WA * WB;
   static constexpr int kThreads = NW * kWave;
   static constexpr int TA = WA * MR * 16, TB = WB * NT * 16;
-  static constexpr int BK = 64;
+  static constexpr int BK = BK_;  // k's of a ring slot: 64 or 32
+  static constexpr int KS = BK / 32;
   static constexpr int kStageA = TA * BK * 2, kStageB = TB * BK * 2;  // bytes
   static constexpr int kStage = kStageA + kStageB;
   static constexpr size_t kSmemBytes = static_cast<size_t>(S) * kStage;
@@ -87,69 +88,57 @@ struct Tile {
     __builtin_amdgcn_sched_barrier(0);
   }
 
+  // The permutation of 16-byte pieces in a KC row.
+  __device__ __forceinline__ static int kc_swizzle(int r) {
+    return BK == 64 ? r & 7 : (r >> 1) & 3;
+  }
   // The permutation of 32-byte units in a KM row.
   __device__ __forceinline__ static int km_swizzle(int k) { return (k & 3) | ((k >> 1) & 4); }
 
-  // Byte offsets, from the operand tile's first element, of the pieces this
-  // lane stages (without the k step's part), and the k of the piece (KC).
+  // Staging of one operand: byte offsets, from the first element of a k tile of
+  // the operand's rows i0 .., of the pieces this lane loads.  They are the same
+  // for every k tile (the tile's start is in scalar registers) but the last,
+  // ragged one, whose pieces past the end move to the last piece.
   template <int L, int T, int I>
   struct Stager {
+    const __bf16* base;  // rows i0 .. at k = 0
+    int64_t step;        // elements from one k tile to the next
     int off[I];
-    int kk[I];  // k of the piece in the tile
     __device__ __forceinline__ void init(const Operand& o, int i0) {
+      base = o.p + (L == kKM ? static_cast<int64_t>(i0) : (L == kFrag ? i0 / 16 : i0) * o.pitch);
+      step = L == kKM ? BK * o.pitch : L == kFrag ? BK * 16 : BK;
+      offsets(o, i0, BK);
+    }
+    // Offsets for a k tile of `ks` k's.
+    __device__ __forceinline__ void offsets(const Operand& o, int i0, int ks) {
       const int lane = threadIdx.x & (kWave - 1);
       static_for<I>([&](auto i) FS_INLINE {
         const int q = (wave() * I + static_cast<int>(i)) * kWave + lane;  // 16-byte slot
         if constexpr (L == kKM) {
-          constexpr int P = T / 8;  // pieces per row
-          const int k = q / P, slot = q % P;
-          const int piece = slot ^ (km_swizzle(k) << 1);
-          off[i] = min(piece * 8, o.n - 8 - i0) * 2;
-          kk[i] = k;
-        } else if constexpr (L == kFrag) {  // piece (group, k step of the tile), 1 KB each
+          constexpr int P = T / 8;  // pieces per row of one k
+          const int k = q / P, piece = (q % P) ^ (km_swizzle(k) << 1);
+          off[i] = min(piece * 8, o.n - 8 - i0) * 2 + min(k, ks - 1) * static_cast<int>(o.pitch * 2);
+        } else if constexpr (L == kFrag) {  // pieces (group, k step of the tile) of 1 KB
           const int piece = q / kWave;
-          off[i] = static_cast<int>(min(piece / 2, o.n - 1 - i0 / 16) * o.pitch) * 2 + lane * 16;
-          kk[i] = (piece % 2) * 32;
+          off[i] = static_cast<int>(min(piece / KS, o.n - 1 - i0 / 16) * o.pitch) * 2 + lane * 16 +
+                   (ks > 32 ? (piece % KS) * 1024 : 0);
         } else {
-          const int r = q / 8, piece = (q % 8) ^ (r & 7);
-          off[i] = static_cast<int>(min(r, o.n - 1 - i0) * o.pitch) * 2;
-          kk[i] = piece * 8;
+          constexpr int P = BK / 8;  // pieces per row
+          const int r = q / P, piece = (q % P) ^ kc_swizzle(r);
+          off[i] = (static_cast<int>(min(r, o.n - 1 - i0) * o.pitch) + min(piece * 8, ks - 8)) * 2;
         }
       });
     }
-    // Tile kt of the operand whose row i0 starts at `base` (start(o, i0)), into
-    // LDS at `dst`.
-    __device__ __forceinline__ static const __bf16* start(const Operand& o, int i0) {
-      return o.p + (L == kKM ? static_cast<int64_t>(i0)
-                             : (L == kFrag ? i0 / 16 : i0) * o.pitch);
-    }
-    __device__ __forceinline__ void stage(const Operand& o, const __bf16* base, int kt,
-                                          unsigned char* dst) const {
-      if constexpr (L == kKM) {
-        const __bf16* b = base + static_cast<int64_t>(kt) * BK * o.pitch;
-        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<__bf16*>(b), 0, 0x7FFFFFFF, kBufferFlags);
-        const int kend = o.k - 1 - kt * BK;
-        static_for<I>([&](auto i) FS_INLINE {
-          const int k = min(kk[i], kend);
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(
-              rsrc, lds(dst + (wave() * I + static_cast<int>(i)) * 1024), 16,
-              off[i] + k * static_cast<int>(o.pitch * 2), 0, 0, 0);
-        });
-      } else {
-        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<__bf16*>(base), 0, 0x7FFFFFFF, kBufferFlags);
-        // KC: element k of a row; fragment order: k step k / 32 of a group, 512 elements each
-        const int kend = o.k - (L == kFrag ? 32 : 8);
-        static_for<I>([&](auto i) FS_INLINE {
-          const int k = min(kt * BK + kk[i], kend) * (L == kFrag ? 32 : 2);
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(
-              rsrc, lds(dst + (wave() * I + static_cast<int>(i)) * 1024), 16, off[i] + k, 0, 0, 0);
-        });
-      }
-    }
-    __device__ __forceinline__ static __attribute__((address_space(3))) void* lds(unsigned char* p) {
-      return (__attribute__((address_space(3))) void*)p;
+    // Tile kt into LDS at `dst`.
+    __device__ __forceinline__ void stage(int kt, unsigned char* dst) const {
+      const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<__bf16*>(base + kt * step), 0, 0x7FFFFFFF, kBufferFlags);
+      static_for<I>([&](auto i) FS_INLINE {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rsrc,
+            (__attribute__((address_space(3))) void*)(dst + (wave() * I + static_cast<int>(i)) * 1024),
+            16, off[i], 0, 0, 0);
+      });
     }
   };
 
@@ -168,10 +157,11 @@ struct Tile {
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     } else if constexpr (L == kFrag) {
       return __builtin_bit_cast(
-          bf16x8, *reinterpret_cast<const u32x4*>(buf + (f * 2 + s) * 1024 + lane * 16));
+          bf16x8, *reinterpret_cast<const u32x4*>(buf + (f * KS + s) * 1024 + lane * 16));
     } else {
       const int li = lane & 15, kb = lane >> 4;
-      const unsigned char* a = buf + (f * 16 + li) * 128 + (((s * 4 + kb) ^ (li & 7)) * 16);
+      const unsigned char* a =
+          buf + (f * 16 + li) * (BK * 2) + (((s * 4 + kb) ^ kc_swizzle(li)) * 16);
       return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(a));
     }
   }
@@ -181,8 +171,15 @@ struct Tile {
   }
 
   // acc[m][n] of C rows b0 + wave_b() + 16 n + li, columns a0 + wave_a() + 16 m
-  // + 4 kb + 0..3, over k tiles [kt0, kt1).  LDS is free for reuse (after a
-  // barrier) when it returns.
+  // + 4 kb + 0..3, over k tiles [kt0, kt1).  LDS is free for reuse when it
+  // returns.
+  //
+  // Every k step's fragments are read from LDS one step ahead, into the other
+  // of two register sets, while the MFMAs of the current step run.  A k tile
+  // has two steps and one barrier, between them: there each wave has read the
+  // whole of the tile (its slot may be refilled) and waited for its share of
+  // the next one (which may then be read).  The direct loads of tile kt + S
+  // go out right behind that barrier and have S - 1 tiles of time to land.
   __device__ __forceinline__ static void run(const Operand& A, const Operand& B, int a0, int b0,
                                              int kt0, int kt1, f32x4 (&acc)[MR][NT],
                                              unsigned char* smem) {
@@ -191,36 +188,100 @@ struct Tile {
     Stager<LB, TB, IB> sb;
     sa.init(A, a0);
     sb.init(B, b0);
-    const __bf16* pa = sa.start(A, a0);
-    const __bf16* pb = sb.start(B, b0);
+    // the first k tile that is not whole for an operand
+    const int raggedA = A.k / BK, raggedB = B.k / BK;
     auto stage = [&](int kt, int slot) FS_INLINE {
       unsigned char* dst = smem + slot * kStage;
-      sa.stage(A, pa, kt, dst);
-      sb.stage(B, pb, kt, dst + kStageA);
+      sa.stage(kt, dst);
+      sb.stage(kt, dst + kStageA);
     };
-    static_for<S - 1>([&](auto i) FS_INLINE {
-      stage(min(kt0 + static_cast<int>(i), kt1 - 1), i);
+    // k tiles past the last are staged as the last one again (never used)
+    auto prepare = [&](int kt) FS_INLINE {
+      if (kt == raggedA) sa.offsets(A, a0, A.k - kt * BK);
+      if (kt == raggedB) sb.offsets(B, b0, B.k - kt * BK);
+    };
+    static_for<S>([&](auto i) FS_INLINE {
+      const int kt = min(kt0 + static_cast<int>(i), kt1 - 1);
+      prepare(kt);
+      stage(kt, i);
       __builtin_amdgcn_sched_barrier(0);
     });
     const int fa = wave_a() / 16, fb = wave_b() / 16;
-    int slot = 0;
-    for (int kt = kt0; kt < kt1; ++kt) {
-      wait_vm<(S - 2) * (IA + IB)>();  // this wave's share of tile kt has landed
-      barrier();                       // ... every wave's; the slot of tile kt - 1 is free
-      stage(min(kt + S - 1, kt1 - 1), slot == 0 ? S - 1 : slot - 1);
-      __builtin_amdgcn_sched_barrier(0);
-      const unsigned char* la = smem + slot * kStage;
-      const unsigned char* lb = la + kStageA;
-      static_for<BK / 32>([&](auto s) FS_INLINE {
-        bf16x8 a[MR], b[NT];
-        static_for<NT>([&](auto n) FS_INLINE { b[n] = frag<LB, TB>(lb, fb + n, s); });
-        static_for<MR>([&](auto m) FS_INLINE { a[m] = frag<LA, TA>(la, fa + m, s); });
-        mma_step(a, b, acc);
-      });
-      slot = slot == S - 1 ? 0 : slot + 1;
-    }
-    wait_vm<0>();  // the trailing (clamped) loads land before LDS is reused
+    bf16x8 a[2][MR], b[2][NT];
+    // k step s of a staged tile into register set `set`
+    auto read = [&](auto set, auto s, const unsigned char* tile) FS_INLINE {
+      constexpr int x = decltype(set)::value, ks = decltype(s)::value;
+      static_for<NT>([&](auto n) FS_INLINE { b[x][n] = frag<LB, TB>(tile + kStageA, fb + n, ks); });
+      static_for<MR>([&](auto m) FS_INLINE { a[x][m] = frag<LA, TA>(tile, fa + m, ks); });
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    wait_lgkm0_vm<(S - 1) * (IA + IB)>();
     barrier();
+    read(I0{}, I0{}, smem);
+    int slot = 0;
+    // the last step of a tile: its fragments are in set X, the next tile's go
+    // into the other
+    auto last_step = [&](auto set, int kt) FS_INLINE {
+      constexpr int x = decltype(set)::value;
+      const int next = slot == S - 1 ? 0 : slot + 1;
+      const int ahead = min(kt + S, kt1 - 1);
+      prepare(ahead);
+      __builtin_amdgcn_sched_barrier(0);
+      wait_lgkm0_vm<(S - 2) * (IA + IB)>();
+      barrier();
+      // (the two slots are distinct: without the qualifiers the compiler would
+      // let no transposing read pass a direct load)
+      [&](const unsigned char* __restrict__ from, unsigned char* __restrict__ to) FS_INLINE {
+        read(std::integral_constant<int, 1 - x>{}, I0{}, from);
+        sa.stage(ahead, to);
+        sb.stage(ahead, to + kStageA);
+      }(smem + next * kStage, smem + slot * kStage);
+      mma_step(a[x], b[x], acc);
+      interleave<IA + IB>();
+      __builtin_amdgcn_sched_barrier(0);
+      slot = next;
+    };
+    if constexpr (KS == 2) {
+      for (int kt = kt0; kt < kt1; ++kt) {
+        read(I1{}, I1{}, smem + slot * kStage);
+        mma_step(a[0], b[0], acc);
+        interleave<0>();
+        last_step(I1{}, kt);
+      }
+    } else {
+      int kt = kt0;
+      for (; kt + 1 < kt1; kt += 2) {
+        last_step(I0{}, kt);
+        last_step(I1{}, kt + 1);
+      }
+      if (kt < kt1) last_step(I0{}, kt);
+    }
+    wait_lgkm0_vm<0>();  // the trailing (clamped) loads land before LDS is reused
+    barrier();
+  }
+
+  // LDS reads of one k step's fragments.
+  static constexpr int kReads = MR * (LA == kKM ? 2 : 1) + NT * (LB == kKM ? 2 : 1);
+  // The order of one step: its MFMAs with the LDS reads of the next step, and
+  // `loads` direct loads, spread between them.
+  template <int loads>
+  __device__ __forceinline__ static void interleave() {
+    constexpr int kMfma = MR * NT;
+    constexpr int kSlots = kReads + loads;
+    static_for<kSlots>([&](auto i) FS_INLINE {
+      constexpr int k = decltype(i)::value;
+      constexpr int from = kMfma * k / kSlots, to = kMfma * (k + 1) / kSlots;
+      if constexpr (k < kReads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      else __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      if constexpr (to > from) __builtin_amdgcn_sched_group_barrier(0x008, to - from, 0);
+    });
+  }
+
+  template <int N>
+  __device__ __forceinline__ static void wait_lgkm0_vm() {
+    static_assert(N >= 0 && N <= 63, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0x0 << 8));
   }
 };
 
