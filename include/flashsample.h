@@ -343,8 +343,8 @@ FS_API fs_status fs_sample_unfused(const void* h, const void* W, int32_t B, int3
  * gradient (fs_policy_loss, fs_preference_loss), take that gradient back
  * through the LM head (fs_token_logprobs_backward) and clip gradients by
  * their global norm (fs_clip_grad_norm).  All calls are asynchronous on
- * `stream`, allocate nothing, take no atomics (equal calls give equal bits)
- * and may be captured into graphs; calls that overlap need distinct
+ * `stream`, allocate nothing, add in a fixed order (equal calls give equal
+ * bits) and may be captured into graphs; calls that overlap need distinct
  * workspaces and outputs.
  */
 
@@ -389,8 +389,9 @@ FS_API fs_status fs_token_logprobs_packed(const void* h, const void* W_packed, i
  *                of this shard): grad_h is then this shard's share, to be
  *                summed over the ranks, and grad_W its own rows
  *   grad_h       bf16 [B][D], grad_W bf16 [V][D]; either may be NULL (not
- *                wanted).  dz is rounded to bf16 between the products, sums
- *                are fp32, results are rounded once
+ *                wanted).  dz is rounded to bf16 between the products
+ *                (but for the tokens' own, which stay fp32), sums are fp32,
+ *                results are rounded once
  *   workspace    >= fs_token_logprobs_backward_workspace_bytes(B, D, V) bytes
  *                (0 for invalid sizes; dz of up to 1 GiB of the vocabulary at
  *                a time is held in it); contents on entry ignored
