@@ -412,10 +412,11 @@ FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_
  * where it is nonzero.  Tokens that do not count get gradient 0 and their
  * other entries are not used (they may be NaN); entries of out_grad outside
  * every sequence are left as they were.  Sums are held in fp64.
- * Up to 2^24 sequences (FS_ERR_UNSUPPORTED beyond).
+ * Up to 2^20 sequences (FS_ERR_UNSUPPORTED beyond).
  *   workspace  >= fs_loss_workspace_bytes(n_sequences, n_tokens) bytes (for
- *              the preference loss n_sequences = 2 * n_pairs), 0 for invalid
- *              sizes; contents on entry ignored */
+ *              the preference loss n_sequences = 2 * n_pairs); small batches
+ *              need 0 bytes, and then it may be NULL (0 for invalid sizes
+ *              too); contents on entry ignored */
 FS_API size_t fs_loss_workspace_bytes(int32_t n_sequences, int32_t n_tokens);
 
 typedef enum { FS_KL_K1 = 1, FS_KL_K2 = 2, FS_KL_K3 = 3 } fs_kl_kind;

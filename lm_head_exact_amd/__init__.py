@@ -25,5 +25,6 @@ def __getattr__(name):
         return importlib.import_module(".binding", __name__)
     if name in _BINDING_NAMES:
         from . import binding
-        return getattr(binding, name)
+        globals()[name] = value = getattr(binding, name)  # found there from now on
+        return value
     raise AttributeError(name)

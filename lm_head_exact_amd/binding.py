@@ -141,6 +141,9 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _req(t: torch.Tensor, name: str, dtype, ndim: int):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == ndim
+            and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -574,7 +577,27 @@ def selected_config(B: int, D: int, V: int, packed: bool = False, grouped: bool 
 
 # ---- training on sampled tokens ----
 # These calls run on the device of their tensors, whatever the current device
-# is, and on torch's current stream of that device.
+# is, and on torch's current stream of that device.  The loss and clipping
+# kernels take a few microseconds, so what the calls do on the host is kept
+# short: addresses go to ctypes as plain integers, and the device is switched
+# only where it differs.
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _call(fn, dev, *args):
+    """fn(*args, stream) on device `dev` and its current stream."""
+    index = dev.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status != FS_OK:
+        _check(status)
+
 
 def _out(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
     if t is None:
@@ -589,14 +612,14 @@ def _out(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Te
 
 def _workspace(t: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
     if t is None:
-        return alloc_workspace(nbytes, device)
+        return alloc_workspace(nbytes, device) if nbytes else None
     if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     return t
 
 
-def _nbytes(t: torch.Tensor) -> int:
-    return t.numel() * t.element_size()
+def _nbytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _row(t: Optional[torch.Tensor], name: str, dtype, n: int, device):
@@ -648,9 +671,8 @@ def token_logprobs(h: torch.Tensor, W: torch.Tensor, temperature: Optional[torch
     lse = _out(lse, "lse", (B,), torch.float32, dev)
     ws = _workspace(workspace, token_logprobs_workspace_bytes(B, D, V), dev)
     fn = lib().fs_token_logprobs_packed if packed else lib().fs_token_logprobs
-    with torch.cuda.device(dev):
-        _check(fn(_ptr(h), _ptr(W), B, D, V, int(vocab_offset), _ptr(temperature), _ptr(token_ids),
-                  _ptr(lp), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(dev)))
+    _call(fn, dev, _addr(h), _addr(W), B, D, V, int(vocab_offset), _addr(temperature),
+          _addr(token_ids), _addr(lp), _addr(lse), _addr(ws), _nbytes(ws))
     return lp, lse
 
 
@@ -684,11 +706,9 @@ def token_logprobs_backward(h: torch.Tensor, W: torch.Tensor, temperature: Optio
     gh = _out(gh, "grad_h", (B, D), torch.bfloat16, dev) if need_h else None
     gw = _out(gw, "grad_W", (V, D), torch.bfloat16, dev) if need_W else None
     ws = _workspace(workspace, token_logprobs_backward_workspace_bytes(B, D, V), dev)
-    with torch.cuda.device(dev):
-        _check(lib().fs_token_logprobs_backward(
-            _ptr(h), _ptr(W), B, D, V, int(vocab_offset), _ptr(temperature), _ptr(token_ids),
-            _ptr(logprob), _ptr(lse), _ptr(grad_logprob), _ptr(gh), _ptr(gw), _ptr(ws), _nbytes(ws),
-            _stream(dev)))
+    _call(lib().fs_token_logprobs_backward, dev, _addr(h), _addr(W), B, D, V, int(vocab_offset),
+          _addr(temperature), _addr(token_ids), _addr(logprob), _addr(lse), _addr(grad_logprob),
+          _addr(gh), _addr(gw), _addr(ws), _nbytes(ws))
     return gh, gw
 
 
@@ -746,12 +766,10 @@ def policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages: to
     stats = _out(stats, "stats", (4,), torch.float32, dev)
     grad = _out(grad, "grad", (N,), torch.float32, dev)
     ws = _workspace(workspace, loss_workspace_bytes(S, N), dev)
-    with torch.cuda.device(dev):
-        _check(lib().fs_policy_loss(
-            _ptr(logprob), _ptr(old_logprob), _ptr(ref_logprob), _ptr(advantages), _ptr(m),
-            _ptr(cu_seqlens), S, N, int(per_token), clip_low, clip_high, dual_clip, kl_coef,
-            _choice(_KL, kl, "kl"), _choice(_REDUCTIONS, reduction, "reduction"), grad_scale,
-            _ptr(stats), _ptr(grad), _ptr(ws), _nbytes(ws), _stream(dev)))
+    _call(lib().fs_policy_loss, dev, _addr(logprob), _addr(old_logprob), _addr(ref_logprob),
+          _addr(advantages), _addr(m), _addr(cu_seqlens), S, N, int(per_token), clip_low, clip_high,
+          dual_clip, kl_coef, _choice(_KL, kl, "kl"), _choice(_REDUCTIONS, reduction, "reduction"),
+          grad_scale, _addr(stats), _addr(grad), _addr(ws), _nbytes(ws))
     return stats, grad
 
 
@@ -776,12 +794,10 @@ def preference_loss(logprob: torch.Tensor, cu_seqlens: torch.Tensor,
     rewards = _out(rewards, "rewards", (S,), torch.float32, dev)
     grad = _out(grad, "grad", (N,), torch.float32, dev)
     ws = _workspace(workspace, loss_workspace_bytes(S, N), dev)
-    with torch.cuda.device(dev):
-        _check(lib().fs_preference_loss(
-            _ptr(logprob), _ptr(ref_logprob), _ptr(m), _ptr(cu_seqlens), S // 2, N,
-            _choice(_PREFERENCES, kind, "kind"), beta, margin, label_smoothing,
-            int(length_normalised), grad_scale, _ptr(stats), _ptr(rewards), _ptr(grad), _ptr(ws),
-            _nbytes(ws), _stream(dev)))
+    _call(lib().fs_preference_loss, dev, _addr(logprob), _addr(ref_logprob), _addr(m),
+          _addr(cu_seqlens), S // 2, N, _choice(_PREFERENCES, kind, "kind"), beta, margin,
+          label_smoothing, int(length_normalised), grad_scale, _addr(stats), _addr(rewards),
+          _addr(grad), _addr(ws), _nbytes(ws))
     return stats, rewards, grad
 
 
@@ -802,26 +818,34 @@ def clip_grad_norm(grads, max_norm: float, out=None, norm: Optional[torch.Tensor
     outs = grads if out is None else list(out)
     if len(outs) != n:
         raise ValueError(f"out must hold {n} tensors (got {len(outs)})")
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        for t, name in ((g, "grads"), (o, "out")):
-            if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
-                raise TypeError(f"{name}[{i}] must be a bf16, fp16 or fp32 tensor")
-            if t.device.type != "cuda" or t.device != dev:
-                raise ValueError(f"{name}[{i}] must be on the first gradient's device")
-            if not t.is_contiguous():
-                raise ValueError(f"{name}[{i}] must be contiguous")
-        if o.dtype != g.dtype or o.shape != g.shape:
-            raise ValueError(f"out[{i}] must have the type and shape of grads[{i}]")
-    spans = sorted((t.data_ptr(), t.data_ptr() + _nbytes(t)) for t in outs if t.numel())
-    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
-        raise ValueError("the tensors written must not overlap")
-    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
-    types = (ctypes.c_int * n)(*[_DTYPES[g.dtype] for g in grads])
-    src = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
-    dst = None if out is None else (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs])
+    try:
+        types = [_DTYPES[g.dtype] for g in grads]
+    except (KeyError, AttributeError):
+        raise TypeError("grads must be bf16, fp16 or fp32 tensors") from None
+    for i, g in enumerate(grads):
+        if not (g.is_cuda and g.is_contiguous() and g.device == dev):
+            raise ValueError(f"grads[{i}] must be contiguous and on the first gradient's device")
+    if out is not None:
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if not (o.dtype is g.dtype and o.shape == g.shape and o.is_contiguous()
+                    and o.device == dev):
+                raise ValueError(f"out[{i}] must be contiguous, of the type and shape of grads[{i}] "
+                                 "and on its device")
+    count = [g.numel() for g in grads]
+    src = [g.data_ptr() for g in grads]
+    dst = src if out is None else [o.data_ptr() for o in outs]
+    # a tensor's bytes end before the next one's begin
+    ends = 0
+    for p, t, k in sorted(zip(dst, types, count)):
+        if k:
+            if p < ends:
+                raise ValueError("the tensors written must not overlap")
+            ends = p + (k << (1 + (t == 2)))
+    array = ctypes.c_void_p * n
+    sizes = (ctypes.c_int64 * n)(*count)
+    types = (ctypes.c_int * n)(*types)
     norm = _out(norm, "norm", (1,), torch.float32, dev)
     ws = _workspace(workspace, int(lib().fs_clip_grad_norm_workspace_bytes(sizes, n)), dev)
-    with torch.cuda.device(dev):
-        _check(lib().fs_clip_grad_norm(src, dst, sizes, types, n, max_norm, _ptr(norm), _ptr(ws),
-                                       _nbytes(ws), _stream(dev)))
+    _call(lib().fs_clip_grad_norm, dev, array(*src), None if out is None else array(*dst), sizes,
+          types, n, max_norm, _addr(norm), _addr(ws), _nbytes(ws))
     return norm

@@ -2,11 +2,12 @@
 //
 //   norm  = sqrt(sum_i sum_j x_ij^2),   y_ij = x_ij * min(1, max / (norm + 1e-6))
 //
-// Three steps: each block sums the squares of one chunk (fp64 throughout: no
-// gradient's square overflows, and a sum of 10^9 terms loses nothing), one
-// block adds the chunks in order and closes the norm, and each block scales
-// its chunk; where nothing is to be scaled in place the last step's blocks
-// return at once.  Bound by HBM: one read for the norm, one read and one
+// Each block sums the squares of one chunk (fp64 throughout: no gradient's
+// square overflows, and a sum of 10^9 terms loses nothing), the chunks' sums
+// are added in order, and each block scales its chunk; where nothing is to be
+// scaled in place the blocks return at once.  A few chunks' sums are added by
+// every scaling block for itself, which saves a launch; more by one block
+// between the two steps.  Bound by HBM: one read for the norm, one read and one
 // write for the scaling, since the scale is known only after the last element.
 // Tensors go to the device as tables in kernel arguments, kTable to a launch,
 // so that nothing is copied or kept.
@@ -26,6 +27,8 @@ constexpr int kUnroll = 4;
 // Bytes of input per block.
 constexpr int64_t kChunkBytes = 64 << 10;
 constexpr int32_t kMaxTensors = 65536;
+// Chunks' sums that every scaling block adds up for itself.
+constexpr int32_t kInBlockSums = 1024;
 
 struct ClipTable {
   const void* in[kTable];
@@ -139,17 +142,23 @@ __global__ __launch_bounds__(kClipThreads) void squares_kernel(ClipTable t, doub
 
 constexpr int kCloseThreads = 1024;
 
+// The factor for all elements from the chunks' sums, on every thread.
+template <int THREADS>
+__device__ __forceinline__ float close_norm(const double* part, int32_t n, float max_norm,
+                                            float* out_norm) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += THREADS) s += part[i];
+  const double norm = sqrt(block_sum<THREADS>(s));
+  if (out_norm != nullptr && threadIdx.x == 0) *out_norm = static_cast<float>(norm);
+  const double c = static_cast<double>(max_norm) / (norm + 1e-6);
+  return isfinite(norm) && c < 1.0 ? static_cast<float>(c) : 1.0f;
+}
+
 __global__ __launch_bounds__(kCloseThreads) void norm_kernel(const double* part, int32_t n,
                                                              float max_norm, float* out_norm,
                                                              float* scale) {
-  double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += kCloseThreads) s += part[i];
-  const double norm = sqrt(block_sum<kCloseThreads>(s));
-  if (threadIdx.x == 0) {
-    *out_norm = static_cast<float>(norm);
-    const double c = static_cast<double>(max_norm) / (norm + 1e-6);
-    *scale = isfinite(norm) && c < 1.0 ? static_cast<float>(c) : 1.0f;
-  }
+  const float c = close_norm<kCloseThreads>(part, n, max_norm, out_norm);
+  if (threadIdx.x == 0) *scale = c;
 }
 
 template <int DT>
@@ -180,8 +189,15 @@ __device__ __forceinline__ void scale_chunk(const ClipItem& it, float c) {
   for (i += threadIdx.x; i < it.end; i += kClipThreads) q[i] = E::put(E::get(p[i]) * c);
 }
 
-__global__ __launch_bounds__(kClipThreads) void scale_kernel(ClipTable t, const float* scale) {
-  const float c = *scale;
+// part == null: the factor is in *scale; else from the n sums, and the first
+// launch's first block writes the norm.
+__global__ __launch_bounds__(kClipThreads) void scale_kernel(ClipTable t, const float* scale,
+                                                             const double* part, int32_t n,
+                                                             float max_norm, float* out_norm) {
+  const float c = part == nullptr ? *scale
+                                  : close_norm<kClipThreads>(part, n, max_norm,
+                                                             t.base + static_cast<int>(blockIdx.x) == 0
+                                                                 ? out_norm : nullptr);
   const ClipItem it = clip_item(t);
   if (c == 1.0f && it.in == it.out) return;  // nothing to change (uniform)
   if (it.dtype == FS_FP32) scale_chunk<FS_FP32>(it, c);
@@ -294,12 +310,17 @@ FS_API fs_status fs_clip_grad_norm(const void* const* grads, void* const* out,
     return hipGetLastError();
   });
   if (e != hipSuccess) return hip_fail(e, "gradient norm launch");
-  norm_kernel<<<1, kCloseThreads, 0, st>>>(part, static_cast<int32_t>(used), max_norm, out_norm,
-                                           scale);
-  if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "gradient norm launch");
-  if (out == nullptr && std::isinf(max_norm)) return FS_OK;
+  const int32_t sums = static_cast<int32_t>(used);
+  const bool norm_only = out == nullptr && std::isinf(max_norm);
+  const bool in_blocks = sums > 0 && sums <= kInBlockSums && !norm_only;
+  if (!in_blocks) {
+    norm_kernel<<<1, kCloseThreads, 0, st>>>(part, sums, max_norm, out_norm, scale);
+    if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "gradient norm launch");
+    if (norm_only) return FS_OK;
+  }
   e = for_each_table(grads, out, numel, dtypes, n, [&](const ClipTable& t, unsigned b) {
-    scale_kernel<<<b, kClipThreads, 0, st>>>(t, scale);
+    scale_kernel<<<b, kClipThreads, 0, st>>>(t, scale, in_blocks ? part : nullptr, sums, max_norm,
+                                             out_norm);
     return hipGetLastError();
   });
   return e == hipSuccess ? FS_OK : hip_fail(e, "gradient scaling launch");

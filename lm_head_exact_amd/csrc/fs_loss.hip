@@ -3,16 +3,17 @@
 // answers.
 //
 // Both read a packed batch of sequences (tokens [cu[s], cu[s+1]) of flat
-// arrays) and run in three phases, because every token's gradient carries a
-// count over the whole batch (tokens, sequences or pairs that count):
-//   sums    one team of threads per part of a sequence: fp64 sums over its
-//           unmasked tokens into the workspace
-//   close   one block: each sequence's weight, the loss and the statistics
-//   grad    the teams again: each token's gradient from its sequence's weight
-// Every sum is taken in a fixed order (strided lanes, shuffles, then parts in
-// order): no atomics, so equal calls give equal bits.  A token is 13 to 21
-// bytes and a few dozen operations, so a batch of any usual size is bound by
-// launches and memory latency, not by bandwidth.
+// arrays).  Every token's gradient carries a count over the whole batch
+// (tokens, sequences or pairs that count), so a batch takes two passes:
+//   policy      counts (the mask alone), then all terms, gradients and sums,
+//               which one block adds up for the statistics
+//   preference  sums of the answers, then the gradients (one value per
+//               answer), for which each block settles its own answers' pair
+// A small batch takes both passes in one block with its sums in LDS.
+// Every sum is taken in fp64 and in a fixed order (strided lanes, shuffles,
+// then parts or blocks in order), so equal calls give equal bits.  A token is
+// 13 to 21 bytes and a few dozen operations: launches and memory latency bound
+// a batch of any usual size, not bandwidth.
 #include <cmath>
 
 #include "fs_host.hpp"
@@ -24,6 +25,22 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaveSize = 64;
 constexpr int kOneBlockThreads = 1024;
+// Token loads in flight per thread.
+constexpr int kAhead = 4;
+
+// The batches one block handles by itself: about what it reads in the time of
+// a further launch.
+constexpr int32_t kOneBlockTokens = 4096;
+constexpr int32_t kOneBlockSequences = 256;
+constexpr int32_t kOneBlockItems = 512;
+// Parts whose sums every block of the second pass adds up by itself; beyond
+// them one block does between the passes.
+constexpr int64_t kInBlockItems = 4096;
+// The sequences' mean length from which a part takes a block, not a wave.
+constexpr int64_t kBlockTeamTokens = 512;
+// Tokens per part of long sequences, and the most parts of one.
+constexpr int64_t kPartTokens = 4096;
+constexpr int32_t kMaxParts = 256;
 
 struct SeqArgs {
   const int32_t* cu;     // [S + 1]
@@ -78,9 +95,42 @@ __device__ __forceinline__ Sum4 block_sum(Sum4 v) {
   if ((threadIdx.x & (kWaveSize - 1)) == 0) s[threadIdx.x / kWaveSize] = v;
   __syncthreads();
   Sum4 r = s[0];
+#pragma unroll
   for (int w = 1; w < THREADS / kWaveSize; ++w) r.add(s[w]);
   __syncthreads();
   return r;
+}
+
+// Two counts over the block, on every thread.
+template <int THREADS>
+__device__ __forceinline__ int2 block_count(int x, int y) {
+  Sum4 v;
+  v.zero();
+  v.n = x;
+  v.k = y;
+  v = block_sum<THREADS>(v);
+  return int2{v.n, v.k};
+}
+
+// Calls f(t) for the tokens [t0 + lane, t1) strided by `team`, with kAhead of
+// them loaded by load(t) at a time.
+template <class Load, class F>
+__device__ __forceinline__ void each_token(int t0, int t1, int lane, int team, Load load, F f) {
+  for (int t = t0 + lane; t < t1; t += team * kAhead) {
+    decltype(load(t)) v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (t1 - t > u * team) v[u] = load(t + u * team);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (t1 - t > u * team) f(t + u * team, v[u]);
+  }
+}
+
+// Team and item (part of a sequence) of a thread: TEAM threads per item.
+template <int TEAM>
+__device__ __forceinline__ int64_t item_of_thread() {
+  return static_cast<int64_t>(blockIdx.x) * (kThreads / TEAM) + threadIdx.x / TEAM;
 }
 
 // ---------------------------------------------------------------------------
@@ -98,21 +148,53 @@ struct PolicyArgs {
   double log_high, log_low, log_cap;
   float high, low, cap;
   double kl_coef, grad_scale;
-  Sum4* part;      // [S][parts]
-  float* weight;   // [S]
-  float* stats;    // [4]
-  float* grad;     // [T]
+  int32_t* count;   // [S * parts]
+  int2* totals;     // tokens, sequences that count; read if have_totals
+  int32_t have_totals;
+  Sum4* part;       // [blocks]: weighted sums of the blocks
+  float* stats;     // [4]
+  float* grad;      // [T]
+};
+
+struct PolicyToken {
+  float lp, old, ref, adv;
+  bool on;
 };
 
 struct TokenTerms {
-  float surr, kl, gs, gk;
+  float surr, kl, g;
   bool clipped;
 };
 
-__device__ __forceinline__ TokenTerms policy_token(const PolicyArgs& a, int t, float A) {
+__device__ __forceinline__ PolicyToken load_policy(const PolicyArgs& a, int t, float As) {
+  PolicyToken k;
+  k.on = counts(a.q, t);
+  k.lp = a.lp[t];
+  k.old = a.old[t];
+  k.ref = a.ref != nullptr ? a.ref[t] : 0.0f;
+  k.adv = a.adv_per_token ? a.adv[t] : As;
+  return k;
+}
+
+// e^q - q - 1, which cancels to q^2 / 2 near 0: there its series (the first
+// term left out is below 2^-25 of it for |q| < 1/2).
+__device__ __forceinline__ float exp_excess(float q) {
+  float p = 1.0f / 3628800.0f;
+  p = __builtin_fmaf(p, q, 1.0f / 362880.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 40320.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 5040.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 720.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 120.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 24.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 6.0f);
+  p = __builtin_fmaf(p, q, 0.5f);
+  return fabsf(q) < 0.5f ? p * q * q : expf(q) - 1.0f - q;
+}
+
+__device__ __forceinline__ TokenTerms policy_token(const PolicyArgs& a, const PolicyToken& k) {
   TokenTerms o;
-  const double lp = a.lp[t];
-  const double d = lp - static_cast<double>(a.old[t]);
+  const float A = k.adv;
+  const double d = static_cast<double>(k.lp) - static_cast<double>(k.old);
   const float r = expf(static_cast<float>(d));
   const bool over = d > a.log_high, under = d < a.log_low;
   const bool cap = A < 0.0f && d > a.log_cap;
@@ -121,99 +203,173 @@ __device__ __forceinline__ TokenTerms policy_token(const PolicyArgs& a, int t, f
   // an advantage of zero leaves nothing, whatever the ratio
   const float live = A == 0.0f ? 0.0f : -(r * A);
   o.surr = o.clipped ? -(rc * A) : live;
-  o.gs = o.clipped ? 0.0f : live;
-  o.kl = o.gk = 0.0f;
+  o.g = o.clipped ? 0.0f : live;
+  o.kl = 0.0f;
   if (a.ref != nullptr) {
-    const double e = static_cast<double>(a.ref[t]) - lp;
+    const float q = static_cast<float>(static_cast<double>(k.ref) - static_cast<double>(k.lp));
+    float gk;
     if (a.kl_kind == FS_KL_K1) {
-      o.kl = static_cast<float>(-e);
-      o.gk = 1.0f;
+      o.kl = -q;
+      gk = 1.0f;
     } else if (a.kl_kind == FS_KL_K2) {
-      o.kl = static_cast<float>(0.5 * e * e);
-      o.gk = static_cast<float>(-e);
+      o.kl = 0.5f * q * q;
+      gk = -q;
     } else {
-      // e^q - q - 1 cancels to q^2 / 2 near 0: in fp64
-      const double x = expm1(e);
-      o.kl = static_cast<float>(x - e);
-      o.gk = static_cast<float>(-x);
+      o.kl = exp_excess(q);
+      gk = -(q + o.kl);  // -(e^q - 1)
     }
+    o.g += static_cast<float>(a.kl_coef) * gk;
   }
   return o;
 }
 
-// Sums of part y of sequence s over a team of `team` threads, lane in [0, team).
-__device__ __forceinline__ Sum4 policy_part(const PolicyArgs& a, int s, int y, int lane, int team) {
+// Tokens that count in part y of sequence s, this lane's share.
+__device__ __forceinline__ int count_part(const SeqArgs& q, int s, int y, int lane, int team) {
+  int t0, t1, n = 0;
+  part_range(q, s, y, t0, t1);
+  if (q.mask == nullptr) return lane == 0 ? t1 - t0 : 0;
+  each_token(t0, t1, lane, team, [&](int t) { return q.mask[t]; },
+             [&](int, uint8_t m) { n += m != 0; });
+  return n;
+}
+
+__device__ __forceinline__ int wave_count(int n) {
+#pragma unroll
+  for (int m = kWaveSize / 2; m >= 1; m >>= 1) n += __shfl_xor(n, m, kWaveSize);
+  return n;
+}
+
+// Gradients of part y of sequence s (weight w per token) and this lane's share
+// of its sums.
+__device__ __forceinline__ Sum4 policy_part(const PolicyArgs& a, int s, int y, float w, int lane,
+                                            int team) {
   int t0, t1;
   part_range(a.q, s, y, t0, t1);
   Sum4 v;
   v.zero();
   const float As = a.adv_per_token ? 0.0f : a.adv[s];
-  for (int t = t0 + lane; t < t1; t += team) {
-    if (!counts(a.q, t)) continue;  // masked tokens may hold anything
-    const TokenTerms o = policy_token(a, t, a.adv_per_token ? a.adv[t] : As);
-    v.x += static_cast<double>(o.surr);
-    v.y += static_cast<double>(o.kl);
-    v.n += 1;
-    v.k += o.clipped ? 1 : 0;
-  }
+  each_token(t0, t1, lane, team, [&](int t) { return load_policy(a, t, As); },
+             [&](int t, const PolicyToken& k) {
+               float g = 0.0f;
+               if (k.on) {  // masked tokens may hold anything
+                 const TokenTerms o = policy_token(a, k);
+                 v.x += static_cast<double>(o.surr);
+                 v.y += static_cast<double>(o.kl);
+                 v.n += 1;
+                 v.k += o.clipped ? 1 : 0;
+                 g = o.g * w;
+               }
+               a.grad[t] = g;
+             });
   return v;
 }
 
-__device__ __forceinline__ void policy_grad_part(const PolicyArgs& a, int s, int y, int lane,
-                                                 int team) {
-  int t0, t1;
-  part_range(a.q, s, y, t0, t1);
-  const float w = a.weight[s], k = static_cast<float>(a.kl_coef);
-  const float As = a.adv_per_token ? 0.0f : a.adv[s];
-  for (int t = t0 + lane; t < t1; t += team) {
-    float g = 0.0f;
-    if (counts(a.q, t)) {
-      const TokenTerms o = policy_token(a, t, a.adv_per_token ? a.adv[t] : As);
-      g = (o.gs + k * o.gk) * w;
-    }
-    a.grad[t] = g;
-  }
+// Weight of a token of a sequence with n tokens that count.
+__device__ __forceinline__ double policy_weight(const PolicyArgs& a, int2 totals, int n) {
+  if (a.seq_mean) return 1.0 / (static_cast<double>(max(n, 1)) * max(totals.y, 1));
+  return 1.0 / max(totals.x, 1);
 }
 
-// Weights and statistics, by one block of THREADS threads.
+// `all`: weighted sums of the surrogate and the KL term, tokens, clipped ones.
+__device__ __forceinline__ void write_policy_stats(const PolicyArgs& a, const Sum4& all) {
+  a.stats[0] = static_cast<float>(all.x + a.kl_coef * all.y);
+  a.stats[1] = static_cast<float>(all.x);
+  a.stats[2] = static_cast<float>(all.y);
+  a.stats[3] = static_cast<float>(static_cast<double>(all.k) / max(all.n, 1));
+}
+
+template <int TEAM>
+__global__ __launch_bounds__(kThreads) void policy_counts_kernel(PolicyArgs a) {
+  const int64_t item = item_of_thread<TEAM>();
+  const bool in = item < static_cast<int64_t>(a.q.S) * a.q.parts;
+  const int s = static_cast<int>(item / a.q.parts), y = static_cast<int>(item % a.q.parts);
+  int n = in ? wave_count(count_part(a.q, s, y, threadIdx.x % TEAM, TEAM)) : 0;
+  if constexpr (TEAM > kWaveSize) n = block_count<kThreads>(threadIdx.x % kWaveSize == 0 ? n : 0, 0).x;
+  if (in && threadIdx.x % TEAM == 0) a.count[item] = n;
+}
+
+// Tokens and sequences that count, over a block of THREADS threads.
 template <int THREADS>
-__device__ __forceinline__ void policy_close(const PolicyArgs& a) {
-  const int S = a.q.S, Y = a.q.parts;
+__device__ __forceinline__ int2 policy_totals(const PolicyArgs& a) {
+  int tokens = 0, filled = 0;
+  for (int s = threadIdx.x; s < a.q.S; s += THREADS) {
+    int n = 0;
+    for (int y = 0; y < a.q.parts; ++y) n += a.count[static_cast<size_t>(s) * a.q.parts + y];
+    tokens += n;
+    filled += n > 0;
+  }
+  return block_count<THREADS>(tokens, filled);
+}
+
+__global__ __launch_bounds__(kOneBlockThreads) void policy_totals_kernel(PolicyArgs a) {
+  const int2 t = policy_totals<kOneBlockThreads>(a);
+  if (threadIdx.x == 0) *a.totals = t;
+}
+
+template <int TEAM>
+__global__ __launch_bounds__(kThreads) void policy_kernel(PolicyArgs a) {
+  const int2 totals = a.have_totals ? *a.totals : policy_totals<kThreads>(a);
+  const int64_t item = item_of_thread<TEAM>();
   Sum4 v;
   v.zero();
-  int filled = 0;
-  for (int s = threadIdx.x; s < S; s += THREADS) {
-    Sum4 one;
-    one.zero();
-    for (int y = 0; y < Y; ++y) one.add(a.part[static_cast<size_t>(s) * Y + y]);
-    if (one.n > 0) ++filled;
-    if (a.seq_mean && one.n > 0) {
-      one.x /= one.n;
-      one.y /= one.n;
-    }
-    v.add(one);
+  if (item < static_cast<int64_t>(a.q.S) * a.q.parts) {
+    const int s = static_cast<int>(item / a.q.parts), y = static_cast<int>(item % a.q.parts);
+    int n = 0;
+    for (int i = 0; i < a.q.parts; ++i) n += a.count[static_cast<size_t>(s) * a.q.parts + i];
+    const double w = policy_weight(a, totals, n);
+    v = policy_part(a, s, y, static_cast<float>(w * a.grad_scale), threadIdx.x % TEAM, TEAM);
+    v.x *= w;
+    v.y *= w;
   }
-  const Sum4 all = block_sum<THREADS>(v);
-  Sum4 f;
-  f.zero();
-  f.n = filled;
-  const int groups = block_sum<THREADS>(f).n;
-  const double denom = a.seq_mean ? max(groups, 1) : max(all.n, 1);
-  for (int s = threadIdx.x; s < S; s += THREADS) {
-    double w = 1.0 / denom;
-    if (a.seq_mean) {
-      int n = 0;
-      for (int y = 0; y < Y; ++y) n += a.part[static_cast<size_t>(s) * Y + y].n;
-      w /= max(n, 1);
-    }
-    a.weight[s] = static_cast<float>(w * a.grad_scale);
+  v = block_sum<kThreads>(v);
+  if (threadIdx.x == 0) a.part[blockIdx.x] = v;
+}
+
+// A launch of its own: letting the last block of the pass before add up the
+// blocks' sums would cost each of them a write-back of its L2 to be seen
+// (27 us for the pass over a million tokens, against 15 and 4).
+__global__ __launch_bounds__(kOneBlockThreads) void policy_stats_kernel(PolicyArgs a,
+                                                                        unsigned blocks) {
+  Sum4 all;
+  all.zero();
+  for (unsigned i = threadIdx.x; i < blocks; i += kOneBlockThreads) all.add(a.part[i]);
+  all = block_sum<kOneBlockThreads>(all);
+  if (threadIdx.x == 0) write_policy_stats(a, all);
+}
+
+// Both passes in one block: a wave per part, gradients first without their
+// weight, then scaled by the threads that wrote them.
+__global__ __launch_bounds__(kOneBlockThreads) void policy_one_block_kernel(PolicyArgs a) {
+  __shared__ Sum4 part[kOneBlockItems];
+  __shared__ float weight[kOneBlockSequences];
+  constexpr int kWaves = kOneBlockThreads / kWaveSize;
+  const int wave = threadIdx.x / kWaveSize, lane = threadIdx.x % kWaveSize;
+  const int Y = a.q.parts, S = a.q.S, items = S * Y;
+  for (int i = wave; i < items; i += kWaves) {
+    Sum4 v = policy_part(a, i / Y, i % Y, 1.0f, lane, kWaveSize);
+    v.wave_sum();
+    if (lane == 0) part[i] = v;
   }
-  if (threadIdx.x == 0) {
-    const double surr = all.x / denom, kl = all.y / denom;
-    a.stats[0] = static_cast<float>(surr + a.kl_coef * kl);
-    a.stats[1] = static_cast<float>(surr);
-    a.stats[2] = static_cast<float>(kl);
-    a.stats[3] = static_cast<float>(static_cast<double>(all.k) / max(all.n, 1));
+  __syncthreads();
+  Sum4 one;  // S <= threads: a sequence each
+  one.zero();
+  const int s = threadIdx.x;
+  if (s < S)
+    for (int y = 0; y < Y; ++y) one.add(part[s * Y + y]);
+  const int2 totals = block_count<kOneBlockThreads>(one.n, one.n > 0);
+  const double w = policy_weight(a, totals, one.n);
+  if (s < S) weight[s] = static_cast<float>(w * a.grad_scale);
+  one.x *= w;
+  one.y *= w;
+  const Sum4 all = block_sum<kOneBlockThreads>(one);
+  if (threadIdx.x == 0) write_policy_stats(a, all);
+  for (int i = wave; i < items; i += kWaves) {
+    int t0, t1;
+    part_range(a.q, i / Y, i % Y, t0, t1);
+    const float c = weight[i / Y];
+    // zero stays zero: a token that does not count has no gradient
+    each_token(t0, t1, lane, kWaveSize, [&](int t) { return a.grad[t]; },
+               [&](int t, float g) { a.grad[t] = g * c; });
   }
 }
 
@@ -225,14 +381,19 @@ struct PreferenceArgs {
   SeqArgs q;       // S = 2 P
   const float *lp, *ref;  // ref may be null
   int32_t kind, normalise;
-  double beta, margin, smoothing;
-  double grad_scale;
-  Sum4* part;      // [2P][parts]: x the sum of lp - ref, n the tokens
-  float* weight;   // [2P]: each token's gradient
+  double beta, margin, smoothing, grad_scale;
+  struct Part {
+    double x;      // sum of lp - ref
+    int32_t n;     // tokens
+  };
+  Part* part;      // [S * parts]
+  int32_t* pairs;  // pairs that count; read if have_pairs
+  int32_t have_pairs;
   float* stats;    // [3]
-  float* rewards;  // [2P]
+  float* rewards;  // [S]
   float* grad;     // [T]
 };
+using Part = PreferenceArgs::Part;
 
 __device__ __forceinline__ Sum4 preference_part(const PreferenceArgs& a, int s, int y, int lane,
                                                 int team) {
@@ -240,169 +401,178 @@ __device__ __forceinline__ Sum4 preference_part(const PreferenceArgs& a, int s, 
   part_range(a.q, s, y, t0, t1);
   Sum4 v;
   v.zero();
-  for (int t = t0 + lane; t < t1; t += team) {
-    if (!counts(a.q, t)) continue;
-    // fp64: long sums whose difference between two answers is small
-    v.x += static_cast<double>(a.lp[t]) - (a.ref ? static_cast<double>(a.ref[t]) : 0.0);
-    v.n += 1;
-  }
+  struct Token {
+    float lp, ref;
+    bool on;
+  };
+  each_token(t0, t1, lane, team,
+             [&](int t) {
+               return Token{a.lp[t], a.ref != nullptr ? a.ref[t] : 0.0f, counts(a.q, t)};
+             },
+             [&](int, const Token& k) {
+               // fp64: long sums whose difference between two answers is small
+               if (k.on) {
+                 v.x += static_cast<double>(k.lp) - static_cast<double>(k.ref);
+                 v.n += 1;
+               }
+             });
   return v;
 }
 
-__device__ __forceinline__ void preference_grad_part(const PreferenceArgs& a, int s, int y,
-                                                     int lane, int team) {
-  int t0, t1;
-  part_range(a.q, s, y, t0, t1);
-  const float w = a.weight[s];
-  for (int t = t0 + lane; t < t1; t += team) a.grad[t] = counts(a.q, t) ? w : 0.0f;
+// One answer: S and its tokens.
+__device__ __forceinline__ Part answer(const PreferenceArgs& a, const Part* part, int s) {
+  Part r = {0.0, 0};
+  for (int y = 0; y < a.q.parts; ++y) {
+    const Part p = part[static_cast<size_t>(s) * a.q.parts + y];
+    r.x += p.x;
+    r.n += p.n;
+  }
+  if (a.normalise && r.n > 0) r.x /= r.n;
+  return r;
+}
+
+// Loss of a pair that counts and its derivative by D = S_chosen - S_rejected.
+__device__ __forceinline__ double pair_loss(const PreferenceArgs& a, double diff, double& dl) {
+  if (a.kind == FS_PREFERENCE_IPO) {
+    const double t = diff - 0.5 / a.beta;
+    dl = 2.0 * t;
+    return t * t;
+  }
+  const double x = a.beta * diff - a.margin;
+  if (a.kind == FS_PREFERENCE_HINGE) {
+    dl = x < 1.0 ? -a.beta : 0.0;
+    return fmax(1.0 - x, 0.0);
+  }
+  // -(1 - eps) log sigmoid(x) - eps log sigmoid(-x)
+  const double l = log1p(exp(-fabs(x)));
+  dl = a.beta * (a.smoothing - 1.0 / (1.0 + exp(x)));
+  return (1.0 - a.smoothing) * (fmax(-x, 0.0) + l) + a.smoothing * (fmax(x, 0.0) + l);
+}
+
+// Gradient of each token of sequence s that counts.
+__device__ __forceinline__ float answer_weight(const PreferenceArgs& a, const Part* part, int s,
+                                               int pairs) {
+  const int P = a.q.S / 2;
+  const int p = s < P ? s : s - P;
+  const Part hi = answer(a, part, p), lo = answer(a, part, P + p);
+  if (hi.n == 0 || lo.n == 0) return 0.0f;
+  double dl;
+  pair_loss(a, hi.x - lo.x, dl);
+  dl *= a.grad_scale / max(pairs, 1);
+  if (a.normalise) dl /= s < P ? hi.n : lo.n;
+  return static_cast<float>(s < P ? dl : -dl);
 }
 
 template <int THREADS>
-__device__ __forceinline__ void preference_close(const PreferenceArgs& a) {
-  const int P = a.q.S / 2, Y = a.q.parts;
-  auto gather = [&](int s) {
-    Sum4 one;
-    one.zero();
-    for (int y = 0; y < Y; ++y) one.add(a.part[static_cast<size_t>(s) * Y + y]);
-    if (a.normalise && one.n > 0) one.x /= one.n;
-    return one;
-  };
-  Sum4 c;
-  c.zero();
+__device__ __forceinline__ int count_pairs(const PreferenceArgs& a, const Part* part) {
+  const int P = a.q.S / 2;
+  int n = 0;
   for (int p = threadIdx.x; p < P; p += THREADS)
-    if (gather(p).n > 0 && gather(P + p).n > 0) ++c.n;
-  const double pairs = max(block_sum<THREADS>(c).n, 1);
+    n += answer(a, part, p).n > 0 && answer(a, part, P + p).n > 0;
+  return block_count<THREADS>(n, 0).x;
+}
+
+// Statistics and rewards, by one block.
+template <int THREADS>
+__device__ __forceinline__ void preference_stats(const PreferenceArgs& a, const Part* part,
+                                                 int pairs) {
+  const int P = a.q.S / 2;
   Sum4 v;  // x: loss, y: margin of rewards, k: pairs whose chosen answer scores higher
   v.zero();
   for (int p = threadIdx.x; p < P; p += THREADS) {
-    const Sum4 hi = gather(p), lo = gather(P + p);
+    const Part hi = answer(a, part, p), lo = answer(a, part, P + p);
     a.rewards[p] = static_cast<float>(a.beta * hi.x);
     a.rewards[P + p] = static_cast<float>(a.beta * lo.x);
-    double dl = 0.0;
     if (hi.n > 0 && lo.n > 0) {
-      const double diff = hi.x - lo.x;
-      if (a.kind == FS_PREFERENCE_IPO) {
-        const double t = diff - 0.5 / a.beta;
-        v.x += t * t;
-        dl = 2.0 * t;
-      } else {
-        const double x = a.beta * diff - a.margin;
-        if (a.kind == FS_PREFERENCE_HINGE) {
-          v.x += fmax(1.0 - x, 0.0);
-          dl = x < 1.0 ? -a.beta : 0.0;
-        } else {
-          // -(1 - eps) log sigmoid(x) - eps log sigmoid(-x)
-          const double l = log1p(exp(-fabs(x)));
-          v.x += (1.0 - a.smoothing) * (fmax(-x, 0.0) + l) + a.smoothing * (fmax(x, 0.0) + l);
-          dl = a.beta * (a.smoothing - 1.0 / (1.0 + exp(x)));
-        }
-      }
-      v.y += a.beta * diff;
-      v.k += diff > 0.0 ? 1 : 0;
-      dl *= a.grad_scale / pairs;
+      double dl;
+      v.x += pair_loss(a, hi.x - lo.x, dl);
+      v.y += a.beta * (hi.x - lo.x);
+      v.k += hi.x > lo.x;
     }
-    const int nh = a.normalise ? max(hi.n, 1) : 1, nl = a.normalise ? max(lo.n, 1) : 1;
-    a.weight[p] = static_cast<float>(dl / nh);
-    a.weight[P + p] = static_cast<float>(-dl / nl);
   }
-  const Sum4 all = block_sum<THREADS>(v);
+  v = block_sum<THREADS>(v);
   if (threadIdx.x == 0) {
-    a.stats[0] = static_cast<float>(all.x / pairs);
-    a.stats[1] = static_cast<float>(all.k / pairs);
-    a.stats[2] = static_cast<float>(all.y / pairs);
+    const double d = max(pairs, 1);
+    a.stats[0] = static_cast<float>(v.x / d);
+    a.stats[1] = static_cast<float>(v.k / d);
+    a.stats[2] = static_cast<float>(v.y / d);
   }
 }
 
-// ---------------------------------------------------------------------------
-// The two losses behind one set of kernels.
-// ---------------------------------------------------------------------------
-struct Policy {
-  using Args = PolicyArgs;
-  __device__ __forceinline__ static Sum4 part(const Args& a, int s, int y, int lane, int team) {
-    return policy_part(a, s, y, lane, team);
-  }
-  __device__ __forceinline__ static void grad(const Args& a, int s, int y, int lane, int team) {
-    policy_grad_part(a, s, y, lane, team);
-  }
-  template <int THREADS>
-  __device__ __forceinline__ static void close(const Args& a) { policy_close<THREADS>(a); }
-};
-
-struct Preference {
-  using Args = PreferenceArgs;
-  __device__ __forceinline__ static Sum4 part(const Args& a, int s, int y, int lane, int team) {
-    return preference_part(a, s, y, lane, team);
-  }
-  __device__ __forceinline__ static void grad(const Args& a, int s, int y, int lane, int team) {
-    preference_grad_part(a, s, y, lane, team);
-  }
-  template <int THREADS>
-  __device__ __forceinline__ static void close(const Args& a) { preference_close<THREADS>(a); }
-};
-
-// TEAM threads per part: a wave each for short sequences, a block for long ones.
-template <class L, int TEAM>
-__global__ __launch_bounds__(kThreads) void loss_sums_kernel(typename L::Args a) {
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / TEAM) + threadIdx.x / TEAM;
-  const int64_t items = static_cast<int64_t>(a.q.S) * a.q.parts;
-  if constexpr (TEAM == kThreads) {
-    const int s = static_cast<int>(item / a.q.parts), y = static_cast<int>(item % a.q.parts);
-    const Sum4 v = block_sum<kThreads>(L::part(a, s, y, threadIdx.x, TEAM));
-    if (threadIdx.x == 0) a.part[item] = v;
-  } else {
-    if (item >= items) return;  // uniform per wave
-    const int s = static_cast<int>(item / a.q.parts), y = static_cast<int>(item % a.q.parts);
-    Sum4 v = L::part(a, s, y, threadIdx.x % TEAM, TEAM);
-    v.wave_sum();
-    if (threadIdx.x % TEAM == 0) a.part[item] = v;
-  }
+__device__ __forceinline__ void preference_grad_part(const PreferenceArgs& a, int s, int y, float w,
+                                                     int lane, int team) {
+  int t0, t1;
+  part_range(a.q, s, y, t0, t1);
+  each_token(t0, t1, lane, team, [&](int t) { return counts(a.q, t); },
+             [&](int t, bool on) { a.grad[t] = on ? w : 0.0f; });
 }
 
-template <class L>
-__global__ __launch_bounds__(kOneBlockThreads) void loss_close_kernel(typename L::Args a) {
-  L::template close<kOneBlockThreads>(a);
+template <int TEAM>
+__global__ __launch_bounds__(kThreads) void preference_sums_kernel(PreferenceArgs a) {
+  const int64_t item = item_of_thread<TEAM>();
+  const bool in = item < static_cast<int64_t>(a.q.S) * a.q.parts;
+  Sum4 v;
+  v.zero();
+  if (in)
+    v = preference_part(a, static_cast<int>(item / a.q.parts), static_cast<int>(item % a.q.parts),
+                        threadIdx.x % TEAM, TEAM);
+  if constexpr (TEAM > kWaveSize) v = block_sum<kThreads>(v);
+  else v.wave_sum();
+  if (in && threadIdx.x % TEAM == 0) a.part[item] = Part{v.x, v.n};
 }
 
-template <class L, int TEAM>
-__global__ __launch_bounds__(kThreads) void loss_grad_kernel(typename L::Args a) {
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / TEAM) + threadIdx.x / TEAM;
+__global__ __launch_bounds__(kOneBlockThreads) void preference_pairs_kernel(PreferenceArgs a) {
+  const int n = count_pairs<kOneBlockThreads>(a, a.part);
+  if (threadIdx.x == 0) *a.pairs = n;
+}
+
+// Gradients; the grid's last block takes the statistics.
+template <int TEAM>
+__global__ __launch_bounds__(kThreads) void preference_grad_kernel(PreferenceArgs a) {
+  const int pairs = a.have_pairs ? *a.pairs : count_pairs<kThreads>(a, a.part);
+  if (blockIdx.x == gridDim.x - 1) {
+    preference_stats<kThreads>(a, a.part, pairs);
+    return;
+  }
+  const int64_t item = item_of_thread<TEAM>();
   if (item >= static_cast<int64_t>(a.q.S) * a.q.parts) return;
-  L::grad(a, static_cast<int>(item / a.q.parts), static_cast<int>(item % a.q.parts),
-          threadIdx.x % TEAM, TEAM);
+  const int s = static_cast<int>(item / a.q.parts), y = static_cast<int>(item % a.q.parts);
+  preference_grad_part(a, s, y, answer_weight(a, a.part, s, pairs), threadIdx.x % TEAM, TEAM);
 }
 
-// The three phases in one block, for batches that one block reads in about
-// the time of the two further launches.
-template <class L>
-__global__ __launch_bounds__(kOneBlockThreads) void loss_one_block_kernel(typename L::Args a) {
-  const int wave = threadIdx.x / kWaveSize, lane = threadIdx.x % kWaveSize;
+__global__ __launch_bounds__(kOneBlockThreads) void preference_one_block_kernel(PreferenceArgs a) {
+  __shared__ Part part[kOneBlockItems];
+  __shared__ float weight[kOneBlockSequences];
   constexpr int kWaves = kOneBlockThreads / kWaveSize;
-  const int items = a.q.S * a.q.parts;
+  const int wave = threadIdx.x / kWaveSize, lane = threadIdx.x % kWaveSize;
+  const int Y = a.q.parts, items = a.q.S * Y;
   for (int i = wave; i < items; i += kWaves) {
-    Sum4 v = L::part(a, i / a.q.parts, i % a.q.parts, lane, kWaveSize);
+    Sum4 v = preference_part(a, i / Y, i % Y, lane, kWaveSize);
     v.wave_sum();
-    if (lane == 0) a.part[i] = v;
+    if (lane == 0) part[i] = Part{v.x, v.n};
   }
   __syncthreads();
-  L::template close<kOneBlockThreads>(a);
+  const int pairs = count_pairs<kOneBlockThreads>(a, part);
+  if (threadIdx.x < static_cast<unsigned>(a.q.S))
+    weight[threadIdx.x] = answer_weight(a, part, threadIdx.x, pairs);
+  preference_stats<kOneBlockThreads>(a, part, pairs);
   __syncthreads();
   for (int i = wave; i < items; i += kWaves)
-    L::grad(a, i / a.q.parts, i % a.q.parts, lane, kWaveSize);
+    preference_grad_part(a, i / Y, i % Y, weight[i / Y], lane, kWaveSize);
 }
 
-// Tokens one block handles by itself, and the sequences' mean length from
-// which a part takes a block rather than a wave.
-constexpr int64_t kOneBlockTokens = 4096;
-constexpr int64_t kBlockTeamTokens = 512;
-// Tokens per part of long sequences, and the most parts of one.
-constexpr int64_t kPartTokens = 4096;
-constexpr int32_t kMaxParts = 256;
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+bool one_block(int64_t S, int64_t T) {
+  return S == 0 || (T <= kOneBlockTokens && S <= kOneBlockSequences);
+}
 
 // Parts per sequence: enough that a few long sequences still spread over the
-// device, one where there are sequences enough.
+// device (or over one block's waves), one where there are sequences enough.
 int32_t loss_parts(int64_t S, int64_t T) {
   if (S <= 0 || S >= 512) return 1;
-  if (T <= kOneBlockTokens) {  // one block: a part for each of its waves
+  if (one_block(S, T)) {
     const int64_t waves = (kOneBlockThreads / kWaveSize + S - 1) / S, by = (T / S + 63) / 64;
     return static_cast<int32_t>(waves < by ? waves : by < 1 ? 1 : by);
   }
@@ -414,36 +584,76 @@ int32_t loss_parts(int64_t S, int64_t T) {
   return static_cast<int32_t>(p < 1 ? 1 : p > kMaxParts ? kMaxParts : p);
 }
 
-size_t part_bytes(int64_t S, int64_t T) {
-  return round_up(sizeof(Sum4) * static_cast<size_t>(S) * loss_parts(S, T), 256);
-}
+struct LossLayout {
+  size_t head, count, part, total;
+  LossLayout(int64_t S, int64_t T) {
+    if (one_block(S, T)) {
+      head = count = part = total = 0;
+      return;
+    }
+    const size_t items = static_cast<size_t>(S) * loss_parts(S, T);
+    head = 0;  // totals
+    count = 256;
+    part = count + round_up(sizeof(int32_t) * items, 256);
+    total = part + round_up(sizeof(Sum4) * items, 256);
+  }
+};
 
-size_t loss_workspace(int64_t S, int64_t T) {
-  return part_bytes(S, T) + round_up(sizeof(float) * static_cast<size_t>(S), 256);
-}
+struct LossGrid {
+  bool wide;
+  int64_t items;
+  unsigned blocks;
+  explicit LossGrid(const SeqArgs& q) {
+    items = static_cast<int64_t>(q.S) * q.parts;
+    wide = q.T / q.S >= kBlockTeamTokens;
+    constexpr int per = kThreads / kWaveSize;
+    blocks = static_cast<unsigned>(wide ? items : (items + per - 1) / per);
+  }
+};
 
-template <class L>
-hipError_t launch_loss(const typename L::Args& a, hipStream_t stream) {
-  const int64_t S = a.q.S, T = a.q.T, items = S * a.q.parts;
-  if (S == 0 || (T <= kOneBlockTokens && S <= kOneBlockTokens)) {
-    loss_one_block_kernel<L><<<1, kOneBlockThreads, 0, stream>>>(a);
+hipError_t launch_policy(PolicyArgs& a, hipStream_t stream) {
+  if (one_block(a.q.S, a.q.T)) {
+    policy_one_block_kernel<<<1, kOneBlockThreads, 0, stream>>>(a);
     return hipGetLastError();
   }
-  const bool wide = T / S >= kBlockTeamTokens;
-  constexpr int per = kThreads / kWaveSize;
-  const dim3 grid(static_cast<unsigned>(wide ? items : (items + per - 1) / per));
-  if (wide) loss_sums_kernel<L, kThreads><<<grid, kThreads, 0, stream>>>(a);
-  else loss_sums_kernel<L, kWaveSize><<<grid, kThreads, 0, stream>>>(a);
+  const LossGrid g(a.q);
+  if (g.wide) policy_counts_kernel<kThreads><<<g.blocks, kThreads, 0, stream>>>(a);
+  else policy_counts_kernel<kWaveSize><<<g.blocks, kThreads, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  loss_close_kernel<L><<<1, kOneBlockThreads, 0, stream>>>(a);
+  a.have_totals = g.items > kInBlockItems;
+  if (a.have_totals) {
+    policy_totals_kernel<<<1, kOneBlockThreads, 0, stream>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (g.wide) policy_kernel<kThreads><<<g.blocks, kThreads, 0, stream>>>(a);
+  else policy_kernel<kWaveSize><<<g.blocks, kThreads, 0, stream>>>(a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (wide) loss_grad_kernel<L, kThreads><<<grid, kThreads, 0, stream>>>(a);
-  else loss_grad_kernel<L, kWaveSize><<<grid, kThreads, 0, stream>>>(a);
+  policy_stats_kernel<<<1, kOneBlockThreads, 0, stream>>>(a, g.blocks);
   return hipGetLastError();
 }
 
-constexpr int32_t kMaxSequences = 1 << 24;
+hipError_t launch_preference(PreferenceArgs& a, hipStream_t stream) {
+  if (one_block(a.q.S, a.q.T)) {
+    preference_one_block_kernel<<<1, kOneBlockThreads, 0, stream>>>(a);
+    return hipGetLastError();
+  }
+  const LossGrid g(a.q);
+  if (g.wide) preference_sums_kernel<kThreads><<<g.blocks, kThreads, 0, stream>>>(a);
+  else preference_sums_kernel<kWaveSize><<<g.blocks, kThreads, 0, stream>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  a.have_pairs = g.items > kInBlockItems;
+  if (a.have_pairs) {
+    preference_pairs_kernel<<<1, kOneBlockThreads, 0, stream>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (g.wide) preference_grad_kernel<kThreads><<<g.blocks + 1, kThreads, 0, stream>>>(a);
+  else preference_grad_kernel<kWaveSize><<<g.blocks + 1, kThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+constexpr int32_t kMaxSequences = 1 << 20;
 
 fs_status check_sequences(const char* who, int32_t S, int32_t T, const int32_t* cu) {
   if (S < 0 || T < 0)
@@ -459,6 +669,7 @@ fs_status check_sequences(const char* who, int32_t S, int32_t T, const int32_t* 
 }
 
 fs_status check_workspace(const char* who, void* workspace, size_t have, size_t need) {
+  if (need == 0) return FS_OK;
   if (!workspace) return fail(FS_ERR_INVALID_ARG, "%s: null workspace", who);
   if (!aligned(workspace, 256))
     return fail(FS_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
@@ -475,8 +686,7 @@ extern "C" {
 
 FS_API size_t fs_loss_workspace_bytes(int32_t n_sequences, int32_t n_tokens) {
   if (n_sequences < 0 || n_tokens < 0 || n_sequences > fs::kMaxSequences) return 0;
-  const size_t b = fs::loss_workspace(n_sequences, n_tokens);
-  return b < 256 ? 256 : b;
+  return fs::LossLayout(n_sequences, n_tokens).total;
 }
 
 FS_API fs_status fs_policy_loss(const float* logprob, const float* old_logprob,
@@ -518,9 +728,11 @@ FS_API fs_status fs_policy_loss(const float* logprob, const float* old_logprob,
     return fail(FS_ERR_INVALID_ARG, "%s: unknown kl_kind %d", who, static_cast<int>(kl_kind));
   if (reduction != FS_TOKEN_MEAN && reduction != FS_SEQUENCE_MEAN)
     return fail(FS_ERR_INVALID_ARG, "%s: unknown reduction %d", who, static_cast<int>(reduction));
-  st = check_workspace(who, workspace, workspace_bytes, loss_workspace(n_sequences, n_tokens));
+  const LossLayout lay(n_sequences, n_tokens);
+  st = check_workspace(who, workspace, workspace_bytes, lay.total);
   if (st != FS_OK) return st;
   if (start_launches()) return injected_failure(who);
+  char* ws = static_cast<char*>(workspace);
   PolicyArgs a;
   a.q = {cu_seqlens, mask, n_sequences, n_tokens, loss_parts(n_sequences, n_tokens)};
   a.lp = logprob;
@@ -538,12 +750,13 @@ FS_API fs_status fs_policy_loss(const float* logprob, const float* old_logprob,
   a.cap = static_cast<float>(dual_clip);
   a.kl_coef = kl_coef;
   a.grad_scale = grad_scale;
-  a.part = static_cast<Sum4*>(workspace);
-  a.weight = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                      part_bytes(n_sequences, n_tokens));
+  a.totals = reinterpret_cast<int2*>(ws + lay.head);
+  a.have_totals = 0;
+  a.count = reinterpret_cast<int32_t*>(ws + lay.count);
+  a.part = reinterpret_cast<Sum4*>(ws + lay.part);
   a.stats = out_stats;
   a.grad = out_grad;
-  const hipError_t e = launch_loss<Policy>(a, static_cast<hipStream_t>(stream));
+  const hipError_t e = launch_policy(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? FS_OK : hip_fail(e, "policy loss launch");
 }
 
@@ -583,9 +796,11 @@ FS_API fs_status fs_preference_loss(const float* logprob, const float* ref_logpr
     return fail(FS_ERR_INVALID_ARG,
                 "%s: label_smoothing must be in [0, 0.5], and 0 but for the sigmoid loss (got %g)",
                 who, label_smoothing);
-  st = check_workspace(who, workspace, workspace_bytes, loss_workspace(2 * n_pairs, n_tokens));
+  const LossLayout lay(2 * n_pairs, n_tokens);
+  st = check_workspace(who, workspace, workspace_bytes, lay.total);
   if (st != FS_OK) return st;
   if (start_launches()) return injected_failure(who);
+  char* ws = static_cast<char*>(workspace);
   PreferenceArgs a;
   a.q = {cu_seqlens, mask, 2 * n_pairs, n_tokens, loss_parts(2 * n_pairs, n_tokens)};
   a.lp = logprob;
@@ -596,13 +811,13 @@ FS_API fs_status fs_preference_loss(const float* logprob, const float* ref_logpr
   a.margin = margin;
   a.smoothing = label_smoothing;
   a.grad_scale = grad_scale;
-  a.part = static_cast<Sum4*>(workspace);
-  a.weight = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                      part_bytes(2 * n_pairs, n_tokens));
+  a.pairs = reinterpret_cast<int32_t*>(ws + lay.head);
+  a.have_pairs = 0;
+  a.part = reinterpret_cast<Part*>(ws + lay.part);
   a.stats = out_stats;
   a.rewards = out_rewards;
   a.grad = out_grad;
-  const hipError_t e = launch_loss<Preference>(a, static_cast<hipStream_t>(stream));
+  const hipError_t e = launch_preference(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? FS_OK : hip_fail(e, "preference loss launch");
 }
 

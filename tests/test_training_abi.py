@@ -28,13 +28,13 @@ def _backward(L, h=A, W=A, B=4, D=256, V=1000, off=0, T=A, ids=A, lp=A, lse=A, g
     return L.fs_token_logprobs_backward(h, W, B, D, V, off, T, ids, lp, lse, g, gh, gw, ws, wsb, None)
 
 
-def _policy(L, lp=A, old=A, ref=A, adv=A, mask=A, cu=A, S=4, N=100, per=0, lo=0.2, hi=0.2, dual=0.0,
+def _policy(L, lp=A, old=A, ref=A, adv=A, mask=A, cu=A, S=4, N=9000, per=0, lo=0.2, hi=0.2, dual=0.0,
             kc=0.1, kl=3, red=0, scale=1.0, stats=A, grad=A, ws=WS, wsb=BIG):
     return L.fs_policy_loss(lp, old, ref, adv, mask, cu, S, N, per, lo, hi, dual, kc, kl, red, scale,
                             stats, grad, ws, wsb, None)
 
 
-def _preference(L, lp=A, ref=A, mask=A, cu=A, P=2, N=100, kind=0, beta=0.1, margin=0.0, eps=0.0,
+def _preference(L, lp=A, ref=A, mask=A, cu=A, P=2, N=9000, kind=0, beta=0.1, margin=0.0, eps=0.0,
                 norm=0, scale=1.0, stats=A, rewards=A, grad=A, ws=WS, wsb=BIG):
     return L.fs_preference_loss(lp, ref, mask, cu, P, N, kind, beta, margin, eps, norm, scale, stats,
                                 rewards, grad, ws, wsb, None)
@@ -136,7 +136,7 @@ def test_backward_argument_errors(L, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(S=-1), bd.FS_ERR_INVALID_ARG),
     (dict(N=-1), bd.FS_ERR_INVALID_ARG),
-    (dict(S=(1 << 24) + 1), bd.FS_ERR_UNSUPPORTED),
+    (dict(S=(1 << 20) + 1), bd.FS_ERR_UNSUPPORTED),
     (dict(cu=None), bd.FS_ERR_INVALID_ARG),
     (dict(cu=A + 1), bd.FS_ERR_INVALID_ARG),
     (dict(lp=None), bd.FS_ERR_INVALID_ARG),
@@ -209,6 +209,17 @@ def test_preference_argument_errors(L, kw, status):
 def test_clip_argument_errors(L, kw, status):
     assert _clip(L, **kw) == status
     assert len(L.fs_last_error()) > 0
+
+
+def test_small_losses_need_no_workspace(L, monkeypatch):
+    monkeypatch.setenv("FS_FAULT_INJECT", "launch")
+    assert L.fs_loss_workspace_bytes(4, 100) == 0 and L.fs_loss_workspace_bytes(0, 0) == 0
+    assert L.fs_loss_workspace_bytes(4, 5000) > 0 and L.fs_loss_workspace_bytes(300, 300) > 0
+    assert _policy(L, N=100, ws=None, wsb=0) == bd.FS_ERR_HIP        # past the checks
+    assert _preference(L, N=100, ws=None, wsb=0) == bd.FS_ERR_HIP
+    need = L.fs_loss_workspace_bytes(4, 9000)
+    assert _policy(L, wsb=need - 1) == bd.FS_ERR_WORKSPACE
+    assert _preference(L, wsb=need - 1) == bd.FS_ERR_WORKSPACE
 
 
 def test_injected_launch_failure(L, monkeypatch):
