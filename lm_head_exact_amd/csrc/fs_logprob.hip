@@ -77,7 +77,7 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const __bf16* h, int32_t 
 // order and folds the 16 rows into its running pairs.  k's past D take zeros
 // of h against W's last piece.
 // ---------------------------------------------------------------------------
-template <int NT, int NW, int KS, int P, bool PACKED>
+template <int NT, int NW, int KS, int P, bool PACKED, bool WHOLE>
 __global__ __launch_bounds__(NW * kWave) void score_stream_kernel(ScoreArgs a) {
   static_assert(KS % P == 0, "the load ring must tile a group");
   extern __shared__ __attribute__((aligned(16))) unsigned char dyn_smem[];
@@ -103,16 +103,21 @@ __global__ __launch_bounds__(NW * kWave) void score_stream_kernel(ScoreArgs a) {
     inv_t[n] = score_inv_t(a.temperature, bc);
     loc[n] = b < a.B ? target_row(a.ids[bc], a.vocab_offset, a.V) : -1;
   });
-  // the lane's piece of k-step s of group t (clamped to the last group)
+  // The lane's first piece of group t (clamped to the last group), and the
+  // piece of its k-step s.  WHOLE: D is 32 * NW * KS, so no step is past D.
   const int last_step = D / 32 - 1;
-  auto load = [&](int t, int s) FS_INLINE {
+  auto group = [&](int t) FS_INLINE {
     const int g = min(t, ngroups - 1);
     if constexpr (PACKED)
-      return load_frag<true>(packed_frag(a.w.p, g, D, lane) +
-                             static_cast<size_t>(min(wave * KS + s, last_step)) * kPackedStep);
+      return packed_frag(a.w.p, g, D, lane) + (WHOLE ? wave * KS * kPackedStep : 0);
     else
-      return load_frag<false>(a.w.p + static_cast<size_t>(clamp_row(16 * g - a.shift + li, a.V)) * D +
-                              min(k0 + 32 * s, D - 8));
+      return a.w.p + static_cast<size_t>(clamp_row(16 * g - a.shift + li, a.V)) * D + (WHOLE ? k0 : 0);
+  };
+  auto load = [&](const __bf16* p, int s) FS_INLINE {
+    if constexpr (PACKED)
+      return load_frag<true>(p + (WHOLE ? s : min(wave * KS + s, last_step)) * kPackedStep);
+    else
+      return load_frag<false>(p + (WHOLE ? 32 * s : min(k0 + 32 * s, D - 8)));
   };
   float m[NT], s_[NT];
   static_for<NT>([&](auto n) FS_INLINE {
@@ -120,17 +125,21 @@ __global__ __launch_bounds__(NW * kWave) void score_stream_kernel(ScoreArgs a) {
     s_[n] = 0.0f;
   });
   int g = blockIdx.x;
+  const __bf16* wp = group(g);
+  const __bf16* wn = group(g + G);
   bf16x8 ring[P];
-  static_for<P>([&](auto p) FS_INLINE { ring[p] = load(g, p); });
+  static_for<P>([&](auto p) FS_INLINE { ring[p] = load(wp, p); });
   for (int it = 0; g < ngroups; g += G, ++it) {
     f32x4 acc[NT];
     static_for<NT>([&](auto n) FS_INLINE { acc[n] = f32x4{0.f, 0.f, 0.f, 0.f}; });
     static_for<KS>([&](auto sc) FS_INLINE {
       constexpr int s = decltype(sc)::value, slot = s % P;
       static_for<NT>([&](auto n) FS_INLINE { acc[n] = mfma16(ring[slot], hreg[s][n], acc[n]); });
-      if constexpr (s + P < KS) ring[slot] = load(g, s + P);
-      else ring[slot] = load(g + G, s + P - KS);
+      if constexpr (s + P < KS) ring[slot] = load(wp, s + P);
+      else ring[slot] = load(wn, s + P - KS);
     });
+    wp = wn;
+    wn = group(g + 2 * G);
     const int par = it & 1;
     static_for<NT>([&](auto n) FS_INLINE {
       red[((par * NW + wave) * NT + n) * kWave + lane] = acc[n];
@@ -222,14 +231,29 @@ __global__ __launch_bounds__(kCloseThreads) void score_close_kernel(ScoreArgs a,
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-using Tile256 = Tile<kKC, kKC, 2, 4, 8, 4, 2>;
-using Tile128 = Tile<kKC, kKC, 4, 2, 4, 4, 3>;
-using Tile64 = Tile<kKC, kKC, 8, 1, 2, 4, 4>;
-using Tile256F = Tile<kFrag, kKC, 2, 4, 8, 4, 2>;
-using Tile128F = Tile<kFrag, kKC, 4, 2, 4, 4, 3>;
-using Tile64F = Tile<kFrag, kKC, 8, 1, 2, 4, 4>;
-constexpr int kTileRows = 256;
-static_assert(Tile256::TA == kTileRows && Tile128::TA == kTileRows && Tile64::TA == kTileRows, "");
+// Blocks of 256 vocabulary rows by 64, 128 or 256 tokens; where those are too
+// few for the CUs (a vocabulary shard), shorter ones of 4 waves, two per CU.
+// L: the layout of W.
+template <int L, int TB> struct TallTile;
+template <int L> struct TallTile<L, 64> { using T = Tile<L, kKC, 8, 1, 2, 4, 4, 64, L == kFrag>; };
+template <int L> struct TallTile<L, 128> { using T = Tile<L, kKC, 4, 2, 4, 4, 3, 64, L == kFrag>; };
+template <int L> struct TallTile<L, 256> { using T = Tile<L, kKC, 2, 4, 8, 4, 2>; };
+template <int L, int TB> struct ShortTile;
+template <int L> struct ShortTile<L, 64> { using T = Tile<L, kKC, 4, 1, 1, 4, 4, 64, L == kFrag>; };
+template <int L> struct ShortTile<L, 128> { using T = Tile<L, kKC, 4, 1, 1, 8, 3, 64, L == kFrag>; };
+template <int L> struct ShortTile<L, 256> { using T = Tile<L, kKC, 2, 2, 4, 4, 2>; };
+constexpr int kTileRows = 256;      // of the tall tiles
+constexpr int kMinTileRows = 64;    // of any
+constexpr int64_t kFillBlocks = 192;
+
+// Tokens of a tall tile for B tokens.
+int tile_tokens(int32_t B) { return B <= 64 ? 64 : B <= 128 ? 128 : 256; }
+
+// Whether the tall tiles' grid keeps three quarters of the CUs busy.
+bool tall_tiles(int32_t B, int32_t V) {
+  const int TB = tile_tokens(B);
+  return (static_cast<int64_t>(V) + kTileRows - 1) / kTileRows * ((B + TB - 1) / TB) >= kFillBlocks;
+}
 
 constexpr int32_t kMaxScoreB = 1 << 24;
 constexpr int32_t kMaxScoreD = 1 << 20;
@@ -240,7 +264,8 @@ int64_t grid_tiles(int32_t B, int32_t S, int TB) {
 }
 
 template <class T>
-hipError_t launch_tile(const ScoreArgs& a, hipStream_t stream) {
+hipError_t launch_tile(ScoreArgs& a, hipStream_t stream) {
+  a.S = static_cast<int32_t>((static_cast<int64_t>(a.V) + a.shift + T::TA - 1) / T::TA);
   static const hipError_t attr = allow_smem(&score_tile_kernel<T>, T::kSmemBytes);
   if (attr != hipSuccess) return attr;
   score_tile_kernel<T><<<static_cast<unsigned>(grid_tiles(a.B, a.S, T::TB)), T::kThreads,
@@ -248,9 +273,23 @@ hipError_t launch_tile(const ScoreArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int NT, int NW, int KS, int P, bool PACKED>
+template <int L>
+hipError_t launch_tiles(ScoreArgs& a, hipStream_t stream) {
+  const int TB = tile_tokens(a.B);
+  if (tall_tiles(a.B, a.V))
+    return TB == 64    ? launch_tile<typename TallTile<L, 64>::T>(a, stream)
+           : TB == 128 ? launch_tile<typename TallTile<L, 128>::T>(a, stream)
+                       : launch_tile<typename TallTile<L, 256>::T>(a, stream);
+  return TB == 64    ? launch_tile<typename ShortTile<L, 64>::T>(a, stream)
+         : TB == 128 ? launch_tile<typename ShortTile<L, 128>::T>(a, stream)
+                     : launch_tile<typename ShortTile<L, 256>::T>(a, stream);
+}
+
+template <int NT, int NW, int KS, int P, bool PACKED, bool WHOLE = false>
 hipError_t launch_stream(ScoreArgs& a, hipStream_t stream) {
-  const auto kernel = score_stream_kernel<NT, NW, KS, P, PACKED>;
+  if constexpr (!WHOLE)
+    if (a.D == 32 * NW * KS) return launch_stream<NT, NW, KS, P, PACKED, true>(a, stream);
+  const auto kernel = score_stream_kernel<NT, NW, KS, P, PACKED, WHOLE>;
   constexpr size_t smem = 2ull * NW * NT * kWave * sizeof(f32x4);
   static OccupancyCache cache;
   int slots = resident_blocks(kernel, NW * kWave, smem, cache);
@@ -263,7 +302,7 @@ hipError_t launch_stream(ScoreArgs& a, hipStream_t stream) {
 }
 
 // Streaming where the waves' slices of h fit in registers.
-bool streams(int32_t B, int32_t D) { return (B <= 16 && D <= 8192) || (B <= 32 && D <= 4096); }
+bool streams(int32_t B, int32_t D) { return (B <= 16 && D <= 8192) || (B <= 32 && D <= 5120); }
 
 template <bool PACKED>
 hipError_t launch_score_stream(ScoreArgs& a, hipStream_t stream) {
@@ -271,20 +310,24 @@ hipError_t launch_score_stream(ScoreArgs& a, hipStream_t stream) {
   if (B <= 16) {
     if (D <= 1024) return launch_stream<1, 8, 4, 4, PACKED>(a, stream);
     if (D <= 2048) return launch_stream<1, 8, 8, 8, PACKED>(a, stream);
-    if (D <= 4096)
-      return PACKED ? launch_stream<1, 16, 8, 4, PACKED>(a, stream)
-                    : launch_stream<1, 8, 16, 8, PACKED>(a, stream);
+    if (D <= 4096) {
+      if constexpr (PACKED) return launch_stream<1, 16, 8, 4, PACKED>(a, stream);
+      else return launch_stream<1, 8, 16, 8, PACKED>(a, stream);
+    }
+    if (D <= 5120) return launch_stream<1, 8, 20, 4, PACKED>(a, stream);
     if (D <= 6144) return launch_stream<1, 8, 24, 8, PACKED>(a, stream);
     return launch_stream<1, 8, 32, 8, PACKED>(a, stream);
   }
   if (D <= 1024) return launch_stream<2, 8, 4, 4, PACKED>(a, stream);
   if (D <= 2048) return launch_stream<2, 8, 8, 8, PACKED>(a, stream);
-  return PACKED ? launch_stream<2, 8, 16, 4, PACKED>(a, stream)
-                : launch_stream<2, 8, 16, 8, PACKED>(a, stream);
+  if (D <= 4096) return launch_stream<2, 8, 16, PACKED ? 4 : 8, PACKED>(a, stream);
+  return launch_stream<2, 8, 20, 4, PACKED>(a, stream);
 }
 
-int32_t tile_count(int32_t V) {  // grid shifted by up to 3 rows
-  return static_cast<int32_t>((static_cast<int64_t>(V) + 3 + kTileRows - 1) / kTileRows);
+// Most vocabulary tiles of a call (the grid is shifted by up to 3 rows).
+int32_t tile_count(int32_t B, int32_t V) {
+  const int rows = tall_tiles(B, V) ? kTileRows : kMinTileRows;
+  return static_cast<int32_t>((static_cast<int64_t>(V) + 3 + rows - 1) / rows);
 }
 
 bool pads(int32_t B, int32_t D) { return !streams(B, D) && D % 64 != 0; }
@@ -292,7 +335,7 @@ bool pads(int32_t B, int32_t D) { return !streams(B, D) && D % 64 != 0; }
 struct ScoreLayout {
   size_t part, target, pad, total;
   ScoreLayout(int32_t B, int32_t D, int32_t V) {
-    const size_t S = streams(B, D) ? kMaxStreamBlocks : tile_count(V);
+    const size_t S = streams(B, D) ? kMaxStreamBlocks : tile_count(B, V);
     target = round_up(sizeof(float2) * S * B, 256);
     part = 0;
     pad = target + round_up(sizeof(float) * B, 256);
@@ -312,7 +355,7 @@ fs_status check_score_shape(const char* who, int32_t B, int32_t D, int32_t V,
   if (B > kMaxScoreB || D > kMaxScoreD)
     return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, D=%d exceed the %d rows or %d elements a call can "
                 "take", who, B, D, kMaxScoreB, kMaxScoreD);
-  if (grid_tiles(B, tile_count(V), 64) > 0x7FFFFFFF)
+  if (grid_tiles(B, tile_count(B, V), 64) > 0x7FFFFFFF)
     return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, V=%d exceed the launch grid", who, B, V);
   return FS_OK;
 }
@@ -367,15 +410,7 @@ fs_status run_score(const char* who, const void* h, const void* W, int32_t B, in
       if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "padding launch");
       a.h = Operand{hp, Dp, B, Dp};
     }
-    a.S = static_cast<int32_t>((static_cast<int64_t>(V) + a.shift + kTileRows - 1) / kTileRows);
-    if (packed)
-      e = B <= 64    ? launch_tile<Tile64F>(a, s)
-          : B <= 128 ? launch_tile<Tile128F>(a, s)
-                     : launch_tile<Tile256F>(a, s);
-    else
-      e = B <= 64    ? launch_tile<Tile64>(a, s)
-          : B <= 128 ? launch_tile<Tile128>(a, s)
-                     : launch_tile<Tile256>(a, s);
+    e = packed ? launch_tiles<kFrag>(a, s) : launch_tiles<kKC>(a, s);
   }
   if (e != hipSuccess) return hip_fail(e, "log-probability launch");
   if (B >= 2048)

@@ -1,8 +1,8 @@
 // fs_tile.hpp -- the block-tiled bf16 matrix product of the training operators
 // on gfx950: C[b][a] = sum_k A(a, k) B(b, k), fp32 accumulators.
 //
-// One block of 8 waves (two per SIMD, one block per CU) computes TA x TB
-// elements of C; wave w holds MR x NT tiles of 16 x 16
+// One block of 8 waves (two per SIMD, one block per CU), or of 4 waves where a
+// grid of those would leave CUs idle, computes TA x TB elements of C; a wave holds MR x NT tiles of 16 x 16
 // (v_mfma_f32_16x16x32_bf16, A as the MFMA's rows).  Both operands go through
 // LDS, staged by direct global->LDS loads in a ring of S slots of 64 k.  An
 // operand is either
@@ -47,7 +47,8 @@ struct Operand {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-template <int LA_, int LB_, int WA_, int WB_, int MR_, int NT_, int S_, int BK_ = 64>
+template <int LA_, int LB_, int WA_, int WB_, int MR_, int NT_, int S_, int BK_ = 64,
+          bool NTA_ = false>
 struct Tile {
   static constexpr int LA = LA_, LB = LB_;
   static_assert(LB != kFrag, "W is operand A");
@@ -56,6 +57,8 @@ struct Tile {
   static constexpr int kThreads = NW * kWave;
   static constexpr int TA = WA * MR * 16, TB = WB * NT * 16;
   static constexpr int BK = BK_;  // k's of a ring slot: 64 or 32
+  // A is read once and by one block: its loads carry the non-temporal hint
+  static constexpr bool NTA = NTA_;
   static constexpr int KS = BK / 32;
   static constexpr int kStageA = TA * BK * 2, kStageB = TB * BK * 2;  // bytes
   static constexpr int kStage = kStageA + kStageB;
@@ -99,7 +102,7 @@ struct Tile {
   // the operand's rows i0 .., of the pieces this lane loads.  They are the same
   // for every k tile (the tile's start is in scalar registers) but the last,
   // ragged one, whose pieces past the end move to the last piece.
-  template <int L, int T, int I>
+  template <int L, int T, int I, bool NT_LOADS = false>
   struct Stager {
     const __bf16* base;  // rows i0 .. at k = 0
     int64_t step;        // elements from one k tile to the next
@@ -137,7 +140,7 @@ struct Tile {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             rsrc,
             (__attribute__((address_space(3))) void*)(dst + (wave() * I + static_cast<int>(i)) * 1024),
-            16, off[i], 0, 0, 0);
+            16, off[i], 0, 0, NT_LOADS ? 2 : 0);
       });
     }
   };
@@ -184,7 +187,7 @@ struct Tile {
                                              int kt0, int kt1, f32x4 (&acc)[MR][NT],
                                              unsigned char* smem) {
     zero_acc(acc);
-    Stager<LA, TA, IA> sa;
+    Stager<LA, TA, IA, NTA> sa;
     Stager<LB, TB, IB> sb;
     sa.init(A, a0);
     sb.init(B, b0);
