@@ -231,30 +231,6 @@ __global__ __launch_bounds__(kCloseThreads) void score_close_kernel(ScoreArgs a,
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-// Blocks of 256 vocabulary rows by 64, 128 or 256 tokens; where those are too
-// few for the CUs (a vocabulary shard), shorter ones of 4 waves, two per CU.
-// L: the layout of W.
-template <int L, int TB> struct TallTile;
-template <int L> struct TallTile<L, 64> { using T = Tile<L, kKC, 8, 1, 2, 4, 4, 64, L == kFrag>; };
-template <int L> struct TallTile<L, 128> { using T = Tile<L, kKC, 4, 2, 4, 4, 3, 64, L == kFrag>; };
-template <int L> struct TallTile<L, 256> { using T = Tile<L, kKC, 2, 4, 8, 4, 2>; };
-template <int L, int TB> struct ShortTile;
-template <int L> struct ShortTile<L, 64> { using T = Tile<L, kKC, 4, 1, 1, 4, 4, 64, L == kFrag>; };
-template <int L> struct ShortTile<L, 128> { using T = Tile<L, kKC, 4, 1, 1, 8, 3, 64, L == kFrag>; };
-template <int L> struct ShortTile<L, 256> { using T = Tile<L, kKC, 2, 2, 4, 4, 2>; };
-constexpr int kTileRows = 256;      // of the tall tiles
-constexpr int kMinTileRows = 64;    // of any
-constexpr int64_t kFillBlocks = 192;
-
-// Tokens of a tall tile for B tokens.
-int tile_tokens(int32_t B) { return B <= 64 ? 64 : B <= 128 ? 128 : 256; }
-
-// Whether the tall tiles' grid keeps three quarters of the CUs busy.
-bool tall_tiles(int32_t B, int32_t V) {
-  const int TB = tile_tokens(B);
-  return (static_cast<int64_t>(V) + kTileRows - 1) / kTileRows * ((B + TB - 1) / TB) >= kFillBlocks;
-}
-
 constexpr int32_t kMaxScoreB = 1 << 24;
 constexpr int32_t kMaxScoreD = 1 << 20;
 constexpr int kMaxStreamBlocks = 2048;

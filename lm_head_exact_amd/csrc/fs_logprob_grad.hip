@@ -55,7 +55,7 @@ struct GradArgs {
   RowTerm* term;      // [Bp]
   __bf16* hz;         // [Bp][Dp]: their hidden states, zeros behind them
   __bf16* dz;         // [Bp][ldz]
-  float* slab;        // [splits][Bp][D] or null
+  float* slab;        // [max_splits][Bp][D] or null
   // targets by tile of 256 vocabulary rows
   int32_t* first;     // [V]: first place whose target the row is, or -1
   int32_t* list;      // [Bp]: places that have a target here, by tile
@@ -63,7 +63,7 @@ struct GradArgs {
   float* side;        // [Bp][D]: dW rows of targets, at their first place
   int32_t Dp, Bp, ldz;
   int32_t v0, nv;     // the slice: rows v0 .. v0 + nv of W
-  int32_t splits, first_slice;
+  int32_t max_splits, hidden_tb, first_slice;
 };
 
 // A row counts where it has a token; a token of another shard still gives
@@ -225,24 +225,30 @@ void grad_logits_kernel(GradArgs a) {
   const int lane = threadIdx.x & (kWave - 1), li = lane & 15, kb = lane >> 4;
   const int row0 = a0 + T::wave_a() + 4 * kb;  // in the slice
   const bool whole = a0 + T::TA <= a.nv;
-  static_for<T::NT>([&](auto nc) FS_INLINE {
-    const int b = b0 + T::wave_b() + 16 * static_cast<int>(nc) + li;
-    const RowTerm t = a.term[b];
-    const int loc = a.loc[b] - a.v0;
-    __bf16* out = a.dz + static_cast<size_t>(b) * a.ldz + row0;
-    static_for<T::MR>([&](auto m) FS_INLINE {
-      const f32x4 z = acc[m][nc];
-      float d[4];
-      static_for<4>([&](auto rc) FS_INLINE {
-        constexpr int r = decltype(rc)::value;
-        const int v = row0 + 16 * static_cast<int>(m) + r;
-        d[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[r], t.c, -t.lse2)) * t.coef;
-        d[r] = v == loc || (!whole && v >= a.nv) ? 0.0f : d[r];
-      });
-      *reinterpret_cast<uint64_t*>(out + 16 * static_cast<int>(m)) =
-          pack_bf16(d[0], d[1], d[2], d[3]);
-    });
+  RowTerm term[T::NT];
+  int loc[T::NT];
+  static_for<T::NT>([&](auto n) FS_INLINE {
+    const int b = b0 + T::wave_b() + 16 * static_cast<int>(n) + li;
+    term[n] = a.term[b];
+    loc[n] = a.loc[b] - a.v0;
   });
+  __bf16* out = a.dz + static_cast<size_t>(b0 + T::wave_b()) * a.ldz + a0 + T::wave_a();
+  T::store_rows(
+      dyn_smem,
+      [&](auto m, auto nc) FS_INLINE {
+        constexpr int n = decltype(nc)::value;
+        const f32x4 z = acc[m][n];
+        float d[4];
+        static_for<4>([&](auto rc) FS_INLINE {
+          constexpr int r = decltype(rc)::value;
+          const int v = row0 + 16 * static_cast<int>(m) + r;
+          d[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[r], term[n].c, -term[n].lse2)) * term[n].coef;
+          d[r] = v == loc[n] || (!whole && v >= a.nv) ? 0.0f : d[r];
+        });
+        return pack_bf16(d[0], d[1], d[2], d[3]);
+      },
+      [&](int r) FS_INLINE { return out + static_cast<size_t>(r) * a.ldz; },
+      [&](int, int) FS_INLINE { return true; });
 }
 
 // dW of one slice: rows v of W, columns d, summed over the rows with a target.
@@ -262,24 +268,31 @@ void grad_weights_kernel(GradArgs a) {
   else zero_acc(acc);
   const int lane = threadIdx.x & (kWave - 1), li = lane & 15, kb = lane >> 4;
   const int d0 = a0 + T::wave_a() + 4 * kb;
-  static_for<T::NT>([&](auto nc) FS_INLINE {
-    const int v = b0 + T::wave_b() + 16 * static_cast<int>(nc) + li;
-    if (v < a.nv) {
-      const int place = a.first[a.v0 + v];
-      __bf16* out = a.dW + (static_cast<size_t>(a.v0) + v) * a.D + d0;
-      float* side = a.side + static_cast<size_t>(place < 0 ? 0 : place) * a.D + d0;
+  // rows that are a target go to the side in fp32, the others to dW
+  int place[T::NT];
+  static_for<T::NT>([&](auto n) FS_INLINE {
+    const int v = b0 + T::wave_b() + 16 * static_cast<int>(n) + li;
+    place[n] = v < a.nv ? a.first[a.v0 + v] : -1;
+  });
+  static_for<T::NT>([&](auto n) FS_INLINE {
+    if (place[n] >= 0) {
+      float* side = a.side + static_cast<size_t>(place[n]) * a.D + d0;
       static_for<T::MR>([&](auto m) FS_INLINE {
-        const f32x4 x = acc[m][nc];
-        if (d0 + 16 * static_cast<int>(m) < a.D) {
-          if (place >= 0)
-            *reinterpret_cast<f32x4*>(side + 16 * static_cast<int>(m)) = x;
-          else
-            *reinterpret_cast<uint64_t*>(out + 16 * static_cast<int>(m)) =
-                pack_bf16(x[0], x[1], x[2], x[3]);
-        }
+        if (d0 + 16 * static_cast<int>(m) < a.D)
+          *reinterpret_cast<f32x4*>(side + 16 * static_cast<int>(m)) = acc[m][n];
       });
     }
   });
+  const int v0 = b0 + T::wave_b(), c0 = a0 + T::wave_a();
+  __bf16* out = a.dW + (static_cast<size_t>(a.v0) + v0) * a.D + c0;
+  T::store_rows(
+      dyn_smem,
+      [&](auto m, auto n) FS_INLINE {
+        const f32x4 x = acc[m][n];
+        return pack_bf16(x[0], x[1], x[2], x[3]);
+      },
+      [&](int r) FS_INLINE { return out + static_cast<size_t>(r) * a.D; },
+      [&](int r, int c) FS_INLINE { return v0 + r < a.nv && c0 + c < a.D; });
 }
 
 // The targets' rows of dW: what the product left on the side plus each target's
@@ -330,6 +343,30 @@ __device__ __forceinline__ f32x4 add_target(f32x4 x, float t, const __bf16* w) {
                __builtin_fmaf(t, static_cast<float>(v[3]), x[3])};
 }
 
+// Parts of a slice's vocabulary rows for dh: its tiles alone are few, and rows
+// without a target leave some of them empty, so that whole rounds of tiles over
+// the CUs would leave many idle.  The number with the least estimated time, in
+// k tiles of 64: rounds of blocks, each its share of the k tiles and about six
+// of prologue and epilogue, and for every part a slab of fp32 written and read
+// (8e5 of its elements take about as long as one k tile).  The same for every
+// slice of a call, so that each adds to the same slabs.
+__device__ __forceinline__ int hidden_splits(const GradArgs& a, int n) {
+  constexpr int kCus = 256;
+  const int nk = a.ldz / 64;
+  const int64_t tiles = static_cast<int64_t>((n + a.hidden_tb - 1) / a.hidden_tb) * ((a.D + 255) / 256);
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int s = 1; s <= a.max_splits; ++s) {
+    const int64_t cost = (tiles * s + kCus - 1) / kCus * ((nk + s - 1) / s + 6) +
+                         static_cast<int64_t>(s) * n * a.D / 800000;
+    if (cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
 // dh of one slice and one part of its vocabulary rows: straight to dh where
 // that is all there is, else into the part's slab (added up from slice to
 // slice in fp32).
@@ -339,15 +376,16 @@ void grad_hidden_kernel(GradArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char dyn_smem[];
   const int n = *a.count;
   const int nb = (n + T::TB - 1) / T::TB, nd = (a.D + T::TA - 1) / T::TA;
+  const int splits = hidden_splits(a, n);
   int btile, at;
-  if (!xcd_tile(blockIdx.x, nb, static_cast<int64_t>(nd) * a.splits, btile, at)) return;
+  if (!xcd_tile(blockIdx.x, nb, static_cast<int64_t>(nd) * splits, btile, at)) return;
   const int dtile = at % nd, split = at / nd;
   const int a0 = dtile * T::TA, b0 = btile * T::TB;
   const Operand w = {a.W + static_cast<size_t>(a.v0) * a.D, a.D, a.D, a.nv};
   const Operand z = {a.dz, a.ldz, a.Bp, a.ldz};
   const int64_t nk = (a.nv + T::BK - 1) / T::BK;
-  const int kt0 = static_cast<int>(nk * split / a.splits);
-  const int kt1 = static_cast<int>(nk * (split + 1) / a.splits);
+  const int kt0 = static_cast<int>(nk * split / splits);
+  const int kt1 = static_cast<int>(nk * (split + 1) / splits);
   f32x4 acc[T::MR][T::NT];
   if (kt0 < kt1) T::run(w, z, a0, b0, kt0, kt1, acc, dyn_smem);
   else zero_acc(acc);
@@ -383,13 +421,15 @@ void grad_hidden_kernel(GradArgs a) {
 // The slabs of each row and its target's term, added in order and rounded once.
 __global__ __launch_bounds__(256) void grad_slabs_kernel(GradArgs a) {
   const int b = blockIdx.x;
-  if (b >= *a.count) return;
+  const int n = *a.count;
+  if (b >= n) return;
+  const int splits = hidden_splits(a, n);
   __bf16* out = a.dh + static_cast<size_t>(a.row[b]) * a.D;
   const int loc = a.loc[b];
   const float target = a.term[b].target;
   for (int d = threadIdx.x * 4; d < a.D; d += 256 * 4) {
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < a.splits; ++s)
+    for (int s = 0; s < splits; ++s)
       x += *reinterpret_cast<const f32x4*>(a.slab + (static_cast<size_t>(s) * a.Bp + b) * a.D + d);
     if (loc >= 0) x = add_target(x, target, a.W + static_cast<size_t>(loc) * a.D + d);
     *reinterpret_cast<uint64_t*>(out + d) = pack_bf16(x[0], x[1], x[2], x[3]);
@@ -414,7 +454,7 @@ struct GradPlan {
   bool slabs;
   size_t count, slot, row, loc, term, hz, dz, slab, first, list, tile, side, total;
   GradPlan(int32_t B, int32_t D, int32_t V) {
-    TB = B <= 64 ? 64 : B <= 128 ? 128 : 256;
+    TB = tile_tokens(B);
     Bp = static_cast<int32_t>(round_up(B, 256));
     Dp = static_cast<int32_t>(round_up(D, 64));
     int64_t s = kSliceBytes / (2 * static_cast<int64_t>(Bp)) / 256 * 256;
@@ -427,13 +467,12 @@ struct GradPlan {
       s = static_cast<int64_t>(round_up((whole + k - 1) / k, 256));
     }
     slice = static_cast<int32_t>(s);
-    // Parts of the vocabulary for dh: its tiles alone are few, and rows without
-    // a target leave some of them empty, so that whole rounds of tiles would
-    // leave CUs idle; parts of at least 1024 vocabulary rows
+    // at most as many parts for dh (hidden_splits) as make four rounds of tiles,
+    // of at least 256 vocabulary rows
     const int64_t tiles = static_cast<int64_t>((B + TB - 1) / TB) * ((D + 255) / 256);
     int64_t p = (1024 + tiles - 1) / tiles;
-    const int64_t most = (slice < V ? slice : V) / 1024;
-    p = p > most ? most : p;
+    const int64_t most = (slice < V ? slice : V) / 256;
+    p = p > most ? most : p > 32 ? 32 : p;
     splits = static_cast<int32_t>(p < 1 ? 1 : p);
     slabs = splits > 1 || slice < V;
     size_t at = 0;
@@ -460,25 +499,14 @@ struct GradPlan {
 
 unsigned padded_grid(int64_t tiles) { return static_cast<unsigned>((tiles + 7) / 8 * 8); }
 
-// 8 waves over 256 x TB.  K-major operands take ring slots of 32 k, four or
-// five deep (their rows are as long in memory as in slots of 64); K-contiguous
-// ones slots of 64, a whole 128-byte line per row.
-template <int TB>
-struct Shapes;
-template <>
-struct Shapes<256> {
-  template <int LA, int LB> using tile =
-      std::conditional_t<LA == kKM, Tile<LA, LB, 2, 4, 8, 4, LB == kKM ? 5 : 4, 32>,
-                         Tile<LA, LB, 2, 4, 8, 4, 2>>;
-};
-template <>
-struct Shapes<128> {
-  template <int LA, int LB> using tile = Tile<LA, LB, 4, 2, 4, 4, 3>;
-};
-template <>
-struct Shapes<64> {
-  template <int LA, int LB> using tile = Tile<LA, LB, 8, 1, 2, 4, 4>;
-};
+// K-major operands take ring slots of 32 k, four or five deep (their rows are as
+// long in memory as in slots of 64).
+template <int TB> struct HiddenTile;
+template <> struct HiddenTile<64> { using T = Tile<kKM, kKC, 8, 1, 2, 4, 4>; };
+template <> struct HiddenTile<128> { using T = Tile<kKM, kKC, 4, 2, 4, 4, 3>; };
+template <> struct HiddenTile<256> { using T = Tile<kKM, kKC, 2, 4, 8, 4, 4, 32>; };
+using WeightsTall = Tile<kKM, kKM, 2, 4, 8, 4, 5, 32>;   // 256 columns x 256 vocabulary rows
+using WeightsShort = Tile<kKM, kKM, 1, 4, 8, 4, 3, 32>;  // 128 x 256, 4 waves, two blocks per CU
 
 template <class Kernel>
 hipError_t launch_tiles(Kernel kernel, const hipError_t& attr, int64_t tiles, int threads,
@@ -488,31 +516,59 @@ hipError_t launch_tiles(Kernel kernel, const hipError_t& attr, int64_t tiles, in
   return hipGetLastError();
 }
 
-template <int TB>
+template <class T>
 hipError_t launch_logits(const GradArgs& a, hipStream_t stream) {
-  using T = typename Shapes<TB>::template tile<kKC, kKC>;
   static const hipError_t attr = allow_smem(&grad_logits_kernel<T>, T::kSmemBytes);
   return launch_tiles(&grad_logits_kernel<T>, attr,
-                      static_cast<int64_t>((a.nv + T::TA - 1) / T::TA) * ((a.B + TB - 1) / TB),
+                      static_cast<int64_t>((a.nv + T::TA - 1) / T::TA) *
+                          ((a.B + T::TB - 1) / T::TB),
                       T::kThreads, T::kSmemBytes, a, stream);
 }
 
-template <int TB>
+hipError_t launch_logits(const GradArgs& a, hipStream_t stream) {
+  const int TB = tile_tokens(a.B);
+  if (tall_tiles(a.B, a.nv))
+    return TB == 64    ? launch_logits<TallTile<kKC, 64>::T>(a, stream)
+           : TB == 128 ? launch_logits<TallTile<kKC, 128>::T>(a, stream)
+                       : launch_logits<TallTile<kKC, 256>::T>(a, stream);
+  return TB == 64    ? launch_logits<ShortTile<kKC, 64>::T>(a, stream)
+         : TB == 128 ? launch_logits<ShortTile<kKC, 128>::T>(a, stream)
+                     : launch_logits<ShortTile<kKC, 256>::T>(a, stream);
+}
+
+template <class T>
 hipError_t launch_hidden(const GradArgs& a, hipStream_t stream) {
-  using T = typename Shapes<TB>::template tile<kKM, kKC>;
   static const hipError_t attr = allow_smem(&grad_hidden_kernel<T>, T::kSmemBytes);
   return launch_tiles(&grad_hidden_kernel<T>, attr,
-                      static_cast<int64_t>((a.B + TB - 1) / TB) * ((a.D + T::TA - 1) / T::TA) *
-                          a.splits,
+                      static_cast<int64_t>((a.B + T::TB - 1) / T::TB) *
+                          ((a.D + T::TA - 1) / T::TA) * a.max_splits,
                       T::kThreads, T::kSmemBytes, a, stream);
 }
 
+hipError_t launch_hidden(const GradArgs& a, hipStream_t stream) {
+  return a.hidden_tb == 64    ? launch_hidden<HiddenTile<64>::T>(a, stream)
+         : a.hidden_tb == 128 ? launch_hidden<HiddenTile<128>::T>(a, stream)
+                              : launch_hidden<HiddenTile<256>::T>(a, stream);
+}
+
+template <class T>
 hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
-  using T = Shapes<256>::tile<kKM, kKM>;
   static const hipError_t attr = allow_smem(&grad_weights_kernel<T>, T::kSmemBytes);
   return launch_tiles(&grad_weights_kernel<T>, attr,
-                      static_cast<int64_t>((a.nv + T::TB - 1) / T::TB) * ((a.D + T::TA - 1) / T::TA),
+                      static_cast<int64_t>((a.nv + T::TB - 1) / T::TB) *
+                          ((a.D + T::TA - 1) / T::TA),
                       T::kThreads, T::kSmemBytes, a, stream);
+}
+
+// Two short blocks per CU hide one another's prologue and epilogue, which count
+// for few tokens, and make finer rounds of few tiles: 512 tokens on an eighth
+// of the vocabulary 137 against 175 us, 2048 tokens 434 against 448 us; with
+// many rounds the tall blocks read less (2048 tokens on the whole of it 1793
+// against 1860 us, equal at 512).
+hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
+  const int64_t tall = static_cast<int64_t>((a.nv + 255) / 256) * ((a.D + 255) / 256);
+  return a.B > 512 && tall >= 16 * 256 ? launch_weights<WeightsTall>(a, stream)
+                                       : launch_weights<WeightsShort>(a, stream);
 }
 
 hipError_t run_grad(GradArgs& a, const GradPlan& p, hipStream_t s) {
@@ -529,18 +585,10 @@ hipError_t run_grad(GradArgs& a, const GradPlan& p, hipStream_t s) {
     a.v0 = v0;
     a.nv = a.V - v0 < p.slice ? a.V - v0 : p.slice;
     a.first_slice = v0 == 0;
-    if (a.B > 0)
-      e = p.TB == 64 ? launch_logits<64>(a, s)
-          : p.TB == 128 ? launch_logits<128>(a, s)
-                        : launch_logits<256>(a, s);
+    if (a.B > 0) e = launch_logits(a, s);
     if (e != hipSuccess) return e;
     if (a.dW != nullptr && (e = launch_weights(a, s)) != hipSuccess) return e;
-    if (a.dh != nullptr) {
-      e = p.TB == 64 ? launch_hidden<64>(a, s)
-          : p.TB == 128 ? launch_hidden<128>(a, s)
-                        : launch_hidden<256>(a, s);
-      if (e != hipSuccess) return e;
-    }
+    if (a.dh != nullptr && (e = launch_hidden(a, s)) != hipSuccess) return e;
     if (a.V - v0 <= p.slice) break;  // (v0 + slice may not fit in 32 bits)
   }
   if (a.dW != nullptr && a.B > 0) {
@@ -603,8 +651,8 @@ FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_
   if (workspace_bytes < p.total)
     return fail(FS_ERR_WORKSPACE, "%s: workspace of %zu bytes is below the %zu required", who,
                 workspace_bytes, p.total);
-  const int64_t most_tiles = (static_cast<int64_t>(p.slice) / 256 + 1) *
-                             ((B + 63) / 64 > (D + 255) / 256 ? (B + 63) / 64 : (D + 255) / 256);
+  const int64_t most_tiles = (static_cast<int64_t>(p.slice) / 64 + 1) *
+                             ((B + 63) / 64 > (D + 127) / 128 ? (B + 63) / 64 : (D + 127) / 128);
   if (most_tiles > 0x7FFFFFFF - 8)
     return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, D=%d, V=%d exceed the launch grid", who, B, D, V);
   if (start_launches()) return injected_failure(who);
@@ -639,7 +687,8 @@ FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_
   a.Bp = p.Bp;
   a.ldz = p.slice;
   a.v0 = a.nv = 0;
-  a.splits = p.splits;
+  a.max_splits = p.splits;
+  a.hidden_tb = p.TB;
   a.first_slice = 1;
   const hipError_t e = run_grad(a, p, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? FS_OK : hip_fail(e, "log-probability gradient launch");

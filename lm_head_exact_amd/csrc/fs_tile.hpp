@@ -264,6 +264,40 @@ struct Tile {
     barrier();
   }
 
+  // Writes the wave's part of C as bf16 rows of its columns, through LDS, so
+  // that each store covers whole stretches of rows with 16 bytes per lane (as
+  // the accumulators lie, a store would be 8 bytes per lane in stretches of
+  // 32).  value(m, n): the four columns of accumulator (m, n), packed.
+  // keep(r, c): whether the eight columns from c of row r are written, to
+  // out(r) + c elements (r and c in the wave's part).  Each wave has a region
+  // of its own: no barrier.
+  template <class Value, class Out, class Keep>
+  __device__ __forceinline__ static void store_rows(unsigned char* smem, Value value, Out out,
+                                                    Keep keep) {
+    constexpr int kPitch = MR * 32 + 16;  // bytes of a row: its columns and a shift of 4 banks
+    constexpr int HN = NT > 4 ? 4 : NT > 1 ? NT / 2 : 1;  // tiles of 16 rows at a time
+    static_assert(NT % HN == 0, "rounds");
+    static_assert(static_cast<size_t>(NW) * HN * 16 * kPitch <= kSmemBytes, "LDS");
+    const int lane = threadIdx.x & (kWave - 1), li = lane & 15, kb = lane >> 4;
+    unsigned char* mine = smem + wave() * (HN * 16 * kPitch);
+    constexpr int kLanes = MR * 2;  // lanes per row, 16 bytes each
+    constexpr int kRows = kWave / kLanes;
+    static_for<NT / HN>([&](auto h) FS_INLINE {
+      static_for<HN>([&](auto n) FS_INLINE {
+        static_for<MR>([&](auto m) FS_INLINE {
+          *reinterpret_cast<uint64_t*>(mine + (16 * n + li) * kPitch + m * 32 + kb * 8) =
+              value(m, std::integral_constant<int, decltype(h)::value * HN + decltype(n)::value>{});
+        });
+      });
+      static_for<HN * 16 / kRows>([&](auto i) FS_INLINE {
+        const int r = static_cast<int>(i) * kRows + lane / kLanes, c = (lane % kLanes) * 8;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * kPitch + c * 2);
+        const int row = static_cast<int>(h) * HN * 16 + r;
+        if (keep(row, c)) *reinterpret_cast<u32x4*>(out(row) + c) = v;
+      });
+    });
+  }
+
   // LDS reads of one k step's fragments.
   static constexpr int kReads = MR * (LA == kKM ? 2 : 1) + NT * (LB == kKM ? 2 : 1);
   // The order of one step: its MFMAs with the LDS reads of the next step, and
