@@ -251,14 +251,14 @@ hipError_t launch_tile(ScoreArgs& a, hipStream_t stream) {
 
 template <int L>
 hipError_t launch_tiles(ScoreArgs& a, hipStream_t stream) {
-  const int TB = tile_tokens(a.B);
-  if (tall_tiles(a.B, a.V))
-    return TB == 64    ? launch_tile<typename TallTile<L, 64>::T>(a, stream)
-           : TB == 128 ? launch_tile<typename TallTile<L, 128>::T>(a, stream)
-                       : launch_tile<typename TallTile<L, 256>::T>(a, stream);
-  return TB == 64    ? launch_tile<typename ShortTile<L, 64>::T>(a, stream)
-         : TB == 128 ? launch_tile<typename ShortTile<L, 128>::T>(a, stream)
-                     : launch_tile<typename ShortTile<L, 256>::T>(a, stream);
+  switch (logits_tile(a.B, a.V)) {
+    case LogitsTile::kTall64: return launch_tile<typename TallTile<L, 64>::T>(a, stream);
+    case LogitsTile::kTall128: return launch_tile<typename TallTile<L, 128>::T>(a, stream);
+    case LogitsTile::kTall256: return launch_tile<typename TallTile<L, 256>::T>(a, stream);
+    case LogitsTile::kShort64: return launch_tile<typename ShortTile<L, 64>::T>(a, stream);
+    case LogitsTile::kShort128: return launch_tile<typename ShortTile<L, 128>::T>(a, stream);
+    default: return launch_tile<typename ShortTile<L, 256>::T>(a, stream);
+  }
 }
 
 template <int NT, int NW, int KS, int P, bool PACKED, bool WHOLE = false>
@@ -302,7 +302,7 @@ hipError_t launch_score_stream(ScoreArgs& a, hipStream_t stream) {
 
 // Most vocabulary tiles of a call (the grid is shifted by up to 3 rows).
 int32_t tile_count(int32_t B, int32_t V) {
-  const int rows = tall_tiles(B, V) ? kTileRows : kMinTileRows;
+  const int rows = is_tall(logits_tile(B, V)) ? kTallRows : kMinTileRows;
   return static_cast<int32_t>((static_cast<int64_t>(V) + 3 + rows - 1) / rows);
 }
 

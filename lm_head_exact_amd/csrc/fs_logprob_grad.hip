@@ -24,6 +24,7 @@
 // Three matrix products of 2 B V D operations each bound the call for batches
 // of training; a batch of a few rows is bound by reading W twice and writing
 // dW.
+#include <algorithm>
 #include <cmath>
 
 #include "fs_host.hpp"
@@ -48,14 +49,14 @@ struct GradArgs {
   const int32_t* ids;
   __bf16 *dh, *dW;    // either may be null
   // workspace
-  int32_t* count;     // rows with a target
+  int32_t* count;     // [2]: rows with a target; parts of the vocabulary for dh
   int32_t* slot;      // [B]: their place among them, or -1
   int32_t* row;       // [Bp]: the inverse
   int32_t* loc;       // [Bp]: target's row of W, or -1
   RowTerm* term;      // [Bp]
   __bf16* hz;         // [Bp][Dp]: their hidden states, zeros behind them
   __bf16* dz;         // [Bp][ldz]
-  float* slab;        // [max_splits][Bp][D] or null
+  float* slab;        // [max_splits][B][D] or null
   // targets by tile of 256 vocabulary rows
   int32_t* first;     // [V]: first place whose target the row is, or -1
   int32_t* list;      // [Bp]: places that have a target here, by tile
@@ -72,7 +73,24 @@ __device__ __forceinline__ bool has_token(int32_t id) { return id >= 0; }
 
 constexpr int kScanThreads = 1024;
 
-// Places of the rows that have a token, in order (one block).
+// Estimated time of dh over `parts` parts of a slice's vocabulary rows, in k
+// tiles of 64: rounds of blocks over the CUs, each its share of the k tiles
+// and about six of prologue and epilogue, and for every part a slab of fp32
+// written and read (8e5 of its elements take about as long as one k tile).
+__device__ __forceinline__ uint64_t hidden_cost(const GradArgs& a, int n, int parts) {
+  constexpr int kCus = 256;
+  const int nk = a.ldz / 64;
+  const uint64_t tiles =
+      static_cast<uint64_t>((n + a.hidden_tb - 1) / a.hidden_tb) * ((a.D + 255) / 256);
+  return (tiles * parts + kCus - 1) / kCus * ((nk + parts - 1) / parts + 6) +
+         static_cast<uint64_t>(parts) * n * a.D / 800000;
+}
+
+// Places of the rows that have a token, in order (one block), and the parts of
+// the vocabulary that dh is taken in: its tiles alone are few, and rows without
+// a token leave some of them empty, so that whole rounds of tiles would leave
+// many CUs idle.  The same number for every slice of a call, so that each adds
+// to the same slabs.
 __global__ __launch_bounds__(kScanThreads) void grad_rows_kernel(GradArgs a) {
   constexpr int kWaves = kScanThreads / kWave;
   __shared__ int32_t s[kWaves];
@@ -98,7 +116,20 @@ __global__ __launch_bounds__(kScanThreads) void grad_rows_kernel(GradArgs a) {
     base += all;
     __syncthreads();
   }
-  if (threadIdx.x == 0) *a.count = base;
+  __shared__ unsigned long long best;
+  if (threadIdx.x == 0) best = ~0ull;
+  __syncthreads();
+  const int parts = static_cast<int>(threadIdx.x) + 1;  // the least cost, then the fewest parts
+  unsigned long long cost = parts <= a.max_splits ? hidden_cost(a, base, parts) << 12 | parts : ~0ull;
+#pragma unroll
+  for (int m = kWave / 2; m >= 1; m >>= 1)
+    cost = min(cost, static_cast<unsigned long long>(__shfl_xor(cost, m, kWave)));
+  if (lane == 0) atomicMin(&best, cost);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a.count[0] = base;
+    a.count[1] = static_cast<int32_t>(best & 4095);
+  }
 }
 
 // Row b < B: its terms and a copy of its hidden state at its place, or a zero
@@ -285,7 +316,7 @@ void grad_weights_kernel(GradArgs a) {
   });
   const int v0 = b0 + T::wave_b(), c0 = a0 + T::wave_a();
   __bf16* out = a.dW + (static_cast<size_t>(a.v0) + v0) * a.D + c0;
-  T::store_rows(
+  T::template store_rows<true>(
       dyn_smem,
       [&](auto m, auto n) FS_INLINE {
         const f32x4 x = acc[m][n];
@@ -297,39 +328,63 @@ void grad_weights_kernel(GradArgs a) {
 
 // The targets' rows of dW: what the product left on the side plus each target's
 // own term, in the order of the places, rounded once.  One block per place,
-// which has something to do where it is its target's first; a wave takes 512
-// columns.
+// which has something to do where it is its target's first; a thread takes
+// eight columns.  The block looks through its tile's targets 256 at a time for
+// those that are its own, then adds these.
 __global__ __launch_bounds__(256) void grad_target_rows_kernel(GradArgs a) {
+  constexpr int kThreads = 256, kWaves = kThreads / kWave, kAhead = 8;
+  __shared__ int32_t s_place[kThreads + kAhead];
+  __shared__ int32_t s_count[kWaves];
   const int p = blockIdx.x;
-  if (p >= *a.count) return;
+  if (p >= a.count[0]) return;
   const int loc = a.loc[p];
   if (loc < 0 || a.first[loc] != p) return;
   const int2 range = a.tile[loc / kTargetTile];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   typedef float f32x8 __attribute__((ext_vector_type(8)));
-  for (int d = (blockIdx.y * 256 + static_cast<int>(threadIdx.x)) * 8; d < a.D;
-       d += gridDim.y * 256 * 8) {
-    f32x8 x = *reinterpret_cast<const f32x8*>(a.side + static_cast<size_t>(p) * a.D + d);
-    constexpr int kAhead = 8;
-    for (int i0 = range.x; i0 < range.y; i0 += kAhead) {
-      int q[kAhead];
-      bf16x8 h[kAhead];
+  const int span = gridDim.y * kThreads * 8;
+  for (int d0 = blockIdx.y * kThreads * 8; d0 < a.D; d0 += span) {  // uniform
+    const int d = d0 + static_cast<int>(threadIdx.x) * 8;
+    const bool in = d < a.D;
+    f32x8 x = {};
+    if (in) x = *reinterpret_cast<const f32x8*>(a.side + static_cast<size_t>(p) * a.D + d);
+    for (int i0 = range.x; i0 < range.y; i0 += kThreads) {
+      const int i = i0 + static_cast<int>(threadIdx.x);
+      const int q = i < range.y ? a.list[i] : -1;
+      const bool own = q >= 0 && a.loc[q] == loc;
+      const uint64_t votes = __ballot(own);
+      if (lane == 0) s_count[wave] = __popcll(votes);
+      __syncthreads();
+      int at = 0, n = 0;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        q[u] = i0 + u < range.y ? a.list[i0 + u] : -1;
-        if (q[u] >= 0 && a.loc[q[u]] != loc) q[u] = -1;
-        if (q[u] >= 0) h[u] = load_frag(a.hz + static_cast<size_t>(q[u]) * a.Dp + d);
+      for (int w = 0; w < kWaves; ++w) {
+        at += w < wave ? s_count[w] : 0;
+        n += s_count[w];
       }
+      if (own) s_place[at + __popcll(votes & ((uint64_t{1} << lane) - 1))] = q;
+      __syncthreads();
+      for (int k0 = 0; in && k0 < n; k0 += kAhead) {
+        bf16x8 h[kAhead];
+        float t[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (q[u] >= 0) {
-          const float t = a.term[q[u]].target;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = __builtin_fmaf(t, static_cast<float>(h[u][j]), x[j]);
+        for (int u = 0; u < kAhead; ++u) {
+          const int k = min(k0 + u, n - 1);
+          t[u] = k0 + u < n ? a.term[s_place[k]].target : 0.0f;
+          h[u] = load_frag(a.hz + static_cast<size_t>(s_place[k]) * a.Dp + d);
         }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (k0 + u < n)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __builtin_fmaf(t[u], static_cast<float>(h[u][j]), x[j]);
+      }
+      __syncthreads();  // s_place and s_count are free again
     }
-    uint64_t* out = reinterpret_cast<uint64_t*>(a.dW + static_cast<size_t>(loc) * a.D + d);
-    out[0] = pack_bf16(x[0], x[1], x[2], x[3]);
-    out[1] = pack_bf16(x[4], x[5], x[6], x[7]);
+    if (in) {
+      uint64_t* out = reinterpret_cast<uint64_t*>(a.dW + static_cast<size_t>(loc) * a.D + d);
+      out[0] = pack_bf16(x[0], x[1], x[2], x[3]);
+      out[1] = pack_bf16(x[4], x[5], x[6], x[7]);
+    }
   }
 }
 
@@ -343,30 +398,6 @@ __device__ __forceinline__ f32x4 add_target(f32x4 x, float t, const __bf16* w) {
                __builtin_fmaf(t, static_cast<float>(v[3]), x[3])};
 }
 
-// Parts of a slice's vocabulary rows for dh: its tiles alone are few, and rows
-// without a target leave some of them empty, so that whole rounds of tiles over
-// the CUs would leave many idle.  The number with the least estimated time, in
-// k tiles of 64: rounds of blocks, each its share of the k tiles and about six
-// of prologue and epilogue, and for every part a slab of fp32 written and read
-// (8e5 of its elements take about as long as one k tile).  The same for every
-// slice of a call, so that each adds to the same slabs.
-__device__ __forceinline__ int hidden_splits(const GradArgs& a, int n) {
-  constexpr int kCus = 256;
-  const int nk = a.ldz / 64;
-  const int64_t tiles = static_cast<int64_t>((n + a.hidden_tb - 1) / a.hidden_tb) * ((a.D + 255) / 256);
-  int best = 1;
-  int64_t best_cost = INT64_MAX;
-  for (int s = 1; s <= a.max_splits; ++s) {
-    const int64_t cost = (tiles * s + kCus - 1) / kCus * ((nk + s - 1) / s + 6) +
-                         static_cast<int64_t>(s) * n * a.D / 800000;
-    if (cost < best_cost) {
-      best = s;
-      best_cost = cost;
-    }
-  }
-  return best;
-}
-
 // dh of one slice and one part of its vocabulary rows: straight to dh where
 // that is all there is, else into the part's slab (added up from slice to
 // slice in fp32).
@@ -376,7 +407,7 @@ void grad_hidden_kernel(GradArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char dyn_smem[];
   const int n = *a.count;
   const int nb = (n + T::TB - 1) / T::TB, nd = (a.D + T::TA - 1) / T::TA;
-  const int splits = hidden_splits(a, n);
+  const int splits = a.count[1];
   int btile, at;
   if (!xcd_tile(blockIdx.x, nb, static_cast<int64_t>(nd) * splits, btile, at)) return;
   const int dtile = at % nd, split = at / nd;
@@ -394,7 +425,7 @@ void grad_hidden_kernel(GradArgs a) {
   static_for<T::NT>([&](auto nc) FS_INLINE {
     const int b = b0 + T::wave_b() + 16 * static_cast<int>(nc) + li;
     if (b < n) {
-      float* slab = a.slab + (static_cast<size_t>(split) * a.Bp + b) * a.D + d0;
+      float* slab = a.slab + (static_cast<size_t>(split) * a.B + b) * a.D + d0;
       __bf16* out = a.dh + static_cast<size_t>(a.slab ? 0 : a.row[b]) * a.D + d0;
       const int loc = a.loc[b];
       const float target = a.term[b].target;
@@ -418,22 +449,32 @@ void grad_hidden_kernel(GradArgs a) {
   });
 }
 
-// The slabs of each row and its target's term, added in order and rounded once.
-__global__ __launch_bounds__(256) void grad_slabs_kernel(GradArgs a) {
-  const int b = blockIdx.x;
-  const int n = *a.count;
-  if (b >= n) return;
-  const int splits = hidden_splits(a, n);
-  __bf16* out = a.dh + static_cast<size_t>(a.row[b]) * a.D;
-  const int loc = a.loc[b];
-  const float target = a.term[b].target;
-  for (int d = threadIdx.x * 4; d < a.D; d += 256 * 4) {
-    f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < splits; ++s)
-      x += *reinterpret_cast<const f32x4*>(a.slab + (static_cast<size_t>(s) * a.Bp + b) * a.D + d);
-    if (loc >= 0) x = add_target(x, target, a.W + static_cast<size_t>(loc) * a.D + d);
-    *reinterpret_cast<uint64_t*>(out + d) = pack_bf16(x[0], x[1], x[2], x[3]);
+// The slabs of each row and its target's term, added in a fixed order and
+// rounded once.  A block takes one row's 256 columns; its GROUPS groups of 64
+// threads split the slabs.
+template <int GROUPS>
+__global__ __launch_bounds__(GROUPS * kWave) void grad_slabs_kernel(GradArgs a) {
+  __shared__ f32x4 s_sum[GROUPS][kWave];
+  const int b = blockIdx.x, lane = threadIdx.x & (kWave - 1), group = threadIdx.x / kWave;
+  if (b >= a.count[0]) return;
+  const int splits = a.count[1];
+  const int d = blockIdx.y * (kWave * 4) + lane * 4;
+  f32x4 x = {0.f, 0.f, 0.f, 0.f};
+  if (d < a.D) {
+    const float* p = a.slab + static_cast<size_t>(b) * a.D + d;
+    const size_t step = static_cast<size_t>(a.B) * a.D;
+#pragma unroll 4
+    for (int s = group; s < splits; s += GROUPS) x += *reinterpret_cast<const f32x4*>(p + s * step);
   }
+  s_sum[group][lane] = x;
+  __syncthreads();
+  if (group != 0 || d >= a.D) return;
+#pragma unroll
+  for (int g = 1; g < GROUPS; ++g) x += s_sum[g][lane];
+  const int loc = a.loc[b];
+  if (loc >= 0) x = add_target(x, a.term[b].target, a.W + static_cast<size_t>(loc) * a.D + d);
+  *reinterpret_cast<uint64_t*>(a.dh + static_cast<size_t>(a.row[b]) * a.D + d) =
+      pack_bf16(x[0], x[1], x[2], x[3]);
 }
 
 // ---------------------------------------------------------------------------
@@ -467,12 +508,12 @@ struct GradPlan {
       s = static_cast<int64_t>(round_up((whole + k - 1) / k, 256));
     }
     slice = static_cast<int32_t>(s);
-    // at most as many parts for dh (hidden_splits) as make four rounds of tiles,
-    // of at least 256 vocabulary rows
+    // at most as many parts for dh as make four rounds of its tiles, of at least
+    // 256 vocabulary rows, with slabs of no more than 512 MiB
     const int64_t tiles = static_cast<int64_t>((B + TB - 1) / TB) * ((D + 255) / 256);
+    const int64_t rows = slice < V ? slice : V;
     int64_t p = (1024 + tiles - 1) / tiles;
-    const int64_t most = (slice < V ? slice : V) / 256;
-    p = p > most ? most : p > 32 ? 32 : p;
+    p = std::min({p, rows / 256, (int64_t{512} << 20) / (4 * static_cast<int64_t>(B) * D)});
     splits = static_cast<int32_t>(p < 1 ? 1 : p);
     slabs = splits > 1 || slice < V;
     size_t at = 0;
@@ -481,14 +522,14 @@ struct GradPlan {
       at += round_up(bytes, 256);
       return o;
     };
-    count = take(4);
+    count = take(8);
     slot = take(4ull * B);
     row = take(4ull * Bp);
     loc = take(4ull * Bp);
     term = take(sizeof(RowTerm) * Bp);
     hz = take(2ull * Bp * Dp);
     dz = take(2ull * Bp * slice);
-    slab = take(slabs ? 4ull * splits * Bp * D : 0);
+    slab = take(slabs ? 4ull * splits * B * D : 0);
     first = take(4ull * V);
     list = take(4ull * Bp);
     tile = take(sizeof(int2) * target_tiles(V));
@@ -526,14 +567,14 @@ hipError_t launch_logits(const GradArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_logits(const GradArgs& a, hipStream_t stream) {
-  const int TB = tile_tokens(a.B);
-  if (tall_tiles(a.B, a.nv))
-    return TB == 64    ? launch_logits<TallTile<kKC, 64>::T>(a, stream)
-           : TB == 128 ? launch_logits<TallTile<kKC, 128>::T>(a, stream)
-                       : launch_logits<TallTile<kKC, 256>::T>(a, stream);
-  return TB == 64    ? launch_logits<ShortTile<kKC, 64>::T>(a, stream)
-         : TB == 128 ? launch_logits<ShortTile<kKC, 128>::T>(a, stream)
-                     : launch_logits<ShortTile<kKC, 256>::T>(a, stream);
+  switch (logits_tile(a.B, a.nv)) {
+    case LogitsTile::kTall64: return launch_logits<TallTile<kKC, 64>::T>(a, stream);
+    case LogitsTile::kTall128: return launch_logits<TallTile<kKC, 128>::T>(a, stream);
+    case LogitsTile::kTall256: return launch_logits<TallTile<kKC, 256>::T>(a, stream);
+    case LogitsTile::kShort64: return launch_logits<ShortTile<kKC, 64>::T>(a, stream);
+    case LogitsTile::kShort128: return launch_logits<ShortTile<kKC, 128>::T>(a, stream);
+    default: return launch_logits<ShortTile<kKC, 256>::T>(a, stream);
+  }
 }
 
 template <class T>
@@ -597,7 +638,9 @@ hipError_t run_grad(GradArgs& a, const GradPlan& p, hipStream_t s) {
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (a.dh != nullptr && p.slabs) {
-    grad_slabs_kernel<<<a.B, 256, 0, s>>>(a);
+    const dim3 grid(a.B, (a.D + 4 * kWave - 1) / (4 * kWave));
+    if (p.splits > 16) grad_slabs_kernel<16><<<grid, 16 * kWave, 0, s>>>(a);
+    else grad_slabs_kernel<1><<<grid, kWave, 0, s>>>(a);
     e = hipGetLastError();
   }
   return e;

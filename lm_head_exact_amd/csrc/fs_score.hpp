@@ -101,9 +101,8 @@ __device__ __forceinline__ void fold_logits(const Z& z, int row0, int32_t V, int
 }
 
 // ---- tiles of the logits (W is operand A, h operand B) ----
-// Blocks of 256 vocabulary rows by 64, 128 or 256 tokens; where those are too
-// few for the CUs (a vocabulary shard), shorter ones of 4 waves, two per CU.
-// L: the layout of W.
+// L: the layout of W.  Tall: 256 vocabulary rows by 64, 128 or 256 tokens.
+// Short, 4 waves, two blocks per CU: 64 by 64, 64 by 128, 128 by 128.
 template <int L, int TB> struct TallTile;
 template <int L> struct TallTile<L, 64> { using T = Tile<L, kKC, 8, 1, 2, 4, 4, 64, L == kFrag>; };
 template <int L> struct TallTile<L, 128> { using T = Tile<L, kKC, 4, 2, 4, 4, 3, 64, L == kFrag>; };
@@ -112,17 +111,33 @@ template <int L, int TB> struct ShortTile;
 template <int L> struct ShortTile<L, 64> { using T = Tile<L, kKC, 4, 1, 1, 4, 4, 64, L == kFrag>; };
 template <int L> struct ShortTile<L, 128> { using T = Tile<L, kKC, 4, 1, 1, 8, 3, 64, L == kFrag>; };
 template <int L> struct ShortTile<L, 256> { using T = Tile<L, kKC, 2, 2, 4, 4, 2>; };
-constexpr int kTileRows = 256;      // of the tall tiles
-constexpr int kMinTileRows = 64;    // of any
-constexpr int64_t kFillBlocks = 192;
+constexpr int kTallRows = 256, kMinTileRows = 64;  // vocabulary rows of the tall tiles, and of any
 
-// Tokens of a tall tile for B tokens.
+enum class LogitsTile { kTall64, kTall128, kTall256, kShort64, kShort128, kShort256 };
+
 inline int tile_tokens(int32_t B) { return B <= 64 ? 64 : B <= 128 ? 128 : 256; }
 
-// Whether the tall tiles' grid keeps three quarters of the CUs busy.
-inline bool tall_tiles(int32_t B, int32_t V) {
+// The tile for B tokens and V rows: the largest whose grid keeps three quarters
+// of the CUs busy.  Large tiles move less per product (512 tokens on 128256
+// rows of 4096: 475 us tall, 608 short); a grid of few leaves CUs idle (the
+// same tokens on 16032 rows of 8192: 195 us tall, 144 short), and where even
+// the short ones are few their k loops alone take the time (1024 tokens on
+// 1000 rows of 8192: 84 us by 128 x 128, 28 by 64 x 64).
+inline LogitsTile logits_tile(int32_t B, int32_t V) {
+  constexpr int64_t kBlocks = 192;
+  auto grid = [&](int rows, int tokens) {
+    return (static_cast<int64_t>(V) + rows - 1) / rows * ((B + tokens - 1) / tokens);
+  };
   const int TB = tile_tokens(B);
-  return (static_cast<int64_t>(V) + kTileRows - 1) / kTileRows * ((B + TB - 1) / TB) >= kFillBlocks;
+  if (grid(kTallRows, TB) >= kBlocks)
+    return TB == 64    ? LogitsTile::kTall64
+           : TB == 128 ? LogitsTile::kTall128
+                       : LogitsTile::kTall256;
+  if (TB == 256 && grid(128, 128) >= kBlocks) return LogitsTile::kShort256;
+  if (TB == 128 && grid(64, 128) >= kBlocks) return LogitsTile::kShort128;
+  return LogitsTile::kShort64;
 }
+
+inline bool is_tall(LogitsTile t) { return t <= LogitsTile::kTall256; }
 
 }  // namespace fs

@@ -271,7 +271,7 @@ struct Tile {
   // keep(r, c): whether the eight columns from c of row r are written, to
   // out(r) + c elements (r and c in the wave's part).  Each wave has a region
   // of its own: no barrier.
-  template <class Value, class Out, class Keep>
+  template <bool NTS = false, class Value, class Out, class Keep>
   __device__ __forceinline__ static void store_rows(unsigned char* smem, Value value, Out out,
                                                     Keep keep) {
     constexpr int kPitch = MR * 32 + 16;  // bytes of a row: its columns and a shift of 4 banks
@@ -293,7 +293,11 @@ struct Tile {
         const int r = static_cast<int>(i) * kRows + lane / kLanes, c = (lane % kLanes) * 8;
         const u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * kPitch + c * 2);
         const int row = static_cast<int>(h) * HN * 16 + r;
-        if (keep(row, c)) *reinterpret_cast<u32x4*>(out(row) + c) = v;
+        if (keep(row, c)) {
+          u32x4* p = reinterpret_cast<u32x4*>(out(row) + c);
+          if constexpr (NTS) __builtin_nontemporal_store(v, p);
+          else *p = v;
+        }
       });
     });
   }
