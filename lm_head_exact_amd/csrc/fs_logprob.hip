@@ -17,7 +17,7 @@ __global__ __launch_bounds__(T::kThreads) __attribute__((amdgpu_waves_per_eu(2))
 void score_tile_kernel(ScoreArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char dyn_smem[];
   int tile, btile;
-  if (!xcd_tile(blockIdx.x, a.S, (a.B + T::TB - 1) / T::TB, tile, btile)) return;
+  if (!xcd_tile<4>(blockIdx.x, a.S, (a.B + T::TB - 1) / T::TB, tile, btile)) return;
   const int a0 = tile * T::TA, b0 = btile * T::TB;
   f32x4 acc[T::MR][T::NT];
   T::run(a.w, a.h, a0, b0, 0, (a.D + T::BK - 1) / T::BK, acc, dyn_smem);

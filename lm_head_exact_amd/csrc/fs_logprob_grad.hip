@@ -246,7 +246,7 @@ void grad_logits_kernel(GradArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char dyn_smem[];
   const int n = *a.count;
   int tile, btile;
-  if (!xcd_tile(blockIdx.x, (a.nv + T::TA - 1) / T::TA, (n + T::TB - 1) / T::TB, tile, btile))
+  if (!xcd_tile<4>(blockIdx.x, (a.nv + T::TA - 1) / T::TA, (n + T::TB - 1) / T::TB, tile, btile))
     return;
   const int a0 = tile * T::TA, b0 = btile * T::TB;
   const Operand w = {a.W + static_cast<size_t>(a.v0) * a.D, a.D, a.nv, a.D};
@@ -289,7 +289,7 @@ void grad_weights_kernel(GradArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char dyn_smem[];
   const int n = *a.count;
   int tile, dtile;
-  if (!xcd_tile(blockIdx.x, (a.nv + T::TB - 1) / T::TB, (a.D + T::TA - 1) / T::TA, tile, dtile))
+  if (!xcd_tile<4>(blockIdx.x, (a.nv + T::TB - 1) / T::TB, (a.D + T::TA - 1) / T::TA, tile, dtile))
     return;
   const int a0 = dtile * T::TA, b0 = tile * T::TB;
   const Operand h = {a.hz, a.Dp, a.D, a.Bp};
@@ -409,7 +409,7 @@ void grad_hidden_kernel(GradArgs a) {
   const int nb = (n + T::TB - 1) / T::TB, nd = (a.D + T::TA - 1) / T::TA;
   const int splits = a.count[1];
   int btile, at;
-  if (!xcd_tile(blockIdx.x, nb, static_cast<int64_t>(nd) * splits, btile, at)) return;
+  if (!xcd_tile<6>(blockIdx.x, nb, static_cast<int64_t>(nd) * splits, btile, at)) return;
   const int dtile = at % nd, split = at / nd;
   const int a0 = dtile * T::TA, b0 = btile * T::TB;
   const Operand w = {a.W + static_cast<size_t>(a.v0) * a.D, a.D, a.D, a.nv};

@@ -329,17 +329,21 @@ struct Tile {
 // Tile (slow, fast) of block `id` in a grid of at least nslow * nfast blocks;
 // false for the blocks beyond.  Blocks are dealt to the 8 XCDs round robin:
 // block id runs on XCD id mod 8, which takes one contiguous eighth of the
-// tiles in an order that walks four slow tiles by all fast ones, so that the
-// blocks resident on an XCD share their operands' tiles through its L2.
+// tiles in an order that walks GROUP slow tiles by all fast ones, so that the
+// 32 blocks resident on an XCD share their operands' tiles through its L2: a
+// square of them reads the fewest (logits of 4096 tokens: 1.17 PFLOP/s with
+// groups of 2, 1.30 with 4, 1.33 with 5; of 1777 tokens 4 are 3% ahead of 5;
+// gradient of W best with 4, of the hidden states with 6, by 1 to 3%).
+template <int GROUP>
 __device__ __forceinline__ bool xcd_tile(int64_t id, int64_t nslow, int64_t nfast, int& slow,
                                          int& fast) {
   const int64_t total = nslow * nfast, per = (total + 7) / 8;
   const int64_t at = id / 8;
   const int64_t l = (id % 8) * per + at;
   if (at >= per || l >= total) return false;
-  const int64_t g = l / (4 * nfast), w = l % (4 * nfast);
-  const int64_t rows = nslow - 4 * g < 4 ? nslow - 4 * g : 4;
-  slow = static_cast<int>(4 * g + w % rows);
+  const int64_t g = l / (GROUP * nfast), w = l % (GROUP * nfast);
+  const int64_t rows = nslow - GROUP * g < GROUP ? nslow - GROUP * g : GROUP;
+  slow = static_cast<int>(GROUP * g + w % rows);
   fast = static_cast<int>(w / rows);
   return true;
 }
