@@ -179,10 +179,15 @@ struct Tile {
   //
   // Every k step's fragments are read from LDS one step ahead, into the other
   // of two register sets, while the MFMAs of the current step run.  A k tile
-  // has two steps and one barrier, between them: there each wave has read the
+  // has one barrier, before its last step's MFMAs: there each wave has read the
   // whole of the tile (its slot may be refilled) and waited for its share of
   // the next one (which may then be read).  The direct loads of tile kt + S
   // go out right behind that barrier and have S - 1 tiles of time to land.
+  // 4096 x 4096 x 128256 in any of the three pairs of layouts: 1.25 to 1.3
+  // PFLOP/s.  The board's power bounds it: the clock falls to 2.0 GHz with the
+  // matrix cores 60% busy.  Of copies that skip one part each, the one without
+  // the direct loads runs at 1.6, without the LDS reads at 1.35, without both
+  // at 1.8 PFLOP/s; with every load an L2 hit it is 1.38.
   __device__ __forceinline__ static void run(const Operand& A, const Operand& B, int a0, int b0,
                                              int kt0, int kt1, f32x4 (&acc)[MR][NT],
                                              unsigned char* smem) {
@@ -193,8 +198,7 @@ struct Tile {
     sb.init(B, b0);
     // the first k tile that is not whole for an operand
     const int raggedA = A.k / BK, raggedB = B.k / BK;
-    auto stage = [&](int kt, int slot) FS_INLINE {
-      unsigned char* dst = smem + slot * kStage;
+    auto stage = [&](int kt, unsigned char* dst) FS_INLINE {
       sa.stage(kt, dst);
       sb.stage(kt, dst + kStageA);
     };
@@ -203,12 +207,6 @@ struct Tile {
       if (kt == raggedA) sa.offsets(A, a0, A.k - kt * BK);
       if (kt == raggedB) sb.offsets(B, b0, B.k - kt * BK);
     };
-    static_for<S>([&](auto i) FS_INLINE {
-      const int kt = min(kt0 + static_cast<int>(i), kt1 - 1);
-      prepare(kt);
-      stage(kt, i);
-      __builtin_amdgcn_sched_barrier(0);
-    });
     const int fa = wave_a() / 16, fb = wave_b() / 16;
     bf16x8 a[2][MR], b[2][NT];
     // k step s of a staged tile into register set `set`
@@ -219,13 +217,35 @@ struct Tile {
     };
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
-    wait_lgkm0_vm<(S - 1) * (IA + IB)>();
-    barrier();
-    read(I0{}, I0{}, smem);
+    // A tile is read while others are loaded into other slots: the qualifiers
+    // below say so (without them the compiler would let no transposing read
+    // pass a direct load).
+    prepare(kt0);
+    stage(kt0, smem);
+    __builtin_amdgcn_sched_barrier(0);
+    [&](const unsigned char* __restrict__ from, unsigned char* __restrict__ to) FS_INLINE {
+      static_for<S - 1>([&](auto i) FS_INLINE {
+        const int kt = min(kt0 + 1 + static_cast<int>(i), kt1 - 1);
+        prepare(kt);
+        stage(kt, to + i * kStage);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      wait_lgkm0_vm<(S - 1) * (IA + IB)>();
+      barrier();
+      read(I0{}, I0{}, from);
+      if constexpr (KS == 2) {
+        read(I1{}, I1{}, from);
+        mma_step(a[0], b[0], acc);
+        interleave<0>();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }(smem, smem + kStage);
     int slot = 0;
-    // the last step of a tile: its fragments are in set X, the next tile's go
-    // into the other
-    auto last_step = [&](auto set, int kt) FS_INLINE {
+    // From the last step of tile kt, whose fragments are in set X, to the next
+    // tile: the barrier, the next tile's first fragments into the other set, the
+    // loads of the tile S ahead and the step's MFMAs; with two steps per tile
+    // also the next tile's first step and the reads of its second.
+    auto advance = [&](auto set, int kt) FS_INLINE {
       constexpr int x = decltype(set)::value;
       const int next = slot == S - 1 ? 0 : slot + 1;
       const int ahead = min(kt + S, kt1 - 1);
@@ -233,32 +253,33 @@ struct Tile {
       __builtin_amdgcn_sched_barrier(0);
       wait_lgkm0_vm<(S - 2) * (IA + IB)>();
       barrier();
-      // (the two slots are distinct: without the qualifiers the compiler would
-      // let no transposing read pass a direct load)
       [&](const unsigned char* __restrict__ from, unsigned char* __restrict__ to) FS_INLINE {
         read(std::integral_constant<int, 1 - x>{}, I0{}, from);
-        sa.stage(ahead, to);
-        sb.stage(ahead, to + kStageA);
+        stage(ahead, to);
+        mma_step(a[x], b[x], acc);
+        interleave<IA + IB>();
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (KS == 2) {
+          read(I1{}, I1{}, from);
+          mma_step(a[0], b[0], acc);
+          interleave<0>();
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }(smem + next * kStage, smem + slot * kStage);
-      mma_step(a[x], b[x], acc);
-      interleave<IA + IB>();
-      __builtin_amdgcn_sched_barrier(0);
       slot = next;
     };
     if constexpr (KS == 2) {
-      for (int kt = kt0; kt < kt1; ++kt) {
-        read(I1{}, I1{}, smem + slot * kStage);
-        mma_step(a[0], b[0], acc);
-        interleave<0>();
-        last_step(I1{}, kt);
-      }
+      for (int kt = kt0; kt + 1 < kt1; ++kt) advance(I1{}, kt);
+      mma_step(a[1], b[1], acc);
     } else {
+      // (the last tile advances too, to one that is staged but not used: an
+      // ending of its own for either set would cost registers)
       int kt = kt0;
       for (; kt + 1 < kt1; kt += 2) {
-        last_step(I0{}, kt);
-        last_step(I1{}, kt + 1);
+        advance(I0{}, kt);
+        advance(I1{}, kt + 1);
       }
-      if (kt < kt1) last_step(I0{}, kt);
+      if (kt < kt1) advance(I0{}, kt);
     }
     wait_lgkm0_vm<0>();  // the trailing (clamped) loads land before LDS is reused
     barrier();
