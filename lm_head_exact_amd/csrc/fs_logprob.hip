@@ -242,8 +242,9 @@ int64_t grid_tiles(int32_t B, int32_t S, int TB) {
 template <class T>
 hipError_t launch_tile(ScoreArgs& a, hipStream_t stream) {
   a.S = static_cast<int32_t>((static_cast<int64_t>(a.V) + a.shift + T::TA - 1) / T::TA);
-  static const hipError_t attr = allow_smem(&score_tile_kernel<T>, T::kSmemBytes);
-  if (attr != hipSuccess) return attr;
+  static SmemRaised raised;
+  const hipError_t e = raise_smem(&score_tile_kernel<T>, T::kSmemBytes, raised);
+  if (e != hipSuccess) return e;
   score_tile_kernel<T><<<static_cast<unsigned>(grid_tiles(a.B, a.S, T::TB)), T::kThreads,
                          T::kSmemBytes, stream>>>(a);
   return hipGetLastError();

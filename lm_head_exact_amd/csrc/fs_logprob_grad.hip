@@ -550,17 +550,18 @@ using WeightsTall = Tile<kKM, kKM, 2, 4, 8, 4, 5, 32>;   // 256 columns x 256 vo
 using WeightsShort = Tile<kKM, kKM, 1, 4, 8, 4, 3, 32>;  // 128 x 256, 4 waves, two blocks per CU
 
 template <class Kernel>
-hipError_t launch_tiles(Kernel kernel, const hipError_t& attr, int64_t tiles, int threads,
-                        size_t smem, const GradArgs& a, hipStream_t stream) {
-  if (attr != hipSuccess) return attr;
+hipError_t launch_tiles(Kernel kernel, SmemRaised& raised, int64_t tiles, int threads, size_t smem,
+                        const GradArgs& a, hipStream_t stream) {
+  const hipError_t e = raise_smem(kernel, smem, raised);
+  if (e != hipSuccess) return e;
   kernel<<<padded_grid(tiles), threads, smem, stream>>>(a);
   return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch_logits(const GradArgs& a, hipStream_t stream) {
-  static const hipError_t attr = allow_smem(&grad_logits_kernel<T>, T::kSmemBytes);
-  return launch_tiles(&grad_logits_kernel<T>, attr,
+  static SmemRaised raised;
+  return launch_tiles(&grad_logits_kernel<T>, raised,
                       static_cast<int64_t>((a.nv + T::TA - 1) / T::TA) *
                           ((a.B + T::TB - 1) / T::TB),
                       T::kThreads, T::kSmemBytes, a, stream);
@@ -579,8 +580,8 @@ hipError_t launch_logits(const GradArgs& a, hipStream_t stream) {
 
 template <class T>
 hipError_t launch_hidden(const GradArgs& a, hipStream_t stream) {
-  static const hipError_t attr = allow_smem(&grad_hidden_kernel<T>, T::kSmemBytes);
-  return launch_tiles(&grad_hidden_kernel<T>, attr,
+  static SmemRaised raised;
+  return launch_tiles(&grad_hidden_kernel<T>, raised,
                       static_cast<int64_t>((a.B + T::TB - 1) / T::TB) *
                           ((a.D + T::TA - 1) / T::TA) * a.max_splits,
                       T::kThreads, T::kSmemBytes, a, stream);
@@ -594,8 +595,8 @@ hipError_t launch_hidden(const GradArgs& a, hipStream_t stream) {
 
 template <class T>
 hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
-  static const hipError_t attr = allow_smem(&grad_weights_kernel<T>, T::kSmemBytes);
-  return launch_tiles(&grad_weights_kernel<T>, attr,
+  static SmemRaised raised;
+  return launch_tiles(&grad_weights_kernel<T>, raised,
                       static_cast<int64_t>((a.nv + T::TB - 1) / T::TB) *
                           ((a.D + T::TA - 1) / T::TA),
                       T::kThreads, T::kSmemBytes, a, stream);

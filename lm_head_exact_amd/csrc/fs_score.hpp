@@ -11,6 +11,8 @@
 // t_target - logsumexp(all) would cancel there.
 #pragma once
 
+#include <atomic>
+
 #include "fs_tile.hpp"
 
 namespace fs {
@@ -139,5 +141,24 @@ inline LogitsTile logits_tile(int32_t B, int32_t V) {
 }
 
 inline bool is_tall(LogitsTile t) { return t <= LogitsTile::kTall256; }
+
+// Raises a kernel's dynamic-LDS limit, once per device (the limit is a device's
+// own).  Each kernel keeps its own record.
+struct SmemRaised {
+  static constexpr int kMaxDevices = 64;
+  std::atomic<bool> on[kMaxDevices];
+};
+template <class Kernel>
+hipError_t raise_smem(Kernel kernel, size_t smem, SmemRaised& raised) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const bool known = dev >= 0 && dev < SmemRaised::kMaxDevices;
+  if (known && raised.on[dev].load(std::memory_order_acquire)) return hipSuccess;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == hipSuccess && known) raised.on[dev].store(true, std::memory_order_release);
+  return e;
+}
 
 }  // namespace fs

@@ -2,10 +2,12 @@
 // on gfx950: C[b][a] = sum_k A(a, k) B(b, k), fp32 accumulators.
 //
 // One block of 8 waves (two per SIMD, one block per CU), or of 4 waves where a
-// grid of those would leave CUs idle, computes TA x TB elements of C; a wave holds MR x NT tiles of 16 x 16
-// (v_mfma_f32_16x16x32_bf16, A as the MFMA's rows).  Both operands go through
-// LDS, staged by direct global->LDS loads in a ring of S slots of 64 k.  An
-// operand is either
+// grid of those would leave CUs idle, computes TA x TB elements of C; a wave
+// holds MR x NT tiles of 16 x 16 (v_mfma_f32_16x16x32_bf16, A as the MFMA's
+// rows).  Both operands go through LDS, staged by direct global->LDS loads in a
+// ring of S slots of BK = 64 or 32 k.  (64 halves the barriers; an operand read
+// by transposing takes 32, whose finer slots hold the same bytes in flight with
+// one k step of registers fewer.)  An operand is either
 //   K-contiguous (KC)  element (i, k) at p[i * pitch + k]: 16-byte pieces
 //                      along k, read back as they are (ds_read_b128);
 //   K-major (KM)       element (i, k) at p[k * pitch + i]: 16-byte pieces
@@ -20,7 +22,8 @@
 // of W.
 //
 // LDS layouts.  KC: rows of 64 k (128 bytes, 8 pieces), piece j of row i at
-// slot j ^ (i mod 8).  KM: rows of one k (T elements), the 32-byte unit u of
+// slot j ^ (i mod 8); rows of 32 k (4 pieces) at slot j ^ (i / 2 mod 4): the 16
+// rows of a read cover the banks evenly.  KM: rows of one k (T elements), the 32-byte unit u of
 // row k at unit u ^ g(k), g(k) = (k mod 4) + 4 (k / 8 mod 2): a transposing
 // read takes from each of its four 16-lane groups four rows of one unit; g
 // spreads the eight rows of 32 lanes over the eight 32-byte bank groups.  The
@@ -65,7 +68,8 @@ struct Tile {
   static constexpr size_t kSmemBytes = static_cast<size_t>(S) * kStage;
   static constexpr int IA = kStageA / (NW * 1024), IB = kStageB / (NW * 1024);
   static_assert(kStageA % (NW * 1024) == 0 && kStageB % (NW * 1024) == 0, "staging divides evenly");
-  static_assert((LA != kKM || TA % 128 == 0) && (LB != kKM || TB % 128 == 0), "KM swizzle needs 8 units a row");
+  static_assert((LA != kKM || TA % 128 == 0) && (LB != kKM || TB % 128 == 0),
+                "KM swizzle needs 8 units a row");
   static_assert(kSmemBytes <= 160 * 1024, "LDS");
   static constexpr int kBufferFlags = 0x00020000;
 
