@@ -345,7 +345,8 @@ FS_API fs_status fs_sample_unfused(const void* h, const void* W, int32_t B, int3
  * their global norm (fs_clip_grad_norm).  All calls are asynchronous on
  * `stream`, allocate nothing, add in a fixed order (equal calls give equal
  * bits) and may be captured into graphs; calls that overlap need distinct
- * workspaces and outputs.
+ * workspaces and outputs.  Outputs and workspaces overlap neither one another
+ * nor an input, except where a call says so.
  */
 
 /* Log-probabilities of given tokens under softmax(z_b / T_b), z_b = W h_b, with
@@ -355,7 +356,8 @@ FS_API fs_status fs_sample_unfused(const void* h, const void* W, int32_t B, int3
  *                fragment order (fs_pack_weights, D % 32 == 0)
  *   temperature  fp32 [B], device, or NULL (all 1).  As in the samplers the
  *                logits are scaled by fp32(1/T), and a row whose temperature
- *                is not a positive number is scored unscaled
+ *                is not a positive number is scored unscaled (below 2^-128
+ *                fp32(1/T) is infinite: NaN)
  *   token_ids    int32 [B], device: GLOBAL ids; negative: the row has none
  *   out_logprob  fp32 [B]: log p(token); 0 for rows without a token; -inf for
  *                a token outside [vocab_offset, vocab_offset + V)
@@ -393,8 +395,10 @@ FS_API fs_status fs_token_logprobs_packed(const void* h, const void* W_packed, i
  *                (but for the tokens' own, which stay fp32), sums are fp32,
  *                results are rounded once
  *   workspace    >= fs_token_logprobs_backward_workspace_bytes(B, D, V) bytes
- *                (0 for invalid sizes; dz of up to 1 GiB of the vocabulary at
- *                a time is held in it); contents on entry ignored
+ *                (0 for invalid sizes).  It holds dz for a slice of the
+ *                vocabulary at a time (up to 1 GiB), partial sums of grad_h in
+ *                fp32 (up to 512 MiB, or one [B][D] if that is more) and six
+ *                bytes per element of h; contents on entry ignored
  * B == 0 sets grad_W to 0. */
 FS_API size_t fs_token_logprobs_backward_workspace_bytes(int32_t B, int32_t D, int32_t V);
 FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_t B, int32_t D,
@@ -410,8 +414,9 @@ FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_
  * non-decreasing; offsets outside [0, n_tokens] are clamped to it).  Sequences
  * may be empty.  mask is uint8 [n_tokens], device, or NULL: a token counts
  * where it is nonzero.  Tokens that do not count get gradient 0 and their
- * other entries are not used (they may be NaN); entries of out_grad outside
- * every sequence are left as they were.  Sums are held in fp64.
+ * other entries are not used (they may be NaN).  Entries of out_grad before
+ * the first and behind the last sequence are set to 0 with zero_outside, else
+ * left as they were.  Sums are held in fp64.
  * Up to 2^20 sequences (FS_ERR_UNSUPPORTED beyond).
  *   workspace  >= fs_loss_workspace_bytes(n_sequences, n_tokens) bytes (for
  *              the preference loss n_sequences = 2 * n_pairs); small batches
@@ -445,9 +450,9 @@ FS_API fs_status fs_policy_loss(const float* logprob, const float* old_logprob,
                                 int32_t n_sequences, int32_t n_tokens,
                                 int32_t advantage_per_token, double clip_low, double clip_high,
                                 double dual_clip, double kl_coef, fs_kl_kind kl_kind,
-                                fs_loss_reduction reduction, double grad_scale, float* out_stats,
-                                float* out_grad, void* workspace, size_t workspace_bytes,
-                                void* stream);
+                                fs_loss_reduction reduction, double grad_scale,
+                                int32_t zero_outside, float* out_stats, float* out_grad,
+                                void* workspace, size_t workspace_bytes, void* stream);
 
 typedef enum {
   FS_PREFERENCE_SIGMOID = 0,
@@ -475,9 +480,10 @@ FS_API fs_status fs_preference_loss(const float* logprob, const float* ref_logpr
                                     const uint8_t* mask, const int32_t* cu_seqlens,
                                     int32_t n_pairs, int32_t n_tokens, fs_preference_kind kind,
                                     double beta, double margin, double label_smoothing,
-                                    int32_t length_normalised, double grad_scale, float* out_stats,
-                                    float* out_rewards, float* out_grad, void* workspace,
-                                    size_t workspace_bytes, void* stream);
+                                    int32_t length_normalised, double grad_scale,
+                                    int32_t zero_outside, float* out_stats, float* out_rewards,
+                                    float* out_grad, void* workspace, size_t workspace_bytes,
+                                    void* stream);
 
 /* Clipping by the global norm: norm = sqrt(sum over all tensors of x^2), and
  * every element times min(1, max_norm / (norm + 1e-6)).  A norm that is not

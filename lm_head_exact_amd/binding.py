@@ -6,6 +6,7 @@ goes to the library on torch's current HIP stream.  Every step of the
 sampler runs in the library's kernels.  If the library is missing or fails
 to load, every function raises; there is no fallback path.
 """
+import bisect
 import ctypes
 import os
 import re
@@ -92,9 +93,9 @@ def lib():
                                         sz, vp], ctypes.c_int),
         ("fs_loss_workspace_bytes", [i32, i32], sz),
         ("fs_policy_loss", [vp, vp, vp, vp, vp, vp, i32, i32, i32, f64, f64, f64, f64, ctypes.c_int,
-                            ctypes.c_int, f64, vp, vp, vp, sz, vp], ctypes.c_int),
-        ("fs_preference_loss", [vp, vp, vp, vp, i32, i32, ctypes.c_int, f64, f64, f64, i32, f64, vp,
-                                vp, vp, vp, sz, vp], ctypes.c_int),
+                            ctypes.c_int, f64, i32, vp, vp, vp, sz, vp], ctypes.c_int),
+        ("fs_preference_loss", [vp, vp, vp, vp, i32, i32, ctypes.c_int, f64, f64, f64, i32, f64, i32,
+                                vp, vp, vp, vp, sz, vp], ctypes.c_int),
         ("fs_clip_grad_norm_workspace_bytes", [vp, i32], sz),
         ("fs_clip_grad_norm", [vp, vp, vp, vp, i32, ctypes.c_float, vp, vp, sz, vp], ctypes.c_int),
         ("fs_debug_noise", [u64, u64, u32, u32, i64, vp, vp, vp], ctypes.c_int),
@@ -622,6 +623,16 @@ def _nbytes(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
+def _apart(written, read):
+    """The given tensors that a call writes overlap neither one another nor one
+    that it reads."""
+    spans = [(t.data_ptr(), t.data_ptr() + _nbytes(t), i < len(written))
+             for i, t in enumerate((*written, *read)) if t is not None and t.numel()]
+    for i, (a, b, w) in enumerate(spans):
+        if w and any(a < d and c < b for c, d, _ in spans[i + 1:]):
+            raise ValueError("outputs and workspace must overlap neither each other nor an input")
+
+
 def _row(t: Optional[torch.Tensor], name: str, dtype, n: int, device):
     if t is None:
         return
@@ -670,6 +681,8 @@ def token_logprobs(h: torch.Tensor, W: torch.Tensor, temperature: Optional[torch
     lp = _out(lp, "logprob", (B,), torch.float32, dev)
     lse = _out(lse, "lse", (B,), torch.float32, dev)
     ws = _workspace(workspace, token_logprobs_workspace_bytes(B, D, V), dev)
+    if out is not None or workspace is not None:
+        _apart((lp, lse, ws), (h, W, temperature, token_ids))
     fn = lib().fs_token_logprobs_packed if packed else lib().fs_token_logprobs
     _call(fn, dev, _addr(h), _addr(W), B, D, V, int(vocab_offset), _addr(temperature),
           _addr(token_ids), _addr(lp), _addr(lse), _addr(ws), _nbytes(ws))
@@ -706,6 +719,8 @@ def token_logprobs_backward(h: torch.Tensor, W: torch.Tensor, temperature: Optio
     gh = _out(gh, "grad_h", (B, D), torch.bfloat16, dev) if need_h else None
     gw = _out(gw, "grad_W", (V, D), torch.bfloat16, dev) if need_W else None
     ws = _workspace(workspace, token_logprobs_backward_workspace_bytes(B, D, V), dev)
+    if out is not None or workspace is not None:
+        _apart((gh, gw, ws), (h, W, temperature, token_ids, logprob, lse, grad_logprob))
     _call(lib().fs_token_logprobs_backward, dev, _addr(h), _addr(W), B, D, V, int(vocab_offset),
           _addr(temperature), _addr(token_ids), _addr(logprob), _addr(lse), _addr(grad_logprob),
           _addr(gh), _addr(gw), _addr(ws), _nbytes(ws))
@@ -756,20 +771,23 @@ def policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages: to
     fp32 [tokens]); stats are the loss, the mean surrogate, the mean KL and
     the clipped share, grad is grad_scale * d loss / d logprob.  advantages
     holds one value per sequence, or with per_token one per token.  mask (bool
-    or uint8): the tokens that count.  With `out` = (stats, grad) the entries
-    of grad outside every sequence are left as they were."""
+    or uint8): the tokens that count.  Entries of grad before the first and
+    behind the last sequence are 0; in a grad given by `out` = (stats, grad)
+    they are left as they were."""
     dev, N, m = _sequences(logprob, cu_seqlens, mask, old_logprob=old_logprob,
                            ref_logprob=ref_logprob)
     S = cu_seqlens.shape[0] - 1
     _row(advantages, "advantages", torch.float32, N if per_token else S, dev)
-    stats, grad = (None, None) if out is None else out
+    stats, given = (None, None) if out is None else out
     stats = _out(stats, "stats", (4,), torch.float32, dev)
-    grad = _out(grad, "grad", (N,), torch.float32, dev)
+    grad = _out(given, "grad", (N,), torch.float32, dev)
     ws = _workspace(workspace, loss_workspace_bytes(S, N), dev)
+    if out is not None or workspace is not None:
+        _apart((stats, grad, ws), (logprob, old_logprob, ref_logprob, advantages, m, cu_seqlens))
     _call(lib().fs_policy_loss, dev, _addr(logprob), _addr(old_logprob), _addr(ref_logprob),
           _addr(advantages), _addr(m), _addr(cu_seqlens), S, N, int(per_token), clip_low, clip_high,
           dual_clip, kl_coef, _choice(_KL, kl, "kl"), _choice(_REDUCTIONS, reduction, "reduction"),
-          grad_scale, _addr(stats), _addr(grad), _addr(ws), _nbytes(ws))
+          grad_scale, int(given is None), _addr(stats), _addr(grad), _addr(ws), _nbytes(ws))
     return stats, grad
 
 
@@ -783,21 +801,24 @@ def preference_loss(logprob: torch.Tensor, cu_seqlens: torch.Tensor,
     then the rejected ones in the same order (cu_seqlens has 2 P + 1 entries):
     returns (stats fp32 [3], rewards fp32 [2 P], grad fp32 [tokens]); stats are
     the loss, the share of pairs that prefer the chosen answer and the mean
-    margin of rewards.  With `out` = (stats, rewards, grad) the entries of grad
-    outside every sequence are left as they were."""
+    margin of rewards.  Entries of grad before the first and behind the last
+    sequence are 0; in a grad given by `out` = (stats, rewards, grad) they are
+    left as they were."""
     dev, N, m = _sequences(logprob, cu_seqlens, mask, ref_logprob=ref_logprob)
     S = cu_seqlens.shape[0] - 1
     if S % 2:
         raise ValueError("cu_seqlens must describe chosen and rejected answers: 2 P + 1 entries")
-    stats, rewards, grad = (None, None, None) if out is None else out
+    stats, rewards, given = (None, None, None) if out is None else out
     stats = _out(stats, "stats", (3,), torch.float32, dev)
     rewards = _out(rewards, "rewards", (S,), torch.float32, dev)
-    grad = _out(grad, "grad", (N,), torch.float32, dev)
+    grad = _out(given, "grad", (N,), torch.float32, dev)
     ws = _workspace(workspace, loss_workspace_bytes(S, N), dev)
+    if out is not None or workspace is not None:
+        _apart((stats, rewards, grad, ws), (logprob, ref_logprob, m, cu_seqlens))
     _call(lib().fs_preference_loss, dev, _addr(logprob), _addr(ref_logprob), _addr(m),
           _addr(cu_seqlens), S // 2, N, _choice(_PREFERENCES, kind, "kind"), beta, margin,
-          label_smoothing, int(length_normalised), grad_scale, _addr(stats), _addr(rewards),
-          _addr(grad), _addr(ws), _nbytes(ws))
+          label_smoothing, int(length_normalised), grad_scale, int(given is None), _addr(stats),
+          _addr(rewards), _addr(grad), _addr(ws), _nbytes(ws))
     return stats, rewards, grad
 
 
@@ -834,13 +855,20 @@ def clip_grad_norm(grads, max_norm: float, out=None, norm: Optional[torch.Tensor
     count = [g.numel() for g in grads]
     src = [g.data_ptr() for g in grads]
     dst = src if out is None else [o.data_ptr() for o in outs]
-    # a tensor's bytes end before the next one's begin
+    # a written tensor's bytes end before the next one's begin ...
     ends = 0
-    for p, t, k in sorted(zip(dst, types, count)):
-        if k:
-            if p < ends:
-                raise ValueError("the tensors written must not overlap")
-            ends = p + (k << (1 + (t == 2)))
+    written = sorted(p for p in zip(dst, types, count) if p[2])
+    for p, t, k in written:
+        if p < ends:
+            raise ValueError("the tensors written must not overlap")
+        ends = p + (k << (1 + (t == 2)))
+    if out is not None:  # ... and touch no tensor read but their own
+        starts = [p for p, _, _ in written]
+        for p, q, t, k in zip(src, dst, types, count):
+            if k and p != q:
+                i = bisect.bisect_left(starts, p + (k << (1 + (t == 2)))) - 1
+                if i >= 0 and starts[i] + (written[i][2] << (1 + (written[i][1] == 2))) > p:
+                    raise ValueError("a tensor of out overlaps one of grads that is not its own")
     array = ctypes.c_void_p * n
     sizes = (ctypes.c_int64 * n)(*count)
     types = (ctypes.c_int * n)(*types)

@@ -47,6 +47,7 @@ struct SeqArgs {
   const uint8_t* mask;   // [T] or null
   int32_t S, T;
   int32_t parts;         // parts per sequence
+  int32_t zero_outside;  // gradients outside every sequence are set to 0
 };
 
 // Tokens [a, b) of part y of sequence s.  Offsets come from device memory, so
@@ -58,6 +59,17 @@ __device__ __forceinline__ void part_range(const SeqArgs& q, int s, int y, int& 
   const int64_t len = hi - lo;
   a = lo + static_cast<int>(len * y / q.parts);
   b = lo + static_cast<int>(len * (y + 1) / q.parts);
+}
+
+// Gradients before the first and behind the last sequence, this thread's share
+// of `threads`.
+__device__ __forceinline__ void outside(const SeqArgs& q, float* grad, int64_t thread,
+                                        int64_t threads) {
+  if (!q.zero_outside) return;
+  const int first = q.S > 0 ? min(max(q.cu[0], 0), q.T) : q.T;
+  const int end = q.S > 0 ? min(max(q.cu[q.S], first), q.T) : q.T;
+  for (int64_t t = thread; t < first; t += threads) grad[t] = 0.0f;
+  for (int64_t t = end + thread; t < q.T; t += threads) grad[t] = 0.0f;
 }
 
 __device__ __forceinline__ bool counts(const SeqArgs& q, int t) {
@@ -308,6 +320,8 @@ __global__ __launch_bounds__(kOneBlockThreads) void policy_totals_kernel(PolicyA
 
 template <int TEAM>
 __global__ __launch_bounds__(kThreads) void policy_kernel(PolicyArgs a) {
+  outside(a.q, a.grad, static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x,
+          static_cast<int64_t>(gridDim.x) * kThreads);
   const int2 totals = a.have_totals ? *a.totals : policy_totals<kThreads>(a);
   const int64_t item = item_of_thread<TEAM>();
   Sum4 v;
@@ -342,6 +356,7 @@ __global__ __launch_bounds__(kOneBlockThreads) void policy_stats_kernel(PolicyAr
 __global__ __launch_bounds__(kOneBlockThreads) void policy_one_block_kernel(PolicyArgs a) {
   __shared__ Sum4 part[kOneBlockItems];
   __shared__ float weight[kOneBlockSequences];
+  outside(a.q, a.grad, threadIdx.x, kOneBlockThreads);
   constexpr int kWaves = kOneBlockThreads / kWaveSize;
   const int wave = threadIdx.x / kWaveSize, lane = threadIdx.x % kWaveSize;
   const int Y = a.q.parts, S = a.q.S, items = S * Y;
@@ -529,6 +544,8 @@ __global__ __launch_bounds__(kOneBlockThreads) void preference_pairs_kernel(Pref
 // Gradients; the grid's last block takes the statistics.
 template <int TEAM>
 __global__ __launch_bounds__(kThreads) void preference_grad_kernel(PreferenceArgs a) {
+  outside(a.q, a.grad, static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x,
+          static_cast<int64_t>(gridDim.x) * kThreads);
   const int pairs = a.have_pairs ? *a.pairs : count_pairs<kThreads>(a, a.part);
   if (blockIdx.x == gridDim.x - 1) {
     preference_stats<kThreads>(a, a.part, pairs);
@@ -543,6 +560,7 @@ __global__ __launch_bounds__(kThreads) void preference_grad_kernel(PreferenceArg
 __global__ __launch_bounds__(kOneBlockThreads) void preference_one_block_kernel(PreferenceArgs a) {
   __shared__ Part part[kOneBlockItems];
   __shared__ float weight[kOneBlockSequences];
+  outside(a.q, a.grad, threadIdx.x, kOneBlockThreads);
   constexpr int kWaves = kOneBlockThreads / kWaveSize;
   const int wave = threadIdx.x / kWaveSize, lane = threadIdx.x % kWaveSize;
   const int Y = a.q.parts, items = a.q.S * Y;
@@ -695,9 +713,9 @@ FS_API fs_status fs_policy_loss(const float* logprob, const float* old_logprob,
                                 int32_t n_sequences, int32_t n_tokens,
                                 int32_t advantage_per_token, double clip_low, double clip_high,
                                 double dual_clip, double kl_coef, fs_kl_kind kl_kind,
-                                fs_loss_reduction reduction, double grad_scale, float* out_stats,
-                                float* out_grad, void* workspace, size_t workspace_bytes,
-                                void* stream) {
+                                fs_loss_reduction reduction, double grad_scale,
+                                int32_t zero_outside, float* out_stats, float* out_grad,
+                                void* workspace, size_t workspace_bytes, void* stream) {
   using namespace fs;
   const char* who = "fs_policy_loss";
   fs_status st = check_sequences(who, n_sequences, n_tokens, cu_seqlens);
@@ -734,7 +752,8 @@ FS_API fs_status fs_policy_loss(const float* logprob, const float* old_logprob,
   if (start_launches()) return injected_failure(who);
   char* ws = static_cast<char*>(workspace);
   PolicyArgs a;
-  a.q = {cu_seqlens, mask, n_sequences, n_tokens, loss_parts(n_sequences, n_tokens)};
+  a.q = {cu_seqlens, mask, n_sequences, n_tokens, loss_parts(n_sequences, n_tokens),
+         zero_outside != 0};
   a.lp = logprob;
   a.old = old_logprob;
   a.ref = ref_logprob;
@@ -764,9 +783,10 @@ FS_API fs_status fs_preference_loss(const float* logprob, const float* ref_logpr
                                     const uint8_t* mask, const int32_t* cu_seqlens,
                                     int32_t n_pairs, int32_t n_tokens, fs_preference_kind kind,
                                     double beta, double margin, double label_smoothing,
-                                    int32_t length_normalised, double grad_scale, float* out_stats,
-                                    float* out_rewards, float* out_grad, void* workspace,
-                                    size_t workspace_bytes, void* stream) {
+                                    int32_t length_normalised, double grad_scale,
+                                    int32_t zero_outside, float* out_stats, float* out_rewards,
+                                    float* out_grad, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
   using namespace fs;
   const char* who = "fs_preference_loss";
   if (n_pairs < 0 || n_pairs > kMaxSequences / 2)
@@ -802,7 +822,8 @@ FS_API fs_status fs_preference_loss(const float* logprob, const float* ref_logpr
   if (start_launches()) return injected_failure(who);
   char* ws = static_cast<char*>(workspace);
   PreferenceArgs a;
-  a.q = {cu_seqlens, mask, 2 * n_pairs, n_tokens, loss_parts(2 * n_pairs, n_tokens)};
+  a.q = {cu_seqlens, mask, 2 * n_pairs, n_tokens, loss_parts(2 * n_pairs, n_tokens),
+         zero_outside != 0};
   a.lp = logprob;
   a.ref = ref_logprob;
   a.kind = kind;

@@ -59,18 +59,18 @@ static void losses(fs_status valid) {
       const int32_t S = Ss[a], T = Ts[b];
       const size_t need = fs_loss_workspace_bytes(S, T);
       EXPECT(fs_policy_loss(F, F, F, F, M, I, S, T, 1, 0.2, 0.2, 3.0, 0.1, FS_KL_K3, FS_TOKEN_MEAN,
-                            1.0, F, F, WS, need, NULL) == valid);
+                            1.0, 0, F, F, WS, need, NULL) == valid);
       if (S % 2 == 0)
         EXPECT(fs_preference_loss(F, F, M, I, S / 2, T, FS_PREFERENCE_SIGMOID, 0.1, 0.0, 0.1, 1, 1.0,
-                                  F, F, F, WS, need, NULL) == valid);
+                                  1, F, F, F, WS, need, NULL) == valid);
       if (need > 0)
         EXPECT(fs_policy_loss(F, F, NULL, F, NULL, I, S, T, 0, 0.2, 0.2, 0.0, 0.0, FS_KL_K1,
-                              FS_SEQUENCE_MEAN, 1.0, F, F, WS, need - 1, NULL) == FS_ERR_WORKSPACE);
+                              FS_SEQUENCE_MEAN, 1.0, 0, F, F, WS, need - 1, NULL) == FS_ERR_WORKSPACE);
     }
   EXPECT(fs_policy_loss(F, F, F, F, M, I, 4, 9000, 0, NAN, 0.2, 0.0, 0.1, FS_KL_K3, FS_TOKEN_MEAN, 1.0,
-                        F, F, WS, BIG, NULL) == FS_ERR_INVALID_ARG);
-  EXPECT(fs_preference_loss(F, F, M, I, 4, 9000, FS_PREFERENCE_IPO, 0.1, 1.0, 0.0, 0, 1.0, F, F, F, WS,
-                            BIG, NULL) == FS_ERR_INVALID_ARG);
+                        0, F, F, WS, BIG, NULL) == FS_ERR_INVALID_ARG);
+  EXPECT(fs_preference_loss(F, F, M, I, 4, 9000, FS_PREFERENCE_IPO, 0.1, 1.0, 0.0, 0, 1.0, 0, F, F, F,
+                            WS, BIG, NULL) == FS_ERR_INVALID_ARG);
 }
 
 static void clipping(fs_status valid) {

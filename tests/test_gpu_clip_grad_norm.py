@@ -96,6 +96,17 @@ def test_norm_that_is_not_finite_scales_nothing(bad):
     assert torch.equal(dev[0].cpu(), grads[0])
 
 
+def test_more_elements_than_32_bits_count():
+    n = (1 << 31) + 12345
+    x = torch.full((n,), 2.0 ** -10, dtype=torch.bfloat16, device="cuda")
+    x[-1] = 1.0
+    want = math.sqrt((n - 1) * 2.0 ** -20 + 1.0)
+    norm = fs.clip_grad_norm([x], want / 2)
+    assert abs(float(norm) / want - 1) <= 2.0 ** -23
+    # times 1/2 exactly but for the 1e-6 in the divisor: below half a step
+    assert float(x[-1]) == 0.5 and float(x[n // 2]) == 2.0 ** -11 and float(x[(1 << 31) - 1]) == 2.0 ** -11
+
+
 def test_zero_gradients_and_zero_limit():
     z = [torch.zeros(1000).cuda()]
     assert float(fs.clip_grad_norm(z, 1.0)) == 0.0 and not z[0].any()
@@ -142,6 +153,11 @@ def test_refusals():
     base = torch.ones(10).cuda()
     with pytest.raises(ValueError):
         fs.clip_grad_norm([base[:6], base[4:]], 1.0)
+    with pytest.raises(ValueError):
+        fs.clip_grad_norm([a, b], 1.0, out=[b, torch.empty_like(b)])   # out[0] is grads[1]
+    with pytest.raises(ValueError):
+        fs.clip_grad_norm([base[:4], base[6:]], 1.0, out=[base[3:7], torch.empty(4).cuda()])
+    fs.clip_grad_norm([a, a], 9.0, out=[torch.empty_like(a), torch.empty_like(a)])  # read twice: fine
     with pytest.raises(ValueError):
         fs.clip_grad_norm([a, b], 1.0, out=[a])
     with pytest.raises(ValueError):

@@ -123,6 +123,36 @@ def test_policy_masked_tokens_may_hold_anything():
     assert torch.allclose(grad.cpu().double()[:end], want[1][:end], rtol=1e-5, atol=1e-9)
 
 
+@pytest.mark.parametrize("lens", [[30, 0, 11, 8], [3000, 900, 5, 2000]])
+def test_padded_batch(lens):
+    """Tokens before the first and behind the last sequence: gradient 0 in a new
+    tensor, left alone in a given one; their entries are not read."""
+    g, cu, N, lp, old, refp, _ = batch(lens)
+    front, back = 7, 300
+    pad = lambda x: torch.cat([torch.full((front,), math.nan), x, torch.full((back,), math.nan)])
+    adv = torch.randn(len(lens), generator=g)
+    want = fs.policy_loss(*cuda(lp, old, adv, cu), ref_logprob=refp.cuda(), kl_coef=0.1)
+    wantp = fs.preference_loss(*cuda(lp, cu), ref_logprob=refp.cuda())
+    a = cuda(pad(lp), pad(old), adv, cu + front, pad(refp))
+    stats, grad = fs.policy_loss(*a[:4], ref_logprob=a[4], kl_coef=0.1)
+    _, rewards, gradp = fs.preference_loss(a[0], a[3], ref_logprob=a[4])
+    assert torch.allclose(stats, want[0], rtol=1e-6) and torch.allclose(rewards, wantp[1], rtol=1e-6)
+    for x, w in ((grad, want[1]), (gradp, wantp[2])):
+        assert torch.allclose(x[front:front + N], w, rtol=1e-6)
+        assert not x[:front].any() and not x[front + N:].any()
+    # a grad of the call's own beside given statistics
+    torch.full((front + N + back,), 3.0).cuda()  # (what a new tensor may find)
+    grad = fs.policy_loss(*a[:4], ref_logprob=a[4], out=(torch.empty(4).cuda(), None))[1]
+    assert not grad[:front].any() and not grad[front + N:].any()
+    mine = torch.full((front + N + back,), 5.0).cuda()
+    fs.policy_loss(*a[:4], ref_logprob=a[4], out=(torch.empty(4).cuda(), mine))
+    assert (mine[:front] == 5).all() and (mine[front + N:] == 5).all()
+    mine.fill_(5.0)
+    fs.preference_loss(a[0], a[3], ref_logprob=a[4],
+                       out=(torch.empty(3).cuda(), torch.empty(len(lens)).cuda(), mine))
+    assert (mine[:front] == 5).all() and (mine[front + N:] == 5).all()
+
+
 @pytest.mark.parametrize("lens", [[3, 5], [5000, 40]])
 def test_nothing_counts(lens):
     g, cu, N, lp, old, refp, mask = batch(lens)
@@ -144,6 +174,7 @@ def test_no_sequences():
     x = torch.ones(9000).cuda()
     stats, grad = fs.policy_loss(x, x, e, cu, out=(torch.ones(4).cuda(), x.clone()))
     assert not stats.any() and (grad == 1).all()
+    assert not fs.policy_loss(x, x, e, cu)[1].any()
 
 
 PREFS = [[1, 1], [4, 0, 3, 7], [64, 65, 130, 1], [300] * 12, [2100, 2000], [513] * 8, [9000, 3],
@@ -257,6 +288,14 @@ def test_refusals():
         fs.policy_loss(lp, old, adv, cu.long())
     with pytest.raises(fs.FlashSampleError):
         fs.policy_loss(lp, old, adv, cu, clip_low=1.5)
+    with pytest.raises(ValueError):
+        fs.policy_loss(lp, old, adv, cu, out=(None, lp))        # in place
+    both = torch.zeros(N + 2).cuda()
+    with pytest.raises(ValueError):
+        fs.policy_loss(lp, old, adv, cu, out=(both[N - 2:], both[:N]))
+    with pytest.raises(ValueError):
+        fs.preference_loss(lp, cu, old, out=(None, None, old))
+    fs.policy_loss(lp, lp, adv, cu, out=(both[-1:].new_empty(4), both[:N]))   # an input twice: fine
     with pytest.raises(ValueError):
         fs.preference_loss(lp, cu[:2])
     with pytest.raises(ValueError):

@@ -292,6 +292,43 @@ def test_equal_calls_give_equal_bits_and_outputs_can_be_given():
     assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
 
 
+@pytest.mark.parametrize("B", [3, 40])
+def test_head_beyond_32_bit_offsets(B):
+    """W of 2.5e9 elements (4.9 GB): the rows past 2^31 elements are read, and
+    their gradients written, where they are."""
+    D, V = 8192, 300000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    W = torch.empty(V, D, dtype=torch.bfloat16, device="cuda")
+    for r in range(0, V, 50000):
+        W[r:r + 50000] = torch.randn(50000, D, generator=g, device="cuda") * (1.5 / math.sqrt(D))
+    h = torch.randn(B, D, generator=g, device="cuda").to(torch.bfloat16)
+    ids = torch.tensor([V - 1, 7, V - 300] * B, dtype=torch.int32, device="cuda")[:B]
+    lp, lse = fs.token_logprobs(h, W, None, ids)
+    z = torch.cat([h.double() @ W[r:r + 50000].double().t() for r in range(0, V, 50000)], dim=1)
+    # logits of size 1.5, |h . W| about 1.5: the tolerance of logit_tolerance, four deviations
+    e = 4 * 2.0 ** -24 * math.sqrt(D) * 2.0 + 2.0 ** -23 * float(z.abs().max())
+    want = torch.logsumexp(z, dim=1)
+    zt = z.gather(1, ids.long()[:, None])[:, 0]
+    assert ((lse.double() - want).abs() <= e + 2.0 ** -22 * want).all()
+    assert ((lp.double() - (zt - want)).abs() <= 2 * e + 2.0 ** -21 * want).all()
+    grad = torch.linspace(-1, 1, B, device="cuda")
+    gh, gw = fs.token_logprobs_backward(h, W, None, ids, lp, lse, grad)
+    dz = -torch.exp(z - lse.double()[:, None])
+    dz[torch.arange(B), ids.long()] = -torch.expm1(lp.double())
+    dz = dz * grad.double()[:, None]
+    for rows in (slice(V - 400, V), slice(0, 50), slice(262100, 262200)):
+        w = dz[:, rows].t() @ h.double()
+        bound = dz[:, rows].abs().t() @ h.double().abs()
+        tol = bound * (2.0 ** -8 + 4 * e + 2.0 ** -18) + 2.0 ** -8 * w.abs()
+        assert ((gw[rows].double() - w).abs() <= tol).all()
+    w, bound = torch.zeros_like(h, dtype=torch.float64), torch.zeros_like(h, dtype=torch.float64)
+    for r in range(0, V, 50000):
+        W64 = W[r:r + 50000].double()
+        w += dz[:, r:r + 50000] @ W64
+        bound += dz[:, r:r + 50000].abs() @ W64.abs()
+    assert ((gh.double() - w).abs() <= bound * (2.0 ** -8 + 4 * e + 2.0 ** -18) + 2.0 ** -8 * w.abs()).all()
+
+
 def test_two_streams_at_once():
     h, W, T, ids = make(70, 256, 3000, seed=15)
     hd, Wd, Td, idd = dev(h, W, T, ids)
@@ -361,6 +398,16 @@ def test_refusals():
     with pytest.raises(fs.FlashSampleError):
         fs.token_logprobs(h, W, T, ids, workspace=torch.empty(64, dtype=torch.uint8).cuda())
     z = torch.zeros(4).cuda()
+    with pytest.raises(ValueError):
+        fs.token_logprobs(h, W, T, ids, out=(z, z))
+    with pytest.raises(ValueError):
+        fs.token_logprobs(h, W, T, ids, out=(T, z))
+    with pytest.raises(ValueError):
+        fs.token_logprobs(h, W, T, ids, workspace=W)
+    with pytest.raises(ValueError):
+        fs.token_logprobs_backward(h, W, T, ids, z, z, z, out=(h, None))
+    with pytest.raises(ValueError):
+        fs.token_logprobs_backward(h, W, T, ids, z, z, z, out=(None, W))
     with pytest.raises(fs.FlashSampleError):
         fs.token_logprobs_backward(h, W, T, ids, z, z, z, need_h=False, need_W=False)
     with pytest.raises(ValueError):

@@ -30,13 +30,13 @@ def _backward(L, h=A, W=A, B=4, D=256, V=1000, off=0, T=A, ids=A, lp=A, lse=A, g
 
 def _policy(L, lp=A, old=A, ref=A, adv=A, mask=A, cu=A, S=4, N=9000, per=0, lo=0.2, hi=0.2, dual=0.0,
             kc=0.1, kl=3, red=0, scale=1.0, stats=A, grad=A, ws=WS, wsb=BIG):
-    return L.fs_policy_loss(lp, old, ref, adv, mask, cu, S, N, per, lo, hi, dual, kc, kl, red, scale,
+    return L.fs_policy_loss(lp, old, ref, adv, mask, cu, S, N, per, lo, hi, dual, kc, kl, red, scale, 0,
                             stats, grad, ws, wsb, None)
 
 
 def _preference(L, lp=A, ref=A, mask=A, cu=A, P=2, N=9000, kind=0, beta=0.1, margin=0.0, eps=0.0,
                 norm=0, scale=1.0, stats=A, rewards=A, grad=A, ws=WS, wsb=BIG):
-    return L.fs_preference_loss(lp, ref, mask, cu, P, N, kind, beta, margin, eps, norm, scale, stats,
+    return L.fs_preference_loss(lp, ref, mask, cu, P, N, kind, beta, margin, eps, norm, scale, 1, stats,
                                 rewards, grad, ws, wsb, None)
 
 
