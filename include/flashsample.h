@@ -352,7 +352,7 @@ FS_API fs_status fs_sample_unfused(const void* h, const void* W, int32_t B, int3
 /* Log-probabilities of given tokens under softmax(z_b / T_b), z_b = W h_b, with
  * no logits in memory.
  *   h, W, B, D, V, vocab_offset  as fs_sample (D up to 2^20, B up to 2^24,
- *                FS_ERR_UNSUPPORTED beyond); the _packed form reads W in
+ *                V up to 2^31 - 513, FS_ERR_UNSUPPORTED beyond); the _packed form reads W in
  *                fragment order (fs_pack_weights, D % 32 == 0)
  *   temperature  fp32 [B], device, or NULL (all 1).  As in the samplers the
  *                logits are scaled by fp32(1/T), and a row whose temperature

@@ -329,9 +329,9 @@ fs_status check_score_shape(const char* who, int32_t B, int32_t D, int32_t V,
   if (vocab_offset < 0 || static_cast<int64_t>(vocab_offset) + V > 2147483647)
     return fail(FS_ERR_INVALID_ARG, "%s: vocab_offset and vocab_offset + V must be in [0, 2^31 - 1]"
                 " (got %d, V = %d)", who, vocab_offset, V);
-  if (B > kMaxScoreB || D > kMaxScoreD)
-    return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, D=%d exceed the %d rows or %d elements a call can "
-                "take", who, B, D, kMaxScoreB, kMaxScoreD);
+  if (B > kMaxScoreB || D > kMaxScoreD || V > kMaxVocab)
+    return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, D=%d, V=%d exceed the %d rows, %d elements or %d "
+                "entries a call can take", who, B, D, V, kMaxScoreB, kMaxScoreD, kMaxVocab);
   if (grid_tiles(B, tile_count(B, V), 64) > 0x7FFFFFFF)
     return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, V=%d exceed the launch grid", who, B, V);
   return FS_OK;
@@ -404,7 +404,9 @@ fs_status run_score(const char* who, const void* h, const void* W, int32_t B, in
 extern "C" {
 
 FS_API size_t fs_token_logprobs_workspace_bytes(int32_t B, int32_t D, int32_t V) {
-  if (B < 0 || D < 8 || D % 8 != 0 || V < 1 || B > fs::kMaxScoreB || D > fs::kMaxScoreD) return 0;
+  if (B < 0 || D < 8 || D % 8 != 0 || V < 1 || B > fs::kMaxScoreB || D > fs::kMaxScoreD ||
+      V > fs::kMaxVocab)
+    return 0;
   return fs::ScoreLayout(B, D, V).total;
 }
 

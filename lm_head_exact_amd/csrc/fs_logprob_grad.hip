@@ -648,7 +648,8 @@ hipError_t run_grad(GradArgs& a, const GradPlan& p, hipStream_t s) {
 }
 
 bool grad_sizes_ok(int32_t B, int32_t D, int32_t V) {
-  return B >= 0 && D >= 8 && D % 8 == 0 && V >= 1 && B <= kMaxGradB && D <= kMaxGradD;
+  return B >= 0 && D >= 8 && D % 8 == 0 && V >= 1 && B <= kMaxGradB && D <= kMaxGradD &&
+         V <= kMaxVocab;
 }
 
 }  // namespace
@@ -677,8 +678,8 @@ FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_
     return fail(FS_ERR_INVALID_ARG, "%s: vocab_offset and vocab_offset + V must be in [0, 2^31 - 1]"
                 " (got %d, V = %d)", who, vocab_offset, V);
   if (!grad_sizes_ok(B, D, V))
-    return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, D=%d exceed the %d rows or %d elements a call can "
-                "take", who, B, D, kMaxGradB, kMaxGradD);
+    return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, D=%d, V=%d exceed the %d rows, %d elements or %d "
+                "entries a call can take", who, B, D, V, kMaxGradB, kMaxGradD, kMaxVocab);
   if (!grad_h && !grad_W)
     return fail(FS_ERR_INVALID_ARG, "%s: neither grad_h nor grad_W is asked for", who);
   if (!grad_W && B == 0) return FS_OK;

@@ -17,6 +17,9 @@
 
 namespace fs {
 
+// Most rows of W in a call: row numbers a tile past the last stay below 2^31.
+constexpr int32_t kMaxVocab = 0x7FFFFFFF - 512;
+
 struct ScoreArgs {
   Operand w, h;             // W [V][D] (or fragment order), h [B][D]
   int32_t B, D, V, vocab_offset, shift;  // shift: rows before row 0 in the grid (fragment order)

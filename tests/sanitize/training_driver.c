@@ -29,7 +29,7 @@ static int failures = 0;
 
 static void logprobs(fs_status valid) {
   const int32_t Bs[] = {0, 1, 16, 17, 33, 300, 1 << 24}, Ds[] = {8, 40, 256, 4096, 8192, 1 << 20};
-  const int32_t Vs[] = {1, 15, 1000, 128256, 2147483647};
+  const int32_t Vs[] = {1, 15, 1000, 128256, 2147483135};
   for (size_t b = 0; b < sizeof Bs / sizeof *Bs; ++b)
     for (size_t d = 0; d < sizeof Ds / sizeof *Ds; ++d)
       for (size_t v = 0; v < sizeof Vs / sizeof *Vs; ++v) {
@@ -47,6 +47,9 @@ static void logprobs(fs_status valid) {
         s = fs_token_logprobs_backward(P, P, B, D, V, 0, F, I, F, F, F, P, P, WS, BIG, NULL);
         EXPECT(s == valid || s == FS_ERR_UNSUPPORTED);
       }
+  EXPECT(fs_token_logprobs_workspace_bytes(1, 8, 2147483647) == 0);
+  EXPECT(fs_token_logprobs_backward_workspace_bytes(1, 8, 2147483647) == 0);
+  EXPECT(fs_token_logprobs(P, P, 1, 8, 2147483647, 0, F, I, F, F, WS, BIG, NULL) == FS_ERR_UNSUPPORTED);
   EXPECT(fs_token_logprobs(NULL, P, 1, 8, 1, 0, F, I, F, F, WS, BIG, NULL) == FS_ERR_INVALID_ARG);
   EXPECT(fs_token_logprobs_backward(P, P, 1, 8, 1, 0, F, I, F, F, F, NULL, NULL, WS, BIG, NULL) ==
          FS_ERR_INVALID_ARG);

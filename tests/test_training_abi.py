@@ -72,6 +72,7 @@ def _clip(L, grads=(A, A), out=None, numel=(100, 200), dtypes=(0, 2), n=2, max_n
     (dict(B=(1 << 24) + 1), bd.FS_ERR_UNSUPPORTED),
     (dict(D=(1 << 20) + 32), bd.FS_ERR_UNSUPPORTED),
     (dict(B=1 << 24, V=2**31 - 1), bd.FS_ERR_UNSUPPORTED),
+    (dict(V=2**31 - 512), bd.FS_ERR_UNSUPPORTED),
     (dict(B=0, h=None, W=None, T=None, ids=None, lp=None, lse=None, ws=None), bd.FS_OK),
 ])
 def test_logprobs_argument_errors(L, fn, kw, status):
@@ -125,6 +126,7 @@ def test_backward_workspace_stays_bounded(L):
     (dict(wsb=8), bd.FS_ERR_WORKSPACE),
     (dict(B=(1 << 22) + 1), bd.FS_ERR_UNSUPPORTED),
     (dict(D=(1 << 20) + 8), bd.FS_ERR_UNSUPPORTED),
+    (dict(V=2**31 - 512), bd.FS_ERR_UNSUPPORTED),
     (dict(B=0, gw=None, h=None, W=None, ws=None), bd.FS_OK),
 ])
 def test_backward_argument_errors(L, kw, status):
