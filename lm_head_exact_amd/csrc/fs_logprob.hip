@@ -278,9 +278,16 @@ hipError_t launch_stream(ScoreArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Streaming where the waves' slices of h fit in registers.
+// Streaming where the waves' slices of h fit in registers: fewer instructions
+// and no barrier per k tile (16 rows on 128256 x 4096: 180 us streaming, 201 by
+// tiles; fragment order 157 and 170; 32 rows 175 and 203, 161 and 170).
 bool streams(int32_t B, int32_t D) { return (B <= 16 && D <= 8192) || (B <= 32 && D <= 5120); }
 
+// Waves per block, k-steps per wave and loads ahead, by row length.  Row-major
+// rows gain from loads of a whole group ahead (128256 x 4096, 16 rows: 16 ahead
+// 180 us, 8 ahead 187; 151936 x 5120: 10 ahead by sixteen waves 270, 4 ahead by
+// eight 283), fragment order, whose groups are contiguous, from more waves
+// (128256 x 4096, 32 rows: sixteen 161, eight 169; one row 155 and 159).
 template <bool PACKED>
 hipError_t launch_score_stream(ScoreArgs& a, hipStream_t stream) {
   const int32_t B = a.B, D = a.D;
@@ -289,15 +296,21 @@ hipError_t launch_score_stream(ScoreArgs& a, hipStream_t stream) {
     if (D <= 2048) return launch_stream<1, 8, 8, 8, PACKED>(a, stream);
     if (D <= 4096) {
       if constexpr (PACKED) return launch_stream<1, 16, 8, 4, PACKED>(a, stream);
-      else return launch_stream<1, 8, 16, 8, PACKED>(a, stream);
+      else return launch_stream<1, 8, 16, 16, PACKED>(a, stream);
     }
-    if (D <= 5120) return launch_stream<1, 8, 20, 4, PACKED>(a, stream);
+    if (D <= 5120) {
+      if constexpr (PACKED) return launch_stream<1, 8, 20, 4, PACKED>(a, stream);
+      else return launch_stream<1, 16, 10, 10, PACKED>(a, stream);
+    }
     if (D <= 6144) return launch_stream<1, 8, 24, 8, PACKED>(a, stream);
     return launch_stream<1, 8, 32, 8, PACKED>(a, stream);
   }
   if (D <= 1024) return launch_stream<2, 8, 4, 4, PACKED>(a, stream);
   if (D <= 2048) return launch_stream<2, 8, 8, 8, PACKED>(a, stream);
-  if (D <= 4096) return launch_stream<2, 8, 16, PACKED ? 4 : 8, PACKED>(a, stream);
+  if (D <= 4096) {
+    if constexpr (PACKED) return launch_stream<2, 16, 8, 4, PACKED>(a, stream);
+    else return launch_stream<2, 8, 16, 8, PACKED>(a, stream);
+  }
   return launch_stream<2, 8, 20, 4, PACKED>(a, stream);
 }
 
@@ -390,6 +403,8 @@ fs_status run_score(const char* who, const void* h, const void* W, int32_t B, in
     e = packed ? launch_tiles<kFrag>(a, s) : launch_tiles<kKC>(a, s);
   }
   if (e != hipSuccess) return hip_fail(e, "log-probability launch");
+  // wide rows of the partials for many tokens (8192 tokens on 32000 rows of 256:
+  // the call 205 us, 210 by eight), many threads per token for few
   if (B >= 2048)
     score_close_kernel<64><<<(B + 63) / 64, kCloseThreads, 0, s>>>(a, logprob, lse);
   else

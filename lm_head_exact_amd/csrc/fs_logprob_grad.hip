@@ -640,7 +640,10 @@ hipError_t run_grad(GradArgs& a, const GradPlan& p, hipStream_t s) {
   }
   if (a.dh != nullptr && p.slabs) {
     const dim3 grid(a.B, (a.D + 4 * kWave - 1) / (4 * kWave));
-    if (p.splits > 16) grad_slabs_kernel<16><<<grid, 16 * kWave, 0, s>>>(a);
+    // few blocks share out the slabs (4 rows of 1024: the call's dh 35.0 us by
+    // sixteen groups, 39.3 by one), many need not (300 rows of 4096: 256, 243)
+    if (static_cast<int64_t>(grid.x) * grid.y <= 512)
+      grad_slabs_kernel<16><<<grid, 16 * kWave, 0, s>>>(a);
     else grad_slabs_kernel<1><<<grid, kWave, 0, s>>>(a);
     e = hipGetLastError();
   }

@@ -28,18 +28,27 @@ constexpr int kOneBlockThreads = 1024;
 // Token loads in flight per thread.
 constexpr int kAhead = 4;
 
-// The batches one block handles by itself: about what it reads in the time of
-// a further launch.
+// The batches one block handles by itself: what it takes longer than the passes
+// over the device is below the two launches (2 to 3 us each on the host) that
+// it saves.  Policy, preference on the device: 8 sequences of 500 tokens 11.5
+// and 9.4 us against 14.9 and 8.3; 4 of 2000, 14.5 and 11.7 against 12.5 and
+// 8.0; 128 of 32, 28.7 and 23.0 against 11.2 and 6.9.
 constexpr int32_t kOneBlockTokens = 4096;
-constexpr int32_t kOneBlockSequences = 256;
-constexpr int32_t kOneBlockItems = 512;
+constexpr int32_t kOneBlockSequences = 32;
+// their parts: sequences with several have kOneBlockThreads / 64 or a few more
+constexpr int32_t kOneBlockItems = kOneBlockSequences + kOneBlockThreads / kWaveSize;
 // Parts whose sums every block of the second pass adds up by itself; beyond
-// them one block does between the passes.
+// them one block does between the passes, in a launch of its own (2048 parts:
+// 14.4 us within the blocks, 14.5 between them; 4096: 18.0 and 16.7, which a
+// call's host side hides; 8192: 30.9 and 21.0).
 constexpr int64_t kInBlockItems = 4096;
-// The sequences' mean length from which a part takes a block, not a wave.
+// A part takes a block where the parts are few and their mean length is at
+// least this, else a wave: 512 sequences of 1024 tokens 14.9 us by blocks, 20.9
+// by waves; of 256, 12.7 and 13.4; of 64, 12.3 and 11.6.  Many parts fill the
+// device by waves: 2048 of 512 tokens 23.4 us by blocks, 18.9 by waves.
 constexpr int64_t kBlockTeamTokens = 512;
-// Tokens per part of long sequences, and the most parts of one.
-constexpr int64_t kPartTokens = 4096;
+constexpr int64_t kBlockTeamItems = 2048;
+// The most parts of a sequence.
 constexpr int32_t kMaxParts = 256;
 
 struct SeqArgs {
@@ -306,6 +315,7 @@ __device__ __forceinline__ int2 policy_totals(const PolicyArgs& a) {
   int tokens = 0, filled = 0;
   for (int s = threadIdx.x; s < a.q.S; s += THREADS) {
     int n = 0;
+#pragma unroll 8
     for (int y = 0; y < a.q.parts; ++y) n += a.count[static_cast<size_t>(s) * a.q.parts + y];
     tokens += n;
     filled += n > 0;
@@ -329,6 +339,7 @@ __global__ __launch_bounds__(kThreads) void policy_kernel(PolicyArgs a) {
   if (item < static_cast<int64_t>(a.q.S) * a.q.parts) {
     const int s = static_cast<int>(item / a.q.parts), y = static_cast<int>(item % a.q.parts);
     int n = 0;
+#pragma unroll 8
     for (int i = 0; i < a.q.parts; ++i) n += a.count[static_cast<size_t>(s) * a.q.parts + i];
     const double w = policy_weight(a, totals, n);
     v = policy_part(a, s, y, static_cast<float>(w * a.grad_scale), threadIdx.x % TEAM, TEAM);
@@ -437,10 +448,22 @@ __device__ __forceinline__ Sum4 preference_part(const PreferenceArgs& a, int s, 
 // One answer: S and its tokens.
 __device__ __forceinline__ Part answer(const PreferenceArgs& a, const Part* part, int s) {
   Part r = {0.0, 0};
-  for (int y = 0; y < a.q.parts; ++y) {
-    const Part p = part[static_cast<size_t>(s) * a.q.parts + y];
-    r.x += p.x;
-    r.n += p.n;
+  part += static_cast<size_t>(s) * a.q.parts;
+  if (a.q.parts == 1) {
+    r = part[0];
+  } else {
+    constexpr int kLoads = 16;  // in flight
+    for (int y0 = 0; y0 < a.q.parts; y0 += kLoads) {
+      Part p[kLoads];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) p[u] = part[min(y0 + u, a.q.parts - 1)];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u)
+        if (y0 + u < a.q.parts) {
+          r.x += p[u].x;
+          r.n += p[u].n;
+        }
+    }
   }
   if (a.normalise && r.n > 0) r.x /= r.n;
   return r;
@@ -594,11 +617,9 @@ int32_t loss_parts(int64_t S, int64_t T) {
     const int64_t waves = (kOneBlockThreads / kWaveSize + S - 1) / S, by = (T / S + 63) / 64;
     return static_cast<int32_t>(waves < by ? waves : by < 1 ? 1 : by);
   }
-  const int64_t by_len = (T / S + kPartTokens - 1) / kPartTokens;
   const int64_t by_grid = (512 + S - 1) / S;
   const int64_t fill = (T / S + 511) / 512;  // no parts below 512 tokens
-  int64_t p = by_len > by_grid ? by_len : by_grid;
-  p = p < fill ? p : fill;
+  const int64_t p = by_grid < fill ? by_grid : fill;
   return static_cast<int32_t>(p < 1 ? 1 : p > kMaxParts ? kMaxParts : p);
 }
 
@@ -623,7 +644,8 @@ struct LossGrid {
   unsigned blocks;
   explicit LossGrid(const SeqArgs& q) {
     items = static_cast<int64_t>(q.S) * q.parts;
-    wide = q.T / q.S >= kBlockTeamTokens;
+    // (parts of a sequence have kBlockTeamTokens or so)
+    wide = items < kBlockTeamItems && q.T / q.S >= kBlockTeamTokens;
     constexpr int per = kThreads / kWaveSize;
     blocks = static_cast<unsigned>(wide ? items : (items + per - 1) / per);
   }
