@@ -69,6 +69,18 @@ def test_policy(lens, reduction, per_token):
     check_policy(lens, per_token=per_token, reduction=reduction, clip_high=0.28, kl_coef=0.1)
 
 
+# more sequences than a block sums by itself, blocks and waves per sequence,
+# sequences of many parts, batches around one block's
+MANY = [[3] * 5000, [0, 9, 1, 0] * 1300, [700] * 600, [520] * 2100, [200000, 3], [150000, 0],
+        [128] * 32, [120] * 34, [16] * 256, [9000] * 30]
+
+
+@pytest.mark.parametrize("lens", MANY, ids=lambda x: f"{len(x)}x{x[0]}")
+@pytest.mark.parametrize("reduction", ["token", "sequence"])
+def test_policy_many(lens, reduction):
+    check_policy(lens, per_token=True, reduction=reduction, clip_high=0.28, kl_coef=0.1)
+
+
 @pytest.mark.parametrize("kl", ["k1", "k2", "k3"])
 @pytest.mark.parametrize("dual", [0.0, 1.5])
 @pytest.mark.parametrize("lens", [[40, 9], [6000, 31]])
@@ -197,6 +209,12 @@ def test_preference(lens, kind, kw, normalise):
     for x, w in zip((stats, rewards, grad), want):
         err = (x.cpu().double() - w).abs()
         assert (err <= 2 * U * w.abs() + 1e-10).all(), (kind, err.max())
+
+
+@pytest.mark.parametrize("lens", MANY, ids=lambda x: f"{len(x)}x{x[0]}")
+@pytest.mark.parametrize("normalise", [False, True])
+def test_preference_many(lens, normalise):
+    test_preference(lens, "sigmoid", {}, normalise)
 
 
 def test_preference_without_reference_or_mask():

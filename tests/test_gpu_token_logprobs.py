@@ -108,6 +108,35 @@ def test_backward(B, D, V, off):
     check_backward(*backward_case(h, W, T, ids, off))
 
 
+@pytest.mark.parametrize("D", [1024, 1056, 2048, 2080, 4096, 4128, 5120, 5152, 6144, 6176, 8192])
+@pytest.mark.parametrize("B", [1, 16, 17, 32])
+def test_forward_streams_every_row_length(B, D):
+    """Each slice length of the streaming kernels, whole and ragged, both layouts."""
+    h, W, T, ids = make(B, D, 333, 6, seed=18)
+    hd, Wd, Td, idd = dev(h, W, T, ids)
+    check_forward(h, W, T, ids, 6, fs.token_logprobs(hd, Wd, Td, idd, vocab_offset=6))
+    Wp = fs.pack_weights(Wd, 6)
+    check_forward(h, W, T, ids, 6, fs.token_logprobs(hd, Wp, Td, idd, vocab_offset=6, V=333))
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_shapes(seed):
+    g = torch.Generator().manual_seed(500 + seed)
+    size = lambda lo, hi: int(round(math.exp(math.log(lo) + float(torch.rand(1, generator=g)) * math.log(hi / lo))))
+    B, D, V = size(1, 900), 8 * size(1, 160), size(1, 3000)
+    off = size(1, 2000) if seed % 3 else 0
+    h, W, T, ids = make(B, D, V, off, seed=seed, ignore=(0.0, 0.3, 0.8)[seed % 3])
+    check_forward(h, W, T, ids, off, fs.token_logprobs(*dev(h, W, T, ids), vocab_offset=off))
+    check_backward(*backward_case(h, W, T, ids, off))
+
+
+@pytest.mark.parametrize("B,D,V", [(5, 64, 9), (300, 136, 700), (700, 264, 1), (513, 2056, 300)])
+def test_backward_where_all_rows_share_a_token(B, D, V):
+    h, W, T, ids = make(B, D, V, seed=19)
+    ids[:] = V // 2
+    check_backward(*backward_case(h, W, T, ids, 0))
+
+
 def test_backward_splits_the_vocabulary_for_few_tokens():
     # several parts of the vocabulary per tile of grad_h
     h, W, T, ids = make(70, 264, 9000, seed=4)
