@@ -258,16 +258,27 @@ hipError_t launch_tile(ScoreArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int L>
-hipError_t launch_tiles(ScoreArgs& a, hipStream_t stream) {
-  switch (logits_tile(a.B, a.V)) {
-    case LogitsTile::kTall64: return launch_tile<typename TallTile<L, 64>::T>(a, stream);
-    case LogitsTile::kTall128: return launch_tile<typename TallTile<L, 128>::T>(a, stream);
+template <int L, bool NTA>
+hipError_t launch_tiles(ScoreArgs& a, LogitsTile tile, hipStream_t stream) {
+  switch (tile) {
+    case LogitsTile::kTall64: return launch_tile<typename TallTile<L, 64, NTA>::T>(a, stream);
+    case LogitsTile::kTall128: return launch_tile<typename TallTile<L, 128, NTA>::T>(a, stream);
     case LogitsTile::kTall256: return launch_tile<typename TallTile<L, 256>::T>(a, stream);
-    case LogitsTile::kShort64: return launch_tile<typename ShortTile<L, 64>::T>(a, stream);
-    case LogitsTile::kShort128: return launch_tile<typename ShortTile<L, 128>::T>(a, stream);
+    case LogitsTile::kShort64: return launch_tile<typename ShortTile<L, 64, NTA>::T>(a, stream);
+    case LogitsTile::kShort128: return launch_tile<typename ShortTile<L, 128, NTA>::T>(a, stream);
     default: return launch_tile<typename ShortTile<L, 256>::T>(a, stream);
   }
+}
+
+// Tokens of one tile read W in fragment order once: past the caches.  More
+// tokens find it there (1300 tokens on 50000 rows of 1024 by tiles of 128: 154
+// us through the caches, 177 past them).
+template <int L>
+hipError_t launch_tiles(ScoreArgs& a, hipStream_t stream) {
+  const LogitsTile tile = logits_tile(a.B, a.V);
+  if constexpr (L == kFrag)
+    if (a.B <= tokens_of(tile)) return launch_tiles<L, true>(a, tile, stream);
+  return launch_tiles<L, false>(a, tile, stream);
 }
 
 template <int NT, int NW, int KS, int P, bool PACKED, bool WHOLE = false>

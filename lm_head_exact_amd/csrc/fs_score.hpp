@@ -107,40 +107,69 @@ __device__ __forceinline__ void fold_logits(const Z& z, int row0, int32_t V, int
 
 // ---- tiles of the logits (W is operand A, h operand B) ----
 // L: the layout of W.  Tall: 256 vocabulary rows by 64, 128 or 256 tokens.
-// Short, 4 waves, two blocks per CU: 64 by 64, 64 by 128, 128 by 128.
-template <int L, int TB> struct TallTile;
-template <int L> struct TallTile<L, 64> { using T = Tile<L, kKC, 8, 1, 2, 4, 4, 64, L == kFrag>; };
-template <int L> struct TallTile<L, 128> { using T = Tile<L, kKC, 4, 2, 4, 4, 3, 64, L == kFrag>; };
-template <int L> struct TallTile<L, 256> { using T = Tile<L, kKC, 2, 4, 8, 4, 2>; };
-template <int L, int TB> struct ShortTile;
-template <int L> struct ShortTile<L, 64> { using T = Tile<L, kKC, 4, 1, 1, 4, 4, 64, L == kFrag>; };
-template <int L> struct ShortTile<L, 128> { using T = Tile<L, kKC, 4, 1, 1, 8, 3, 64, L == kFrag>; };
-template <int L> struct ShortTile<L, 256> { using T = Tile<L, kKC, 2, 2, 4, 4, 2>; };
+// Short, 4 waves, two blocks per CU: 64 by 64, 64 by 128, 128 by 128.  NTA: W's
+// loads are non-temporal.
+template <int L, int TB, bool NTA = false> struct TallTile;
+template <int L, bool NTA> struct TallTile<L, 64, NTA> { using T = Tile<L, kKC, 8, 1, 2, 4, 4, 64, NTA>; };
+template <int L, bool NTA> struct TallTile<L, 128, NTA> { using T = Tile<L, kKC, 4, 2, 4, 4, 3, 64, NTA>; };
+template <int L, bool NTA> struct TallTile<L, 256, NTA> { using T = Tile<L, kKC, 2, 4, 8, 4, 2, 64, NTA>; };
+template <int L, int TB, bool NTA = false> struct ShortTile;
+template <int L, bool NTA> struct ShortTile<L, 64, NTA> { using T = Tile<L, kKC, 4, 1, 1, 4, 4, 64, NTA>; };
+template <int L, bool NTA> struct ShortTile<L, 128, NTA> { using T = Tile<L, kKC, 4, 1, 1, 8, 3, 64, NTA>; };
+template <int L, bool NTA> struct ShortTile<L, 256, NTA> { using T = Tile<L, kKC, 2, 2, 4, 4, 2, 64, NTA>; };
 constexpr int kTallRows = 256, kMinTileRows = 64;  // vocabulary rows of the tall tiles, and of any
 
 enum class LogitsTile { kTall64, kTall128, kTall256, kShort64, kShort128, kShort256 };
 
 inline int tile_tokens(int32_t B) { return B <= 64 ? 64 : B <= 128 ? 128 : 256; }
 
-// The tile for B tokens and V rows: the largest whose grid keeps three quarters
-// of the CUs busy.  Large tiles move less per product (512 tokens on 128256
-// rows of 4096: 475 us tall, 608 short); a grid of few leaves CUs idle (the
-// same tokens on 16032 rows of 8192: 195 us tall, 144 short), and where even
-// the short ones are few their k loops alone take the time (1024 tokens on
-// 1000 rows of 8192: 84 us by 128 x 128, 28 by 64 x 64).
+// The tile for B tokens and V rows: the one whose grid takes the least time.  A
+// tall tile's block has a CU to itself, so its grid takes whole rounds of 256
+// blocks; of the short ones, two share a CU, and their grids take about a round
+// and a half of its cost for two.  The costs are in hundredths of a round of
+// 256 x 64 tiles, from 16032 rows of 8192: a round of 256 x 64, 256 x 128 and
+// 256 x 256 takes 91, 115 and 209 us (252 blocks each), 251, 502 and 1004
+// blocks of 64 x 64 take 49, 68 and 123 us, of 64 x 128 60, 104 and 184, and
+// 252, 504 and 1008 of 128 x 128 119, 138 and 252.  256 x 128 is given a little
+// more: of two alike, 256 x 256 reads less.  (256 tokens there: 91 us by
+// 256 x 64, 117 by 128 x 128; 768 tokens: 194 us by 256 x 256, 222 by 128 x 128;
+// 1024 tokens on 1000 rows: 90 us by 128 x 128, 37 by 64 x 64.)
 inline LogitsTile logits_tile(int32_t B, int32_t V) {
-  constexpr int64_t kBlocks = 192;
-  auto grid = [&](int rows, int tokens) {
-    return (static_cast<int64_t>(V) + rows - 1) / rows * ((B + tokens - 1) / tokens);
+  struct Choice {
+    LogitsTile tile;
+    int32_t rows, tokens;
   };
-  const int TB = tile_tokens(B);
-  if (grid(kTallRows, TB) >= kBlocks)
-    return TB == 64    ? LogitsTile::kTall64
-           : TB == 128 ? LogitsTile::kTall128
-                       : LogitsTile::kTall256;
-  if (TB == 256 && grid(128, 128) >= kBlocks) return LogitsTile::kShort256;
-  if (TB == 128 && grid(64, 128) >= kBlocks) return LogitsTile::kShort128;
-  return LogitsTile::kShort64;
+  constexpr Choice kChoices[] = {
+      {LogitsTile::kTall64, 256, 64},  {LogitsTile::kTall128, 256, 128},
+      {LogitsTile::kTall256, 256, 256}, {LogitsTile::kShort64, 64, 64},
+      {LogitsTile::kShort128, 64, 128}, {LogitsTile::kShort256, 128, 128}};
+  LogitsTile best = LogitsTile::kTall64;
+  int64_t least = INT64_MAX;
+  for (const Choice& c : kChoices) {
+    const int64_t blocks = (static_cast<int64_t>(V) + c.rows - 1) / c.rows *
+                           ((static_cast<int64_t>(B) + c.tokens - 1) / c.tokens);
+    const int64_t rounds = (blocks + 255) / 256;
+    int64_t cost = 0;
+    switch (c.tile) {
+      case LogitsTile::kTall64: cost = 100 * rounds; break;
+      case LogitsTile::kTall128: cost = 132 * rounds; break;
+      case LogitsTile::kTall256: cost = 230 * rounds; break;
+      case LogitsTile::kShort64: cost = 22 + 30 * rounds; break;
+      case LogitsTile::kShort128: cost = 25 + 48 * rounds; break;
+      case LogitsTile::kShort256: cost = 148 * (rounds / 2) + 125 * (rounds % 2); break;
+    }
+    if (cost < least) {
+      least = cost;
+      best = c.tile;
+    }
+  }
+  return best;
+}
+
+inline int tokens_of(LogitsTile t) {
+  return t == LogitsTile::kTall64 || t == LogitsTile::kShort64 ? 64
+         : t == LogitsTile::kTall256                           ? 256
+                                                               : 128;
 }
 
 inline bool is_tall(LogitsTile t) { return t <= LogitsTile::kTall256; }

@@ -119,6 +119,27 @@ def test_forward_streams_every_row_length(B, D):
     check_forward(h, W, T, ids, 6, fs.token_logprobs(hd, Wp, Td, idd, vocab_offset=6, V=333))
 
 
+# one shape per tile of the logits: 256 x 64, 256 x 128, 256 x 256, 128 x 128, 64 x 128, 64 x 64
+@pytest.mark.parametrize("B,D,V", [(200, 64, 16032), (500, 72, 16001), (1000, 64, 16030),
+                                   (3833, 96, 2161), (513, 136, 2001), (60, 32, 803)])
+def test_every_tile(B, D, V):
+    h, W, T, ids = make(B, D, V, 3, seed=20)
+    hd, Wd, Td, idd = dev(h, W, T, ids)
+    check_forward(h, W, T, ids, 3, fs.token_logprobs(hd, Wd, Td, idd, vocab_offset=3))
+    if D % 32 == 0:
+        Wp = fs.pack_weights(Wd, 3)
+        check_forward(h, W, T, ids, 3, fs.token_logprobs(hd, Wp, Td, idd, vocab_offset=3, V=V))
+    check_backward(*backward_case(h, W, T, ids, 3))
+
+
+@pytest.mark.parametrize("B,V", [(64, 40000), (128, 50000), (128, 16032)])
+def test_fragment_order_in_tiles_that_read_it_once(B, V):
+    h, W, T, ids = make(B, 64, V, 2, seed=21)
+    hd, Wd, Td, idd = dev(h, W, T, ids)
+    Wp = fs.pack_weights(Wd, 2)
+    check_forward(h, W, T, ids, 2, fs.token_logprobs(hd, Wp, Td, idd, vocab_offset=2, V=V))
+
+
 @pytest.mark.parametrize("seed", range(12))
 def test_random_shapes(seed):
     g = torch.Generator().manual_seed(500 + seed)
