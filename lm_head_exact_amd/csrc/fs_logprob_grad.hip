@@ -574,7 +574,7 @@ hipError_t launch_logits(const GradArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_logits(const GradArgs& a, hipStream_t stream) {
-  switch (logits_tile(a.B, a.nv)) {
+  switch (logits_tile(a.B, a.nv, true)) {
     case LogitsTile::kTall64: return launch_logits<TallTile<kKC, 64>::T>(a, stream);
     case LogitsTile::kTall128: return launch_logits<TallTile<kKC, 128>::T>(a, stream);
     case LogitsTile::kTall256: return launch_logits<TallTile<kKC, 256>::T>(a, stream);
