@@ -3,6 +3,7 @@ runs them: sample from the head, score under old, reference and current
 weights, loss, gradients of the head and the hidden states, clipping -- against
 the same chain in fp64, and captured into one graph (GPU)."""
 import math
+import threading
 
 import pytest
 import torch
@@ -145,3 +146,42 @@ def test_whole_step_in_one_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
         assert torch.equal(wg, we) and torch.equal(mg, me)
+
+
+def test_calls_of_several_host_threads():
+    """Each thread on its own stream, outputs and workspaces its own: the bits of
+    a call by itself."""
+    g = torch.Generator().manual_seed(21)
+    B, D, V = 300, 264, 5000
+    h = torch.randn(B, D, generator=g).to(torch.bfloat16).cuda()
+    W = (0.1 * torch.randn(V, D, generator=g)).to(torch.bfloat16).cuda()
+    ids = torch.randint(0, V, (B,), generator=g).to(torch.int32).cuda()
+    cu = torch.tensor([0, 100, 300], dtype=torch.int32).cuda()
+    old, adv = torch.full((B,), -9.0).cuda(), torch.tensor([1.0, -1.0]).cuda()
+
+    def step():
+        lp, lse = fs.token_logprobs(h, W, None, ids)
+        stats, grad = fs.policy_loss(lp, old, adv, cu)
+        gh, gw = fs.token_logprobs_backward(h, W, None, ids, lp, lse, grad)
+        return lp, lse, stats, grad, gh, gw, fs.clip_grad_norm([gh, gw], 0.5)
+
+    want = step()
+    torch.cuda.synchronize()
+    same = []
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            ok = True
+            for _ in range(10):
+                got = step()
+                torch.cuda.current_stream().synchronize()
+                ok = ok and all(torch.equal(a, b) for a, b in zip(got, want))
+            torch.cuda.current_stream().synchronize()
+        same.append(ok)
+
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert same == [True] * 3
