@@ -20,6 +20,7 @@
 
 #include "fs_host.hpp"
 #include "fs_internal.hpp"
+#include "fs_tokens.hpp"
 
 namespace fs {
 namespace {
@@ -27,8 +28,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaveSize = 64;
 constexpr int kOneBlockThreads = 1024;
-// Token loads in flight per thread.
-constexpr int kAhead = 4;
 
 // The batches one block handles by itself: what it takes longer than the passes
 // over the device is below the two launches (2 to 3 us each on the host) that
@@ -133,21 +132,6 @@ __device__ __forceinline__ int2 block_count(int x, int y) {
   v.k = y;
   v = block_sum<THREADS>(v);
   return int2{v.n, v.k};
-}
-
-// Calls f(t) for the tokens [t0 + lane, t1) strided by `team`, with kAhead of
-// them loaded by load(t) at a time.
-template <class Load, class F>
-__device__ __forceinline__ void each_token(int t0, int t1, int lane, int team, Load load, F f) {
-  for (int t = t0 + lane; t < t1; t += team * kAhead) {
-    decltype(load(t)) v[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (t1 - t > u * team) v[u] = load(t + u * team);
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (t1 - t > u * team) f(t + u * team, v[u]);
-  }
 }
 
 // Team and item (part of a sequence) of a thread: TEAM threads per item.
