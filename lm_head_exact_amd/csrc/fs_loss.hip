@@ -183,9 +183,12 @@ __device__ __forceinline__ PolicyToken load_policy(const PolicyArgs& a, int t, f
   return k;
 }
 
-// e^q - q - 1, which cancels to q^2 / 2 near 0: there its series (the first
-// term left out is below 2^-25 of it for |q| < 1/2).
-__device__ __forceinline__ float exp_excess(float q) {
+// em = e^q - 1 and e^q - q - 1.  The latter cancels to q^2 / 2 near 0: there its
+// series (the first term left out is below 2^-25 of it for |q| < 1/2), and em is
+// the sum of it and q, which does not cancel; elsewhere em is taken from e^q, as
+// the excess would have lost it to q (q = -1e8: em is -1).  Both have their
+// limits at infinite q.
+__device__ __forceinline__ float exp_excess(float q, float& em) {
   float p = 1.0f / 3628800.0f;
   p = __builtin_fmaf(p, q, 1.0f / 362880.0f);
   p = __builtin_fmaf(p, q, 1.0f / 40320.0f);
@@ -195,7 +198,10 @@ __device__ __forceinline__ float exp_excess(float q) {
   p = __builtin_fmaf(p, q, 1.0f / 24.0f);
   p = __builtin_fmaf(p, q, 1.0f / 6.0f);
   p = __builtin_fmaf(p, q, 0.5f);
-  return fabsf(q) < 0.5f ? p * q * q : expf(q) - 1.0f - q;
+  const bool near = fabsf(q) < 0.5f;
+  const float series = p * q * q, far = expf(q) - 1.0f;
+  em = near ? q + series : far;
+  return near ? series : far == INFINITY ? far : far - q;
 }
 
 __device__ __forceinline__ TokenTerms policy_token(const PolicyArgs& a, const PolicyToken& k) {
@@ -222,8 +228,8 @@ __device__ __forceinline__ TokenTerms policy_token(const PolicyArgs& a, const Po
       o.kl = 0.5f * q * q;
       gk = -q;
     } else {
-      o.kl = exp_excess(q);
-      gk = -(q + o.kl);  // -(e^q - 1)
+      o.kl = exp_excess(q, gk);
+      gk = -gk;
     }
     o.g += static_cast<float>(a.kl_coef) * gk;
   }

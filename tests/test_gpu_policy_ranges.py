@@ -1,0 +1,70 @@
+"""fs_policy_loss where its terms leave their usual range, against plain fp64
+(GPU)."""
+import math
+
+import pytest
+import torch
+
+import lm_head_exact_amd as fs
+import training_ref as ref
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+# one block; blocks or waves per sequence
+LENS = [[40, 9], [6000, 31], [16] * 300]
+
+
+def batch(lens, seed=0):
+    g = torch.Generator().manual_seed(seed + sum(lens))
+    cu = torch.tensor([0] + list(torch.tensor(lens).cumsum(0)), dtype=torch.int32)
+    N = int(cu[-1])
+    old = -2 * torch.rand(N, generator=g) - 0.01
+    lp = old + 0.3 * torch.randn(N, generator=g)
+    return g, cu, N, lp, old
+
+
+def run(lp, old, adv, cu, refp=None, mask=None, **kw):
+    d = lambda x: None if x is None else x.cuda()
+    stats, grad = fs.policy_loss(d(lp), d(old), d(adv), d(cu), ref_logprob=d(refp), mask=d(mask), **kw)
+    return stats.cpu().double(), grad.cpu().double()
+
+
+@pytest.mark.parametrize("lens", LENS)
+@pytest.mark.parametrize("kl", ["k1", "k2", "k3"])
+def test_gradient_of_far_references(lens, kl):
+    """q = ref - lp from -1e30 to 80 and -inf (a reference of another shard's
+    token).  Per token, with A = 1: the surrogate's term is off by at most
+    (6 + |d|) 2^-24 of it (three roundings, exp's own two half steps and its
+    rounded argument), the KL's by its coefficient's, its product's and its own
+    roundings, 6 2^-24 of it, q's rounding (2^-24 |q|) seen through its
+    derivative, their sum by 2^-24; the weight adds 2 2^-24."""
+    g, cu, N, lp, old = batch(lens)
+    q = torch.tensor([-1e30, -1e9, -3e7, -1e5, -100.0, -20.0, -3.0, -0.6, -0.5, -0.4, -1e-3, 0.0,
+                      1e-3, 0.49, 0.51, 3.0, 20.0, 80.0, -math.inf])[torch.arange(N) % 19]
+    if kl == "k2":
+        q = q.clamp(min=-1e15)   # (its value, q^2 / 2, stays in range)
+    refp = lp + q
+    adv, coef = torch.ones(len(lens)), 0.5
+    _, want = ref.policy(lp, old, adv, cu, ref=refp, kl=kl, kl_coef=coef)
+    stats, grad = run(lp, old, adv, cu, refp, kl=kl, kl_coef=coef)
+    q64, d = refp.double() - lp.double(), (lp.double() - old.double())
+    slope, moves = {"k1": (torch.ones(N), torch.zeros(N)), "k2": (q64.abs(), q64.abs()),
+                    "k3": (torch.expm1(q64).abs(), q64.abs().nan_to_num(posinf=0) * q64.exp())}[kl]
+    tol = U / N * (torch.exp(d) * (9 + d.abs()) + coef * (9 * slope.double() + moves))
+    assert torch.isfinite(want).all()
+    assert ((grad - want).abs() <= tol).all(), float(((grad - want).abs() / tol).max())
+    assert stats[2] == math.inf or kl != "k3"
+
+
+@pytest.mark.parametrize("lens", LENS)
+def test_infinite_log_ratios_have_their_limits(lens):
+    """K3 at q = +inf (the model gives the token probability 0): the value's
+    limit is +inf, the gradient's -inf."""
+    g, cu, N, lp, old = batch(lens)
+    refp = lp.clone()
+    lp[5] = -math.inf
+    stats, grad = run(lp, old, torch.ones(len(lens)), cu, refp, kl="k3", kl_coef=0.1)
+    assert stats[0] == math.inf and stats[2] == math.inf and grad[5] == -math.inf
+    rest = torch.arange(N) != 5
+    assert torch.isfinite(grad[rest]).all()
