@@ -433,7 +433,8 @@ typedef enum { FS_TOKEN_MEAN = 0, FS_SEQUENCE_MEAN = 1 } fs_loss_reduction;
  *              dual_clip = c > 1 and A < 0 no larger than -c A (0: off)
  *   kl         K1: -q;  K2: q^2 / 2;  K3: exp(q) - q - 1  (0 without a
  *              reference)
- *   loss       surrogate + kl_coef * kl
+ *   loss       surrogate + kl_coef * kl (kl_coef 0: the surrogate alone, and
+ *              the mean kl is still reported)
  * averaged over the tokens that count (FS_TOKEN_MEAN) or, per sequence and
  * then over the sequences that have such tokens (FS_SEQUENCE_MEAN).  Without
  * any token that counts everything is 0.  A token has a surrogate gradient

@@ -231,7 +231,8 @@ __device__ __forceinline__ TokenTerms policy_token(const PolicyArgs& a, const Po
       o.kl = exp_excess(q, gk);
       gk = -gk;
     }
-    o.g += static_cast<float>(a.kl_coef) * gk;
+    // without a coefficient the term is only reported: it may be infinite or NaN
+    if (a.kl_coef != 0.0) o.g += static_cast<float>(a.kl_coef) * gk;
   }
   return o;
 }
@@ -285,7 +286,7 @@ __device__ __forceinline__ double policy_weight(const PolicyArgs& a, int2 totals
 
 // `all`: weighted sums of the surrogate and the KL term, tokens, clipped ones.
 __device__ __forceinline__ void write_policy_stats(const PolicyArgs& a, const Sum4& all) {
-  a.stats[0] = static_cast<float>(all.x + a.kl_coef * all.y);
+  a.stats[0] = static_cast<float>(a.kl_coef != 0.0 ? all.x + a.kl_coef * all.y : all.x);
   a.stats[1] = static_cast<float>(all.x);
   a.stats[2] = static_cast<float>(all.y);
   a.stats[3] = static_cast<float>(static_cast<double>(all.k) / max(all.n, 1));

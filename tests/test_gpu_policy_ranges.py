@@ -68,3 +68,21 @@ def test_infinite_log_ratios_have_their_limits(lens):
     assert stats[0] == math.inf and stats[2] == math.inf and grad[5] == -math.inf
     rest = torch.arange(N) != 5
     assert torch.isfinite(grad[rest]).all()
+
+
+@pytest.mark.parametrize("lens", LENS)
+@pytest.mark.parametrize("kl", ["k1", "k2", "k3"])
+def test_a_reference_without_a_coefficient_is_only_reported(lens, kl):
+    """kl_coef = 0: loss and gradient are those without a reference, bit for bit,
+    whatever the term is."""
+    g, cu, N, lp, old = batch(lens)
+    adv = torch.randn(len(lens), generator=g)
+    alone = run(lp, old, adv, cu)
+    refp = lp + 0.1
+    near = run(lp, old, adv, cu, refp, kl=kl)
+    assert near[0][2].isfinite() and near[0][2] != 0
+    refp[3], refp[7], refp[11] = 200.0, -math.inf, math.nan
+    far = run(lp, old, adv, cu, refp, kl=kl)
+    for stats, grad in (near, far):
+        assert torch.equal(stats[[0, 1, 3]], alone[0][[0, 1, 3]]) and torch.equal(grad, alone[1])
+    assert far[0][2].isnan()
