@@ -254,8 +254,9 @@ __device__ __forceinline__ int wave_count(int n) {
 }
 
 // Gradients of part y of sequence s (weight w per token) and this lane's share
-// of its sums.
-__device__ __forceinline__ Sum4 policy_part(const PolicyArgs& a, int s, int y, float w, int lane,
+// of its sums.  The weight stays fp64: a gradient is rounded with its product
+// alone, and a weight beyond fp32 leaves tokens that do not count at 0.
+__device__ __forceinline__ Sum4 policy_part(const PolicyArgs& a, int s, int y, double w, int lane,
                                             int team) {
   int t0, t1;
   part_range(a.q, s, y, t0, t1);
@@ -271,7 +272,7 @@ __device__ __forceinline__ Sum4 policy_part(const PolicyArgs& a, int s, int y, f
                  v.y += static_cast<double>(o.kl);
                  v.n += 1;
                  v.k += o.clipped ? 1 : 0;
-                 g = o.g * w;
+                 g = static_cast<float>(o.g * w);
                }
                a.grad[t] = g;
              });
@@ -335,7 +336,7 @@ __global__ __launch_bounds__(kThreads) void policy_kernel(PolicyArgs a) {
 #pragma unroll 8
     for (int i = 0; i < a.q.parts; ++i) n += a.count[static_cast<size_t>(s) * a.q.parts + i];
     const double w = policy_weight(a, totals, n);
-    v = policy_part(a, s, y, static_cast<float>(w * a.grad_scale), threadIdx.x % TEAM, TEAM);
+    v = policy_part(a, s, y, w * a.grad_scale, threadIdx.x % TEAM, TEAM);
     v.x *= w;
     v.y *= w;
   }
@@ -359,13 +360,13 @@ __global__ __launch_bounds__(kOneBlockThreads) void policy_stats_kernel(PolicyAr
 // weight, then scaled by the threads that wrote them.
 __global__ __launch_bounds__(kOneBlockThreads) void policy_one_block_kernel(PolicyArgs a) {
   __shared__ Sum4 part[kOneBlockItems];
-  __shared__ float weight[kOneBlockSequences];
+  __shared__ double weight[kOneBlockSequences];
   outside(a.q, a.grad, threadIdx.x, kOneBlockThreads);
   constexpr int kWaves = kOneBlockThreads / kWaveSize;
   const int wave = threadIdx.x / kWaveSize, lane = threadIdx.x % kWaveSize;
   const int Y = a.q.parts, S = a.q.S, items = S * Y;
   for (int i = wave; i < items; i += kWaves) {
-    Sum4 v = policy_part(a, i / Y, i % Y, 1.0f, lane, kWaveSize);
+    Sum4 v = policy_part(a, i / Y, i % Y, 1.0, lane, kWaveSize);
     v.wave_sum();
     if (lane == 0) part[i] = v;
   }
@@ -377,7 +378,7 @@ __global__ __launch_bounds__(kOneBlockThreads) void policy_one_block_kernel(Poli
     for (int y = 0; y < Y; ++y) one.add(part[s * Y + y]);
   const int2 totals = block_count<kOneBlockThreads>(one.n, one.n > 0);
   const double w = policy_weight(a, totals, one.n);
-  if (s < S) weight[s] = static_cast<float>(w * a.grad_scale);
+  if (s < S) weight[s] = w * a.grad_scale;
   one.x *= w;
   one.y *= w;
   const Sum4 all = block_sum<kOneBlockThreads>(one);
@@ -385,10 +386,10 @@ __global__ __launch_bounds__(kOneBlockThreads) void policy_one_block_kernel(Poli
   for (int i = wave; i < items; i += kWaves) {
     int t0, t1;
     part_range(a.q, i / Y, i % Y, t0, t1);
-    const float c = weight[i / Y];
+    const double c = weight[i / Y];
     // zero stays zero: a token that does not count has no gradient
     each_token(t0, t1, lane, kWaveSize, [&](int t) { return a.grad[t]; },
-               [&](int t, float g) { a.grad[t] = g * c; });
+               [&](int t, float g) { a.grad[t] = static_cast<float>(g * c); });
   }
 }
 

@@ -86,3 +86,35 @@ def test_a_reference_without_a_coefficient_is_only_reported(lens, kl):
     for stats, grad in (near, far):
         assert torch.equal(stats[[0, 1, 3]], alone[0][[0, 1, 3]]) and torch.equal(grad, alone[1])
     assert far[0][2].isnan()
+
+
+@pytest.mark.parametrize("lens", LENS + [[n, 1] for n in (10, 96, 1000, 4100, 6007)])
+@pytest.mark.parametrize("reduction", ["token", "sequence"])
+def test_gradient_is_rounded_once(lens, reduction):
+    """Ratio 1 and advantages of small whole numbers: a token's term is exact, so
+    its gradient is off by its own rounding alone, 2^-24, and the 3 2^-53 of a
+    weight in fp64."""
+    g, cu, N, lp, _ = batch(lens)
+    adv = torch.tensor([3.0, -5.0, 7.0, -11.0, 13.0])[torch.arange(len(lens)) % 5]
+    _, want = ref.policy(lp, lp, adv, cu, reduction=reduction)
+    _, grad = run(lp, lp, adv, cu, reduction=reduction)
+    assert ((grad - want).abs() <= want.abs() * (U + 2.0 ** -50)).all()
+
+
+@pytest.mark.parametrize("lens", LENS)
+@pytest.mark.parametrize("reduction", ["token", "sequence"])
+def test_weights_beyond_fp32_leave_masked_tokens_at_zero(lens, reduction):
+    g, cu, N, lp, old = batch(lens)
+    mask = torch.rand(N, generator=g) < 0.5
+    adv = torch.zeros(len(lens))
+    adv[0] = 1e-30
+    kw = dict(reduction=reduction, clip_low=0.9, clip_high=50.0)
+    for scale in (1e60, 1e300):
+        _, grad = run(lp, old, adv, cu, mask=mask, grad_scale=scale, **kw)
+        assert (grad[~mask] == 0).all() and (grad[lens[0]:] == 0).all()
+        assert grad[:lens[0]][mask[:lens[0]]].isinf().all() == (scale == 1e300)
+    # a weight that fp32 does not hold, a gradient that it does
+    _, want = ref.policy(lp, old, adv, cu, mask=mask, **kw)
+    _, grad = run(lp, old, adv, cu, mask=mask, grad_scale=1e40, **kw)
+    d = float((lp - old).abs().max())
+    assert ((grad - want * 1e40).abs() <= (8 + d) * U * (want * 1e40).abs()).all()
