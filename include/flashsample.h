@@ -352,7 +352,9 @@ FS_API fs_status fs_sample_unfused(const void* h, const void* W, int32_t B, int3
 /* Log-probabilities of given tokens under softmax(z_b / T_b), z_b = W h_b, with
  * no logits in memory.
  *   h, W, B, D, V, vocab_offset  as fs_sample (D up to 2^20, B up to 2^24,
- *                V up to 2^31 - 513, FS_ERR_UNSUPPORTED beyond); the _packed form reads W in
+ *                V up to 2^31 - 513, FS_ERR_UNSUPPORTED beyond, and where a
+ *                launch would hold 2^32 threads: never for V up to 2^31 - 4096
+ *                and B * V up to 2^37); the _packed form reads W in
  *                fragment order (fs_pack_weights, D % 32 == 0)
  *   temperature  fp32 [B], device, or NULL (all 1).  As in the samplers the
  *                logits are scaled by fp32(1/T), and a row whose temperature
@@ -385,7 +387,8 @@ FS_API fs_status fs_token_logprobs_packed(const void* h, const void* W_packed, i
  * Rows without a token (negative id) have no gradient: their grad_h is 0 and
  * their h, logprob, lse and grad_logprob are not used (they may be NaN).
  *   h, W, B, D, V, vocab_offset, temperature, token_ids  as in the forward
- *                call (row-major W; B up to 2^22)
+ *                call (row-major W; B up to 2^22, B * D up to 2^38, with
+ *                grad_W V below 2^30: FS_ERR_UNSUPPORTED beyond)
  *   logprob, lse fp32 [B]: the forward call's outputs; on a vocabulary shard
  *                the whole vocabulary's (logprob is read only for the tokens
  *                of this shard): grad_h is then this shard's share, to be

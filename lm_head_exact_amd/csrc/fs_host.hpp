@@ -16,6 +16,10 @@ fs_status hip_fail(hipError_t e, const char* what);
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// A launch holds fewer than 2^32 threads along a dimension of its grid.  The entry
+// points refuse what would take more before anything runs.
+inline bool grid_fits(int64_t blocks, int64_t threads) { return blocks <= 0xFFFFFFFFll / threads; }
+
 // Testing hook for failure handling: with FS_FAULT_INJECT=launch in the
 // environment, every entry point that would launch device work returns
 // FS_ERR_HIP once its arguments have passed the checks, before its first

@@ -243,12 +243,11 @@ constexpr int32_t kMaxScoreB = 1 << 24;
 constexpr int32_t kMaxScoreD = 1 << 20;
 constexpr int kMaxStreamBlocks = 2048;
 
-int64_t grid_tiles(int32_t B, int32_t S, int TB) {
-  return (static_cast<int64_t>(S) * ((B + TB - 1) / TB) + 7) / 8 * 8;
-}
+int64_t grid_tiles(int32_t B, int64_t S, int TB) { return (S * ((B + TB - 1) / TB) + 7) / 8 * 8; }
 
 template <class T>
 hipError_t launch_tile(ScoreArgs& a, hipStream_t stream) {
+  static_assert(T::kThreads == (T::TA == kTallRows ? 512 : 256), "threads_of");
   a.S = static_cast<int32_t>((static_cast<int64_t>(a.V) + a.shift + T::TA - 1) / T::TA);
   static SmemRaised raised;
   const hipError_t e = raise_smem(&score_tile_kernel<T>, T::kSmemBytes, raised);
@@ -364,8 +363,12 @@ fs_status check_score_shape(const char* who, int32_t B, int32_t D, int32_t V,
   if (B > kMaxScoreB || D > kMaxScoreD || V > kMaxVocab)
     return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, D=%d, V=%d exceed the %d rows, %d elements or %d "
                 "entries a call can take", who, B, D, V, kMaxScoreB, kMaxScoreD, kMaxVocab);
-  if (grid_tiles(B, tile_count(B, V), 64) > 0x7FFFFFFF)
-    return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, V=%d exceed the launch grid", who, B, V);
+  if (!streams(B, D)) {  // (streaming grids are bounded by the device)
+    const LogitsTile t = logits_tile(B, V);
+    const int64_t S = (static_cast<int64_t>(V) + 3 + rows_of(t) - 1) / rows_of(t);
+    if (!grid_fits(grid_tiles(B, S, tokens_of(t)), threads_of(t)))
+      return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, V=%d exceed the launch grid", who, B, V);
+  }
   return FS_OK;
 }
 

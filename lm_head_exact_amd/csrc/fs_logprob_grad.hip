@@ -656,6 +656,21 @@ hipError_t run_grad(GradArgs& a, const GradPlan& p, hipStream_t s) {
   return e;
 }
 
+// Whether every launch's grid holds fewer than 2^32 threads: the products' (the
+// logits at most one block of 512 per 64 x 64 of them, dW one of 256 per 256 x
+// 128 or of 512 per 256 x 256, dh one of 512 per tile and part) and the
+// targets', one block per 256 rows of W.  (The others have at most 2^22 + 256
+// blocks of 256 threads, or few.)
+bool grad_grids_fit(int32_t B, int32_t D, int32_t V, const GradPlan& p, bool dh, bool dW) {
+  const int64_t b64 = (B + 63) / 64, slice64 = (static_cast<int64_t>(p.slice) + 63) / 64;
+  const int64_t slice256 = (static_cast<int64_t>(p.slice) + 255) / 256;
+  const int64_t hidden = static_cast<int64_t>((B + p.TB - 1) / p.TB) * ((D + 255) / 256) * p.splits;
+  return grid_fits(slice64 * b64 + 7, 512) &&
+         (!dh || grid_fits(hidden + 7, 512)) &&
+         (!dW || (grid_fits(slice256 * ((D + 127) / 128) + 7, 256) &&
+                  grid_fits(target_tiles(V), kTargetThreads)));
+}
+
 bool grad_sizes_ok(int32_t B, int32_t D, int32_t V) {
   return B >= 0 && D >= 8 && D % 8 == 0 && V >= 1 && B <= kMaxGradB && D <= kMaxGradD &&
          V <= kMaxVocab;
@@ -705,9 +720,7 @@ FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_
   if (workspace_bytes < p.total)
     return fail(FS_ERR_WORKSPACE, "%s: workspace of %zu bytes is below the %zu required", who,
                 workspace_bytes, p.total);
-  const int64_t most_tiles = (static_cast<int64_t>(p.slice) / 64 + 1) *
-                             ((B + 63) / 64 > (D + 127) / 128 ? (B + 63) / 64 : (D + 127) / 128);
-  if (most_tiles > 0x7FFFFFFF - 8)
+  if (!grad_grids_fit(B, D, V, p, B > 0 && grad_h, grad_W))
     return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, D=%d, V=%d exceed the launch grid", who, B, D, V);
   if (start_launches()) return injected_failure(who);
   char* ws = static_cast<char*>(workspace);

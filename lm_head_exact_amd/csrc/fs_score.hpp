@@ -183,6 +183,9 @@ inline int tokens_of(LogitsTile t) {
 
 inline bool is_tall(LogitsTile t) { return t <= LogitsTile::kTall256; }
 
+inline int threads_of(LogitsTile t) { return is_tall(t) ? 512 : 256; }
+inline int rows_of(LogitsTile t) { return kTileShapes[static_cast<int>(t)].rows; }
+
 // Raises a kernel's dynamic-LDS limit, once per device (the limit is a device's
 // own).  Each kernel keeps its own record.
 struct SmemRaised {
