@@ -12,47 +12,27 @@
 // 1.85 GB of bf16 on an MI355X: 265 us for the norm (7.0 TB/s) and 600 us for
 // the scaling (6.2 TB/s, reads and writes); a copy of 2 GiB by torch runs at
 // 4.9 TB/s.
-// Tensors go to the device as tables in kernel arguments, kTable to a launch,
-// so that nothing is copied or kept.
+// Tensors go to the device as tables in kernel arguments (fs_clip_tables.hpp), so
+// that nothing is copied or kept.
 #include <cmath>
 
-#include "fs_host.hpp"
+#include "fs_clip_tables.hpp"
 #include "fs_device.hpp"
 #include "fs_internal.hpp"
 
 namespace fs {
 namespace {
 
-constexpr int kClipThreads = 256;
-constexpr int kTable = 96;              // 96 * 32 + ... bytes: below the 4 KB of kernel arguments
-constexpr int kVec = 16;                // bytes a lane loads at once
-constexpr int kUnroll = 4;
-// Bytes of input per block: one round of loads, which streams best when written
-// back (16 KB 596 us against 645 us with 64 KB); the norm's blocks take four
-// times that of many tensors, to leave fewer sums.
-constexpr int64_t kChunkBytes = kClipThreads * kVec * kUnroll;
 constexpr int64_t kManyBytes = kChunkBytes * 1024;
 // Inputs beyond the memory-side cache are not found there by the second step:
 // both then read past the caches (non-temporal: 1.85 GB 861 against 930 us);
 // smaller ones are (64 MB 31 against 34 us).  Results are stored past them in
 // either case (256 MB 115 against 146 us, equal for less).
 constexpr int64_t kCachedBytes = int64_t{256} << 20;
-constexpr int32_t kMaxTensors = 65536;
 // Chunks' sums that every scaling block adds up for itself; more are added by a
 // launch of their own (32 MB of fp32, 512 sums: 9.5 us in the blocks, 9.8 by a
 // launch; 64 MB: 19.4 and 17.8).
 constexpr int32_t kInBlockSums = 512;
-
-struct ClipTable {
-  const void* in[kTable];
-  void* out[kTable];
-  int64_t numel[kTable];
-  int32_t first[kTable + 1];  // first block of each tensor in this launch
-  uint8_t dtype[kTable];
-  int32_t n;
-  int32_t base;               // chunk index of the launch's first block
-  int32_t chunk;              // bytes per block
-};
 
 struct ClipItem {
   const void* in;
@@ -60,8 +40,6 @@ struct ClipItem {
   int64_t beg, end;  // elements
   int32_t dtype;
 };
-
-__host__ __device__ constexpr int type_bytes(int dtype) { return dtype == FS_FP32 ? 4 : 2; }
 
 // The block's tensor and elements.  Thread k looks at entry k; the one whose
 // blocks hold this one publishes the entry.
@@ -225,54 +203,6 @@ __global__ __launch_bounds__(kClipThreads) void scale_kernel(ClipTable t, const 
   if (it.dtype == FS_FP32) scale_chunk<FS_FP32, NTL>(it, c);
   else if (it.dtype == FS_BF16) scale_chunk<FS_BF16, NTL>(it, c);
   else scale_chunk<FS_FP16, NTL>(it, c);
-}
-
-int64_t tensor_blocks(int64_t numel, int dtype, int64_t chunk) {
-  const int64_t elems = chunk / type_bytes(dtype);
-  return (numel + elems - 1) / elems;
-}
-
-// Fills tables for blocks of `chunk` bytes and calls launch(table, blocks) for
-// each, in order.
-template <class F>
-hipError_t for_each_table(const void* const* grads, void* const* out, const int64_t* numel,
-                          const fs_dtype* dtypes, int32_t n, int64_t chunk, F launch) {
-  ClipTable t;
-  t.n = 0;
-  t.base = 0;
-  t.chunk = static_cast<int32_t>(chunk);
-  int64_t blocks = 0;
-  for (int32_t i = 0; i < n; ++i) {
-    if (numel[i] > 0) {
-      t.in[t.n] = grads[i];
-      t.out[t.n] = out ? out[i] : const_cast<void*>(grads[i]);
-      t.numel[t.n] = numel[i];
-      t.dtype[t.n] = static_cast<uint8_t>(dtypes[i]);
-      t.first[t.n] = static_cast<int32_t>(blocks);
-      blocks += tensor_blocks(numel[i], dtypes[i], chunk);
-      t.first[++t.n] = static_cast<int32_t>(blocks);
-    }
-    if (t.n > 0 && (t.n == kTable || i == n - 1)) {
-      const hipError_t e = launch(t, static_cast<unsigned>(blocks));
-      if (e != hipSuccess) return e;
-      t.base += static_cast<int32_t>(blocks);
-      t.n = 0;
-      blocks = 0;
-    }
-  }
-  return hipSuccess;
-}
-
-// Blocks of all tensors at the smaller chunk and fp32 (an upper bound), or -1.
-int64_t max_chunks(const int64_t* numel, int32_t n) {
-  if (n < 0 || n > kMaxTensors || (n > 0 && !numel)) return -1;
-  int64_t c = 0;
-  for (int32_t i = 0; i < n; ++i) {
-    if (numel[i] < 0 || numel[i] > (int64_t{1} << 42)) return -1;
-    c += tensor_blocks(numel[i], FS_FP32, kChunkBytes);
-    if (c > 0x7FFFFFFF) return -1;
-  }
-  return c;
 }
 
 constexpr size_t kScaleBytes = 256;
