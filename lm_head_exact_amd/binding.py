@@ -871,9 +871,12 @@ def clip_grad_norm(grads, max_norm: float, out=None, norm: Optional[torch.Tensor
                     raise ValueError("a tensor of out overlaps one of grads that is not its own")
     array = ctypes.c_void_p * n
     sizes = (ctypes.c_int64 * n)(*count)
-    types = (ctypes.c_int * n)(*types)
+    given = norm is not None or workspace is not None
     norm = _out(norm, "norm", (1,), torch.float32, dev)
     ws = _workspace(workspace, int(lib().fs_clip_grad_norm_workspace_bytes(sizes, n)), dev)
+    if given:
+        _apart((norm, ws), grads if out is None else (*grads, *outs))
+    types = (ctypes.c_int * n)(*types)
     _call(lib().fs_clip_grad_norm, dev, array(*src), None if out is None else array(*dst), sizes,
           types, n, max_norm, _addr(norm), _addr(ws), _nbytes(ws))
     return norm
