@@ -8,6 +8,7 @@ to load, every function raises; there is no fallback path.
 """
 import bisect
 import ctypes
+import math
 import os
 import re
 from typing import Optional, Tuple
@@ -633,6 +634,12 @@ def _apart(written, read):
             raise ValueError("outputs and workspace must overlap neither each other nor an input")
 
 
+def _changed(*tensors: Optional[torch.Tensor]):
+    """Tells autograd that these tensors of the caller's were written: a graph that
+    saved one refuses its backward pass."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def _row(t: Optional[torch.Tensor], name: str, dtype, n: int, device):
     if t is None:
         return
@@ -686,6 +693,8 @@ def token_logprobs(h: torch.Tensor, W: torch.Tensor, temperature: Optional[torch
     fn = lib().fs_token_logprobs_packed if packed else lib().fs_token_logprobs
     _call(fn, dev, _addr(h), _addr(W), B, D, V, int(vocab_offset), _addr(temperature),
           _addr(token_ids), _addr(lp), _addr(lse), _addr(ws), _nbytes(ws))
+    if out is not None:
+        _changed(*out)
     return lp, lse
 
 
@@ -724,6 +733,8 @@ def token_logprobs_backward(h: torch.Tensor, W: torch.Tensor, temperature: Optio
     _call(lib().fs_token_logprobs_backward, dev, _addr(h), _addr(W), B, D, V, int(vocab_offset),
           _addr(temperature), _addr(token_ids), _addr(logprob), _addr(lse), _addr(grad_logprob),
           _addr(gh), _addr(gw), _addr(ws), _nbytes(ws))
+    if out is not None:
+        _changed(gh, gw)
     return gh, gw
 
 
@@ -788,6 +799,8 @@ def policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages: to
           _addr(advantages), _addr(m), _addr(cu_seqlens), S, N, int(per_token), clip_low, clip_high,
           dual_clip, kl_coef, _choice(_KL, kl, "kl"), _choice(_REDUCTIONS, reduction, "reduction"),
           grad_scale, int(given is None), _addr(stats), _addr(grad), _addr(ws), _nbytes(ws))
+    if out is not None:
+        _changed(*out)
     return stats, grad
 
 
@@ -819,6 +832,8 @@ def preference_loss(logprob: torch.Tensor, cu_seqlens: torch.Tensor,
           _addr(cu_seqlens), S // 2, N, _choice(_PREFERENCES, kind, "kind"), beta, margin,
           label_smoothing, int(length_normalised), grad_scale, int(given is None), _addr(stats),
           _addr(rewards), _addr(grad), _addr(ws), _nbytes(ws))
+    if out is not None:
+        _changed(*out)
     return stats, rewards, grad
 
 
@@ -876,7 +891,10 @@ def clip_grad_norm(grads, max_norm: float, out=None, norm: Optional[torch.Tensor
     ws = _workspace(workspace, int(lib().fs_clip_grad_norm_workspace_bytes(sizes, n)), dev)
     if given:
         _apart((norm, ws), grads if out is None else (*grads, *outs))
+        _changed(norm)
     types = (ctypes.c_int * n)(*types)
     _call(lib().fs_clip_grad_norm, dev, array(*src), None if out is None else array(*dst), sizes,
           types, n, max_norm, _addr(norm), _addr(ws), _nbytes(ws))
+    if out is not None or max_norm != math.inf:  # (an infinite limit in place: the norm alone)
+        _changed(*outs)
     return norm
