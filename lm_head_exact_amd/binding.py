@@ -662,7 +662,16 @@ def token_logprobs(h: torch.Tensor, W: torch.Tensor, temperature: Optional[torch
     token_ids are global ids (int32); rows with a negative id have none and get
     log-probability 0, ids outside this W's rows get -inf.  temperature None
     means 1.  W is row-major V x D, or (1-D, with V given) its fragment-order
-    copy from pack_weights at the same vocab_offset."""
+    copy from pack_weights at the same vocab_offset.
+
+    Where torch records gradients and h or W requires one, the log-probabilities
+    carry a graph whose backward pass is token_logprobs_backward (not within a
+    graph capture: capture that call).  None leads through the log-sum-exps, the
+    temperatures or a fragment-order W: its backward pass raises.  Results
+    written to `out` carry no graph."""
+    if out is None and torch.is_grad_enabled() and any(
+            isinstance(t, torch.Tensor) and t.requires_grad for t in (h, W, temperature)):
+        return _TokenLogprobs.apply(h, W, temperature, token_ids, vocab_offset, workspace, V)
     _req(h, "h", torch.bfloat16, 2)
     packed = isinstance(W, torch.Tensor) and W.dim() == 1
     _req(W, "W", torch.bfloat16, 1 if packed else 2)
@@ -700,6 +709,40 @@ def token_logprobs(h: torch.Tensor, W: torch.Tensor, temperature: Optional[torch
 
 def token_logprobs_backward_workspace_bytes(B: int, D: int, V: int) -> int:
     return int(lib().fs_token_logprobs_backward_workspace_bytes(B, D, V))
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    """token_logprobs with its backward pass."""
+
+    @staticmethod
+    def forward(ctx, h, W, temperature, token_ids, vocab_offset, workspace, V):
+        lp, lse = token_logprobs(h, W, temperature, token_ids, vocab_offset, None, workspace, V)
+        ctx.save_for_backward(h, W, temperature, token_ids, lp, lse)
+        ctx.vocab_offset = vocab_offset
+        ctx.set_materialize_grads(False)  # (a gradient of lse is one that somebody asked for)
+        return lp, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_logprob, grad_lse):
+        h, W, temperature, token_ids, lp, lse = ctx.saved_tensors
+        if grad_lse is not None:
+            raise RuntimeError("token_logprobs: no gradient leads through the log-sum-exps")
+        if ctx.needs_input_grad[2]:
+            raise RuntimeError("token_logprobs: no gradient leads to the temperatures")
+        if W.dim() == 1:
+            raise RuntimeError("token_logprobs: no gradient leads through a fragment-order W; "
+                               "score with the row-major one")
+        if torch.cuda.is_current_stream_capturing():
+            # (accumulating into leaves that an eager graph holds too would leave the capture)
+            raise RuntimeError("token_logprobs: its backward pass cannot be captured; capture "
+                               "token_logprobs_backward")
+        if grad_logprob is None:
+            return (None,) * 7
+        gh, gw = token_logprobs_backward(h, W, temperature, token_ids, lp, lse,
+                                         grad_logprob.contiguous(), ctx.vocab_offset,
+                                         ctx.needs_input_grad[0], ctx.needs_input_grad[1])
+        return gh, gw, None, None, None, None, None
 
 
 def token_logprobs_backward(h: torch.Tensor, W: torch.Tensor, temperature: Optional[torch.Tensor],
@@ -780,7 +823,8 @@ def policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages: to
     """fs_policy_loss over packed sequences (tokens cu_seqlens[s] to
     cu_seqlens[s + 1] of the flat fp32 arrays): returns (stats fp32 [4], grad
     fp32 [tokens]); stats are the loss, the mean surrogate, the mean KL and
-    the clipped share, grad is grad_scale * d loss / d logprob.  advantages
+    the clipped share, grad is grad_scale * d loss / d logprob; neither carries
+    a graph (a logprob with one goes on by logprob.backward(grad)).  advantages
     holds one value per sequence, or with per_token one per token.  mask (bool
     or uint8): the tokens that count.  Entries of grad before the first and
     behind the last sequence are 0; in a grad given by `out` = (stats, grad)
@@ -814,7 +858,7 @@ def preference_loss(logprob: torch.Tensor, cu_seqlens: torch.Tensor,
     then the rejected ones in the same order (cu_seqlens has 2 P + 1 entries):
     returns (stats fp32 [3], rewards fp32 [2 P], grad fp32 [tokens]); stats are
     the loss, the share of pairs that prefer the chosen answer and the mean
-    margin of rewards.  Entries of grad before the first and behind the last
+    margin of rewards; none carries a graph (logprob.backward(grad)).  Entries of grad before the first and behind the last
     sequence are 0; in a grad given by `out` = (stats, rewards, grad) they are
     left as they were."""
     dev, N, m = _sequences(logprob, cu_seqlens, mask, ref_logprob=ref_logprob)
