@@ -368,7 +368,8 @@ FS_API fs_status fs_sample_unfused(const void* h, const void* W, int32_t B, int3
  *                invalid sizes); contents on entry ignored
  * On a vocabulary shard logprob + lse is the token's scaled logit on the rank
  * that holds it and -inf elsewhere, and the log-sum-exp of the ranks' lse is
- * the whole vocabulary's.  NaN entries of h or W give NaN in their rows. */
+ * the whole vocabulary's.  NaN entries of h or W give NaN in their rows, and so
+ * do scaled logits of +inf; one of -inf has probability 0 (all of them: NaN). */
 FS_API size_t fs_token_logprobs_workspace_bytes(int32_t B, int32_t D, int32_t V);
 FS_API fs_status fs_token_logprobs(const void* h, const void* W, int32_t B, int32_t D, int32_t V,
                                    int32_t vocab_offset, const float* temperature,

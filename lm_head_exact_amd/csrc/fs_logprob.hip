@@ -229,7 +229,8 @@ __global__ __launch_bounds__(kCloseThreads) void score_close_kernel(ScoreArgs a,
     const float soft = fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
     // NaN logits give NaN (fmaxf alone would drop it)
     logprob[b] = x != x ? x : -soft;
-    lse[b] = x != x ? x : zt + soft;
+    // (a target at -inf: the others' alone)
+    lse[b] = x != x ? x : zt == -INFINITY ? rest : zt + soft;
   } else {
     logprob[b] = id < 0 ? 0.0f : -INFINITY;
     lse[b] = rest;

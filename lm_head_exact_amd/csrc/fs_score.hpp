@@ -9,6 +9,8 @@
 //   log p(target) = -log(1 + exp(L - t_target)),
 // which keeps its relative accuracy where the target is nearly certain;
 // t_target - logsumexp(all) would cancel there.
+//
+// Logits of -inf add nothing (exp gives 0); NaN or +inf among them gives NaN.
 #pragma once
 
 #include <atomic>
@@ -52,6 +54,13 @@ __device__ __forceinline__ void pair_xor(float& m, float& s, int mask) {
   pair_merge(m, s, om, os);
 }
 
+// What is taken from the exponents of a lane's logits, whose maximum is mz: 0
+// where that is -inf (the maximum starts at kMasked), for which the product
+// would make -inf - (-inf) of them.
+__device__ __forceinline__ float exponent_offset(float mz, float c) {
+  return mz == LseAcc::kMasked ? 0.0f : mz * c;
+}
+
 // Folds the wave's logits of one token into (m, s): z[i][r] is vocabulary row
 // row0 + 16 i + r + 4 kb.  All values are in registers, so the maximum comes
 // first and each logit costs one multiply-add and one exp2.  `plain` (the
@@ -69,7 +78,7 @@ __device__ __forceinline__ void fold_logits(const Z& z, int row0, int32_t V, int
       const f32x4 x = z(i);
       mz = fmaxf(fmaxf(mz, fmaxf(x[0], x[1])), fmaxf(x[2], x[3]));
     });
-    const float off = mz * c;
+    const float off = exponent_offset(mz, c);
     static_for<MR>([&](auto i) FS_INLINE {
       const f32x4 x = z(i);
       static_for<4>([&](auto r) FS_INLINE {
@@ -91,7 +100,7 @@ __device__ __forceinline__ void fold_logits(const Z& z, int row0, int32_t V, int
         mz = keep(v) ? fmaxf(mz, x[decltype(r)::value]) : mz;
       });
     });
-    const float off = mz * c;
+    const float off = exponent_offset(mz, c);
     static_for<MR>([&](auto i) FS_INLINE {
       const f32x4 x = z(i);
       static_for<4>([&](auto r) FS_INLINE {
