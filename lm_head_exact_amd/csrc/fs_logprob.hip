@@ -81,8 +81,9 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const __bf16* h, int32_t 
 // grid, so that the rows being read form a narrow moving window of W (HBM
 // page locality), through a ring of P loads that runs ahead across groups.
 // The partial sums meet in LDS; the wave whose turn it is adds them in wave
-// order and folds the 16 rows into its running pairs.  k's past D take zeros
-// of h against W's last piece.
+// order and folds the 16 rows into its running pairs.  k's past D load W's last
+// piece again and take zeros of both operands (an infinite entry of that piece
+// must not meet a zero of h).
 // ---------------------------------------------------------------------------
 template <int NT, int NW, int KS, int P, bool PACKED, bool WHOLE>
 __global__ __launch_bounds__(NW * kWave) void score_stream_kernel(ScoreArgs a) {
@@ -126,6 +127,10 @@ __global__ __launch_bounds__(NW * kWave) void score_stream_kernel(ScoreArgs a) {
     else
       return load_frag<false>(p + (WHOLE ? 32 * s : min(k0 + 32 * s, D - 8)));
   };
+  // The wave's k-steps within D (scalar), and whether the lane's piece of the next
+  // one is, where D ends in it.
+  const int whole_steps = __builtin_amdgcn_readfirstlane(min(max(D / 32 - wave * KS, 0), KS));
+  const bool part = !PACKED && D / 32 >= wave * KS && 8 * kb < D % 32;
   float m[NT], s_[NT];
   static_for<NT>([&](auto n) FS_INLINE {
     m[n] = LseAcc::kMasked;
@@ -139,9 +144,15 @@ __global__ __launch_bounds__(NW * kWave) void score_stream_kernel(ScoreArgs a) {
   for (int it = 0; g < ngroups; g += G, ++it) {
     f32x4 acc[NT];
     static_for<NT>([&](auto n) FS_INLINE { acc[n] = f32x4{0.f, 0.f, 0.f, 0.f}; });
+    // (compared anew for every group: kept, the steps' masks would fill the scalar
+    // registers)
+    int steps = whole_steps;
+    if constexpr (!WHOLE) asm volatile("" : "+s"(steps));
     static_for<KS>([&](auto sc) FS_INLINE {
       constexpr int s = decltype(sc)::value, slot = s % P;
-      static_for<NT>([&](auto n) FS_INLINE { acc[n] = mfma16(ring[slot], hreg[s][n], acc[n]); });
+      const bf16x8 w =
+          WHOLE || s < steps || (s == steps && part) ? ring[slot] : zero_frag();
+      static_for<NT>([&](auto n) FS_INLINE { acc[n] = mfma16(w, hreg[s][n], acc[n]); });
       if constexpr (s + P < KS) ring[slot] = load(wp, s + P);
       else ring[slot] = load(wn, s + P - KS);
     });

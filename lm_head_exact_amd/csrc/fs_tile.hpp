@@ -30,9 +30,13 @@
 // direct loads write LDS in lane order, so the permutation is applied to the
 // addresses they read.
 //
-// Bounds.  Rows, k's and columns past an operand's end are read at its last
-// one: no access leaves the operand.  What they contribute is masked by the
-// epilogue (rows of A and B) or multiplied by the other operand's zeros (k).
+// Bounds.  Rows and columns past an operand's end are read at its last one, and
+// so are the k's of a KM operand; the k's past a KC or fragment-order operand's
+// end are offsets beyond the buffer's size, which load zeros: no access leaves
+// the operand.  What lies past the end is masked by the epilogue (rows of A and
+// B) or multiplied by the other operand's zeros (k).  (Where A's k's end is
+// ragged it is W of the logits, and an infinite entry of it read again would
+// make inf * 0 of those zeros.)
 #pragma once
 
 #include "fs_mma.hpp"
@@ -72,6 +76,10 @@ struct Tile {
                 "KM swizzle needs 8 units a row");
   static_assert(kSmemBytes <= 160 * 1024, "LDS");
   static constexpr int kBufferFlags = 0x00020000;
+  // The buffers' size in bytes, above every offset of an operand's; and an offset
+  // past it, for which a load gives zeros.
+  static constexpr int kBufferBytes = 0x7FFFFFFF;
+  static constexpr int kPastEnd = static_cast<int>(0x80000000u);
 
   __device__ __forceinline__ static int wave() {
     return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
@@ -105,7 +113,7 @@ struct Tile {
   // Staging of one operand: byte offsets, from the first element of a k tile of
   // the operand's rows i0 .., of the pieces this lane loads.  They are the same
   // for every k tile (the tile's start is in scalar registers) but the last,
-  // ragged one, whose pieces past the end move to the last piece.
+  // ragged one.
   template <int L, int T, int I, bool NT_LOADS = false>
   struct Stager {
     const __bf16* base;  // rows i0 .. at k = 0
@@ -127,19 +135,23 @@ struct Tile {
           off[i] = min(piece * 8, o.n - 8 - i0) * 2 + min(k, ks - 1) * static_cast<int>(o.pitch * 2);
         } else if constexpr (L == kFrag) {  // pieces (group, k step of the tile) of 1 KB
           const int piece = q / kWave;
-          off[i] = static_cast<int>(min(piece / KS, o.n - 1 - i0 / 16) * o.pitch) * 2 + lane * 16 +
-                   (ks > 32 ? (piece % KS) * 1024 : 0);
+          off[i] = piece % KS * 32 < ks
+                       ? static_cast<int>(min(piece / KS, o.n - 1 - i0 / 16) * o.pitch) * 2 +
+                             lane * 16 + piece % KS * 1024
+                       : kPastEnd;
         } else {
           constexpr int P = BK / 8;  // pieces per row
           const int r = q / P, piece = (q % P) ^ kc_swizzle(r);
-          off[i] = (static_cast<int>(min(r, o.n - 1 - i0) * o.pitch) + min(piece * 8, ks - 8)) * 2;
+          off[i] = piece * 8 < ks
+                       ? (static_cast<int>(min(r, o.n - 1 - i0) * o.pitch) + piece * 8) * 2
+                       : kPastEnd;
         }
       });
     }
     // Tile kt into LDS at `dst`.
     __device__ __forceinline__ void stage(int kt, unsigned char* dst) const {
       const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<__bf16*>(base + kt * step), 0, 0x7FFFFFFF, kBufferFlags);
+          const_cast<__bf16*>(base + kt * step), 0, kBufferBytes, kBufferFlags);
       static_for<I>([&](auto i) FS_INLINE {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             rsrc,

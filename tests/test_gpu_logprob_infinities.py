@@ -1,5 +1,6 @@
 """fs_token_logprobs where logits are infinite, against plain fp64 (GPU): a logit
-of -inf has probability 0, +inf or NaN gives NaN, whichever kernel makes them.
+of -inf has probability 0, +inf or NaN gives NaN, whichever kernel makes them
+and wherever in W the infinite entry lies.
 
 The log-sum-exps and log-probabilities are compared within the tolerances of
 test_gpu_token_logprobs (a logit is off by e, the rest by 2^-22 of values of
@@ -33,7 +34,7 @@ def infinite(h, W, T, ids, off, rows, column, value):
 
 
 @pytest.mark.parametrize("B,D,V", SHAPES)
-@pytest.mark.parametrize("where", ["first"])
+@pytest.mark.parametrize("where", ["first", "last"])
 @pytest.mark.parametrize("count", [1, 37, 160])
 def test_logits_of_minus_infinity_have_probability_zero(B, D, V, where, count):
     """Rows whose logits are -inf for the even hidden states, alone and in
@@ -84,3 +85,16 @@ def test_every_logit_at_minus_infinity_gives_nan(B, D, V):
     lp, lse = fs.token_logprobs(*dev(h, W, T, ids))
     assert not torch.isfinite(lse).any() and (lse < 0).logical_or(lse.isnan()).all()
     assert lp.cpu()[ids >= 0].isnan().all()
+
+
+@pytest.mark.parametrize("B,D,V", [s for s in SHAPES if s[1] % 64])
+def test_padding_of_rows_takes_nothing_from_infinite_entries(B, D, V):
+    """Hidden states of zero where W is infinite are NaN by the product itself;
+    those of +1 in the last column of an odd D see no product with padding."""
+    h, W, T, ids = make(B, D, V, seed=34)
+    h, W = infinite(h, W, T, ids, 0, torch.tensor([1, V - 1]), D - 1, -math.inf)
+    h[:, D - 1] = 1.0
+    ids[ids >= 0] = 0
+    keep = torch.ones(V, dtype=torch.bool)
+    keep[[1, V - 1]] = False
+    check_forward(h, W[keep], T, ids, 0, fs.token_logprobs(*dev(h, W, T, ids)))
