@@ -902,8 +902,9 @@ def clip_grad_norm(grads, max_norm: float, out=None, norm: Optional[torch.Tensor
         types = [_DTYPES[g.dtype] for g in grads]
     except (KeyError, AttributeError):
         raise TypeError("grads must be bf16, fp16 or fp32 tensors") from None
+    on = dev.type == "cuda"
     for i, g in enumerate(grads):
-        if not (g.is_cuda and g.is_contiguous() and g.device == dev):
+        if not (on and g.is_contiguous() and g.device == dev):
             raise ValueError(f"grads[{i}] must be contiguous and on the first gradient's device")
     if out is not None:
         for i, (g, o) in enumerate(zip(grads, outs)):
@@ -916,7 +917,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, norm: Optional[torch.Tensor
     dst = src if out is None else [o.data_ptr() for o in outs]
     # a written tensor's bytes end before the next one's begin ...
     ends = 0
-    written = sorted(p for p in zip(dst, types, count) if p[2])
+    written = sorted([p for p in zip(dst, types, count) if p[2]])
     for p, t, k in written:
         if p < ends:
             raise ValueError("the tensors written must not overlap")
@@ -940,5 +941,5 @@ def clip_grad_norm(grads, max_norm: float, out=None, norm: Optional[torch.Tensor
     _call(lib().fs_clip_grad_norm, dev, array(*src), None if out is None else array(*dst), sizes,
           types, n, max_norm, _addr(norm), _addr(ws), _nbytes(ws))
     if out is not None or max_norm != math.inf:  # (an infinite limit in place: the norm alone)
-        _changed(*outs)
+        torch.autograd.graph.increment_version(outs)
     return norm
