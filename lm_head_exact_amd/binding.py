@@ -620,6 +620,14 @@ def _workspace(t: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
     return t
 
 
+def _int32(*values: int):
+    """The call's sizes and offsets fit the library's 32-bit arguments (ctypes would
+    drop their upper bits)."""
+    for v in values:
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"sizes and offsets must be below 2^31 (got {v})")
+
+
 def _nbytes(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
@@ -651,6 +659,7 @@ def _row(t: Optional[torch.Tensor], name: str, dtype, n: int, device):
 
 
 def token_logprobs_workspace_bytes(B: int, D: int, V: int) -> int:
+    _int32(B, D, V)
     return int(lib().fs_token_logprobs_workspace_bytes(B, D, V))
 
 
@@ -676,9 +685,11 @@ def token_logprobs(h: torch.Tensor, W: torch.Tensor, temperature: Optional[torch
     packed = isinstance(W, torch.Tensor) and W.dim() == 1
     _req(W, "W", torch.bfloat16, 1 if packed else 2)
     B, D = h.shape
+    _int32(vocab_offset)
     if packed:
         if V is None:
             raise ValueError("V is required with fragment-order W")
+        _int32(D, V)
         need = packed_weights_bytes(V, D, vocab_offset)
         if need == 0 or W.numel() * 2 < need:
             raise ValueError(f"W_packed holds {W.numel() * 2} bytes; {need} needed")
@@ -708,6 +719,7 @@ def token_logprobs(h: torch.Tensor, W: torch.Tensor, temperature: Optional[torch
 
 
 def token_logprobs_backward_workspace_bytes(B: int, D: int, V: int) -> int:
+    _int32(B, D, V)
     return int(lib().fs_token_logprobs_backward_workspace_bytes(B, D, V))
 
 
@@ -758,6 +770,7 @@ def token_logprobs_backward(h: torch.Tensor, W: torch.Tensor, temperature: Optio
     _req(W, "W", torch.bfloat16, 2)
     B, D = h.shape
     V = W.shape[0]
+    _int32(vocab_offset)
     if W.shape[1] != D:
         raise ValueError(f"h is B x {D} but W is V x {W.shape[1]}")
     dev = h.device
@@ -782,6 +795,7 @@ def token_logprobs_backward(h: torch.Tensor, W: torch.Tensor, temperature: Optio
 
 
 def loss_workspace_bytes(n_sequences: int, n_tokens: int) -> int:
+    _int32(n_sequences, n_tokens)
     return int(lib().fs_loss_workspace_bytes(n_sequences, n_tokens))
 
 

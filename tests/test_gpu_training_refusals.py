@@ -36,3 +36,25 @@ def test_clipping_keeps_norm_and_workspace_apart_from_the_tensors():
     norm = fs.clip_grad_norm(grads, 1e9, norm=big[1500:1501], workspace=ws[off:])
     assert norm.data_ptr() == big[1500:].data_ptr() and abs(float(norm) - 8000 ** 0.5) < 1e-4
     assert (a == 1).all() and (b == 1).all()
+
+
+def test_sizes_and_offsets_beyond_32_bits():
+    """They are refused, not cut to 32 bits."""
+    h, W = torch.ones(2, 64).to(torch.bfloat16).cuda(), torch.ones(40, 64).to(torch.bfloat16).cuda()
+    ids, z = torch.zeros(2, dtype=torch.int32).cuda(), torch.zeros(2).cuda()
+    Wp = fs.pack_weights(W)
+    for off in (2**31, 2**32, 2**40, -2**32):
+        with pytest.raises(ValueError, match="2\\^31"):
+            fs.token_logprobs(h, W, None, ids, vocab_offset=off)
+        with pytest.raises(ValueError, match="2\\^31"):
+            fs.token_logprobs_backward(h, W, None, ids, z, z, z, vocab_offset=off)
+    with pytest.raises(ValueError, match="2\\^31"):
+        fs.token_logprobs(h, Wp, None, ids, V=2**32 + 40)
+    with pytest.raises(fs.FlashSampleError):
+        fs.token_logprobs(h, W, None, ids, vocab_offset=2**31 - 40)
+    x = torch.empty(2**32 + 5, device="cuda")
+    cu = torch.tensor([0, 2, 5], dtype=torch.int32).cuda()
+    with pytest.raises(ValueError, match="2\\^31"):
+        fs.policy_loss(x, x, z, cu)
+    with pytest.raises(ValueError, match="2\\^31"):
+        fs.preference_loss(x, cu)
