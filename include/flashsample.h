@@ -400,7 +400,8 @@ FS_API fs_status fs_token_logprobs_packed(const void* h, const void* W_packed, i
  *                results are rounded once
  *   workspace    >= fs_token_logprobs_backward_workspace_bytes(B, D, V) bytes
  *                (0 for invalid sizes).  It holds dz for a slice of the
- *                vocabulary at a time (up to 1 GiB), partial sums of grad_h in
+ *                vocabulary at a time (up to 1 GiB, or 512 bytes per row if
+ *                that is more), partial sums of grad_h in
  *                fp32 (up to 512 MiB, or one [B][D] if that is more) and six
  *                bytes per element of h; contents on entry ignored
  * B == 0 sets grad_W to 0. */
@@ -416,7 +417,7 @@ FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_
 /* Losses over a packed batch: sequence s holds tokens [cu_seqlens[s],
  * cu_seqlens[s+1]) of the flat token arrays (int32 [n_sequences + 1], device,
  * non-decreasing; offsets outside [0, n_tokens] are clamped to it).  Sequences
- * may be empty.  mask is uint8 [n_tokens], device, or NULL: a token counts
+ * may be empty; n_tokens up to 2^31 - 1.  mask is uint8 [n_tokens], device, or NULL: a token counts
  * where it is nonzero.  Tokens that do not count get gradient 0 and their
  * other entries are not used (they may be NaN).  Entries of out_grad before
  * the first and behind the last sequence are set to 0 with zero_outside, else

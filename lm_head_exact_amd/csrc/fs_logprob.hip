@@ -13,8 +13,8 @@ namespace {
 // Block-tiled kernel: any B and D.  Grid of vocabulary tiles by token tiles; a
 // tile's logits become one pair (maximum, sum of exponentials) per token in
 // registers, and the pairs of its waves one in LDS.  1777 tokens on 151936 rows
-// of 5120: 2.2 to 2.4 ms, 1.15 to 1.25 PFLOP/s, bound by the board's power as
-// the tile loop is (a bf16 library product of that size: 1.4 PFLOP/s, without
+// of 5120: 2.2 to 2.4 ms, 1.15 to 1.25 PFLOP/s, at 1.8 GHz as the tile loop
+// runs there (a bf16 library product of that size: 1.4 PFLOP/s, without
 // the reduction and with 540 MB of logits written).
 // ---------------------------------------------------------------------------
 template <class T>

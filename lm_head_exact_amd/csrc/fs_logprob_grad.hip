@@ -12,20 +12,22 @@
 //
 // dz (B x V) is made in bf16, one slice of the vocabulary at a time, from the
 // logits recomputed on chip, and both products read it back from the
-// workspace.  MFMA takes bf16 operands, so every dz is rounded once (2^-9
-// relative), but for the targets': they are what most of a gradient is made
+// workspace.  MFMA takes bf16 operands, so every dz is rounded once (by up to
+// 2^-8 of it, 1.7e-3 root mean square), but for the targets': they are what most of a gradient is made
 // of, a rounding of them would not average out, and there is one per row.  dz
 // holds zero there, and their terms are added in fp32 where the results are
 // rounded: g/T (1 - p) W_target to a row of dh, g/T (1 - p) h to a target's
 // row of dW (the product leaves those rows in fp32 on the side).  Measured
 // against fp64 (Frobenius norm): 1.7e-3 with 2.4e-3 before, bf16 results alone
-// being 1.7e-3.
+// being 1.7e-3; up to 2.0e-3 where few of the batch's targets lie in the rows of
+// W.  (A second bf16 for what the first leaves would halve the rate of both
+// products.)
 //
 // Three matrix products of 2 B V D operations each bound the call for batches
 // of training; a batch of a few rows is bound by reading W twice and writing
 // dW.  4096 tokens, of which three quarters count, on 128256 rows of 4096:
-// logits 2.5 to 2.7 ms, dW 2.6, dh 2.5 (1.2 to 1.3 PFLOP/s each), everything
-// else 0.11 ms.  One token there: 175, 230 and 168 us (6.0, 4.6 and 6.2 TB/s).
+// logits 2.4 to 2.8 ms, dW 2.5 to 2.7, dh 2.4 to 2.5 (1.2 to 1.3 PFLOP/s each),
+// everything else 0.11 ms.  One token there: 175, 230 and 168 us (6.0, 4.6 and 6.2 TB/s).
 #include <algorithm>
 #include <cmath>
 

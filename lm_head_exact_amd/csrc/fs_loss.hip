@@ -15,7 +15,7 @@
 // 13 to 21 bytes and a few dozen operations: launches and memory latency bound
 // a batch of any usual size, not bandwidth (8 answers of 100 tokens: 9.5 us
 // policy, 8.3 preference, in one block; 512 answers of 1900 tokens: 4 us
-// counts, 16 terms, 4 sums, and 6 sums, 7 gradients).
+// counts, 15 terms, 4 sums, and 7 sums, 7 gradients).
 #include <cmath>
 
 #include "fs_host.hpp"

@@ -142,7 +142,8 @@ inline int tile_tokens(int32_t B) { return B <= 64 ? 64 : B <= 128 ? 128 : 256; 
 // 252, 504 and 1008 of 128 x 128 119, 138 and 252.  256 x 128 is given a little
 // more: of two alike, 256 x 256 reads less.  (256 tokens there: 91 us by
 // 256 x 64, 117 by 128 x 128; 768 tokens: 194 us by 256 x 256, 222 by 128 x 128;
-// 1024 tokens on 1000 rows: 90 us by 128 x 128, 37 by 64 x 64.)
+// 1024 tokens on 1000 rows: 90 us by 128 x 128, 37 by 64 x 64.)  The costs do not
+// see D: where it is small a block's prologue and epilogue weigh more than there.
 struct TileShape {
   LogitsTile tile;
   int32_t rows, tokens;

@@ -200,8 +200,9 @@ struct Tile {
   // the next one (which may then be read).  The direct loads of tile kt + S
   // go out right behind that barrier and have S - 1 tiles of time to land.
   // 4096 x 4096 x 128256 in any of the three pairs of layouts: 1.25 to 1.3
-  // PFLOP/s.  The board's power bounds it: the clock falls to 2.0 GHz with the
-  // matrix cores 60% busy.  Of copies that skip one part each, the one without
+  // PFLOP/s.  Under it the clock falls from 2.4 GHz to 1.8 or 1.9, as under every
+  // product that draws the board's 1400 W, with the matrix cores busy 62 to 70%
+  // of its cycles.  Of copies that skip one part each, the one without
   // the direct loads runs at 1.6, without the LDS reads at 1.35, without both
   // at 1.8 PFLOP/s; with every load an L2 hit it is 1.38.
   __device__ __forceinline__ static void run(const Operand& A, const Operand& B, int a0, int b0,
