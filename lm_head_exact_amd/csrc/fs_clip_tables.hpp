@@ -12,7 +12,7 @@ constexpr int kVec = 16;                // bytes a lane loads at once
 constexpr int kUnroll = 4;
 // Bytes of input per block: one round of loads, which streams best when written
 // back (16 KB 596 us against 645 us with 64 KB); the norm's blocks take four
-// times that of many tensors, to leave fewer sums.
+// times that of much input, to leave fewer sums.
 constexpr int64_t kChunkBytes = kClipThreads * kVec * kUnroll;
 constexpr int kTable = 96;              // 96 * 32 + ... bytes: below the 4 KB of kernel arguments
 constexpr int32_t kMaxTensors = 65536;

@@ -11,7 +11,6 @@ import pytest
 import torch
 
 import lm_head_exact_amd as fs
-import training_ref as ref
 from test_gpu_token_logprobs import check_forward, dev, make
 
 pytestmark = pytest.mark.gpu
