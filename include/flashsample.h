@@ -414,6 +414,45 @@ FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_
                                             void* workspace, size_t workspace_bytes,
                                             void* stream);
 
+/* Softmax cross entropy of the LM head with its gradients, with no logits in
+ * memory.  With z_b = W h_b, lse = log sum_v exp z_v, p = exp(z - lse), y the
+ * target, s = label_smoothing and l = z_loss, a row's loss is
+ *   (1 - s) (lse - z_y) + s (lse - mean_v z_v) + l lse^2
+ * and u = grad_scale (mean: over the number of rows that have a target)
+ *   dz_v = u ((1 + 2 l lse) p_v - s / V - [v = y] (1 - s))
+ *   grad_h = dz W,  grad_W = dz^T h
+ * Rows without a target (negative, as -100) have loss and gradient 0 and count
+ * in no mean; their h is not used (it may be NaN).  A target of V or more has
+ * probability 0: its row's loss is +inf, and the gradient that of the other
+ * entries.
+ *   h, W         bf16 [B][D] and [V][D], D % 8 == 0: sizes as
+ *                fs_token_logprobs_backward takes them; the whole vocabulary
+ *   targets      int32 [B], device
+ *   label_smoothing in [0, 1], z_loss >= 0, grad_scale: finite
+ *   mean         nonzero: the loss is the mean over the rows that have a target
+ *                (0 without any), zero: their sum
+ *   out_stats    fp32 [3]: the loss; the mean of lse - z_y (its exp is the
+ *                perplexity); the mean of lse^2
+ *   out_losses   fp32 [B]: every row's loss
+ *   grad_h, grad_W  bf16 [B][D], [V][D], the gradient of grad_scale * loss;
+ *                either or both may be NULL (not wanted).  dz is rounded to bf16
+ *                between the products (but for the targets' own, which stay
+ *                fp32), sums are fp32, results are rounded once
+ *   workspace    >= fs_cross_entropy_workspace_bytes(B, D, V, grads) bytes (0 for
+ *                invalid sizes), grads nonzero where a gradient is wanted.  It
+ *                holds two bytes per row and vocabulary entry, up to 4 GiB (a
+ *                larger batch takes a slice of the vocabulary at a time and makes
+ *                the logits twice), and what fs_token_logprobs_backward holds
+ *                beside dz; contents on entry ignored
+ * Logits of -inf have probability 0; NaN or +inf among a row's give NaN.  B == 0
+ * sets the stats and grad_W to 0. */
+FS_API size_t fs_cross_entropy_workspace_bytes(int32_t B, int32_t D, int32_t V, int32_t grads);
+FS_API fs_status fs_cross_entropy(const void* h, const void* W, int32_t B, int32_t D, int32_t V,
+                                  const int32_t* targets, double label_smoothing, double z_loss,
+                                  int32_t mean, double grad_scale, float* out_stats,
+                                  float* out_losses, void* grad_h, void* grad_W, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 /* Losses over a packed batch: sequence s holds tokens [cu_seqlens[s],
  * cu_seqlens[s+1]) of the flat token arrays (int32 [n_sequences + 1], device,
  * non-decreasing; offsets outside [0, n_tokens] are clamped to it).  Sequences

@@ -15,7 +15,8 @@ _BINDING_NAMES = ("sample", "sample_partial", "merge", "sample_partial_lse", "me
                   "sample_groups_lse", "groups_workspace_bytes",
                   "token_logprobs", "token_logprobs_workspace_bytes", "token_logprobs_backward",
                   "token_logprobs_backward_workspace_bytes", "policy_loss", "preference_loss",
-                  "loss_workspace_bytes", "clip_grad_norm")
+                  "loss_workspace_bytes", "clip_grad_norm", "cross_entropy",
+                  "cross_entropy_workspace_bytes")
 __all__ = list(_BINDING_NAMES)
 
 

@@ -92,6 +92,9 @@ def lib():
         ("fs_token_logprobs_backward_workspace_bytes", [i32, i32, i32], sz),
         ("fs_token_logprobs_backward", [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp,
                                         sz, vp], ctypes.c_int),
+        ("fs_cross_entropy_workspace_bytes", [i32, i32, i32, i32], sz),
+        ("fs_cross_entropy", [vp, vp, i32, i32, i32, vp, f64, f64, i32, f64, vp, vp, vp, vp, vp, sz,
+                              vp], ctypes.c_int),
         ("fs_loss_workspace_bytes", [i32, i32], sz),
         ("fs_policy_loss", [vp, vp, vp, vp, vp, vp, i32, i32, i32, f64, f64, f64, f64, ctypes.c_int,
                             ctypes.c_int, f64, i32, vp, vp, vp, sz, vp], ctypes.c_int),
@@ -794,6 +797,54 @@ def token_logprobs_backward(h: torch.Tensor, W: torch.Tensor, temperature: Optio
     return gh, gw
 
 
+def cross_entropy_workspace_bytes(B: int, D: int, V: int, grads: bool = True) -> int:
+    _int32(B, D, V)
+    return int(lib().fs_cross_entropy_workspace_bytes(B, D, V, int(grads)))
+
+
+def cross_entropy(h: torch.Tensor, W: torch.Tensor, targets: torch.Tensor,
+                  label_smoothing: float = 0.0, z_loss: float = 0.0, reduction: str = "mean",
+                  grad_scale: float = 1.0, need_h: bool = True, need_W: bool = True, out=None,
+                  workspace: Optional[torch.Tensor] = None):
+    """fs_cross_entropy of the head W (bf16 [V][D]) on hidden states h (bf16
+    [B][D]) and targets (int32 [B]; negative: the row has none): returns (stats
+    fp32 [3], losses fp32 [B], grad_h bf16 [B][D], grad_W bf16 [V][D]).  stats are
+    the loss (reduction "mean" or "sum" over the rows that have a target), their
+    mean negative log-probability and their mean squared log-sum-exp; the
+    gradients are those of grad_scale * loss.  need_h / need_W false: None in that
+    gradient's place, and without both the loss alone is computed.  Nothing
+    returned carries a graph (an h with one goes on by h.backward(grad_h), W by
+    W.grad = grad_W).  out: (stats, losses, grad_h, grad_W) to write into, each may
+    be None."""
+    _req(h, "h", torch.bfloat16, 2)
+    _req(W, "W", torch.bfloat16, 2)
+    B, D = h.shape
+    V = W.shape[0]
+    if W.shape[1] != D:
+        raise ValueError(f"h is B x {D} but W is V x {W.shape[1]}")
+    dev = h.device
+    if W.device != dev:
+        raise ValueError("all tensors must be on one device")
+    _row(targets, "targets", torch.int32, B, dev)
+    if targets is None:
+        raise TypeError("targets must be a tensor")
+    mean = _choice(_LOSS_REDUCTIONS, reduction, "reduction")
+    stats, losses, gh, gw = (None,) * 4 if out is None else out
+    stats = _out(stats, "stats", (3,), torch.float32, dev)
+    losses = _out(losses, "losses", (B,), torch.float32, dev)
+    gh = _out(gh, "grad_h", (B, D), torch.bfloat16, dev) if need_h else None
+    gw = _out(gw, "grad_W", (V, D), torch.bfloat16, dev) if need_W else None
+    ws = _workspace(workspace, cross_entropy_workspace_bytes(B, D, V, need_h or need_W), dev)
+    if out is not None or workspace is not None:
+        _apart((stats, losses, gh, gw, ws), (h, W, targets))
+    _call(lib().fs_cross_entropy, dev, _addr(h), _addr(W), B, D, V, _addr(targets), label_smoothing,
+          z_loss, mean, grad_scale, _addr(stats), _addr(losses), _addr(gh), _addr(gw), _addr(ws),
+          _nbytes(ws))
+    if out is not None:
+        _changed(stats, losses, gh, gw)
+    return stats, losses, gh, gw
+
+
 def loss_workspace_bytes(n_sequences: int, n_tokens: int) -> int:
     _int32(n_sequences, n_tokens)
     return int(lib().fs_loss_workspace_bytes(n_sequences, n_tokens))
@@ -818,6 +869,7 @@ def _sequences(logprob, cu_seqlens, mask, **rows):
 
 
 _KL = {"k1": 1, "k2": 2, "k3": 3}
+_LOSS_REDUCTIONS = {"sum": 0, "mean": 1}
 _REDUCTIONS = {"token": 0, "sequence": 1}
 _PREFERENCES = {"sigmoid": 0, "hinge": 1, "ipo": 2}
 

@@ -28,48 +28,13 @@
 // dW.  4096 tokens, of which three quarters count, on 128256 rows of 4096:
 // logits 2.4 to 2.8 ms, dW 2.5 to 2.7, dh 2.4 to 2.5 (1.2 to 1.3 PFLOP/s each),
 // everything else 0.11 ms.  One token there: 175, 230 and 168 us (6.0, 4.6 and 6.2 TB/s).
-#include <algorithm>
 #include <cmath>
 
-#include "fs_host.hpp"
-#include "fs_score.hpp"
+#include "fs_grad.hpp"
 #include "fs_sampler.hpp"
 
 namespace fs {
 namespace {
-
-// Per row that has a target, in order.
-struct RowTerm {
-  float c;       // log2(e) / T
-  float lse2;    // log2(e) * lse
-  float coef;    // -g / T
-  float target;  // g / T * (1 - p_target)
-};
-
-struct GradArgs {
-  const __bf16 *h, *W;
-  int32_t B, D, V, vocab_offset;
-  const float *temperature, *logprob, *lse, *grad;
-  const int32_t* ids;
-  __bf16 *dh, *dW;    // either may be null
-  // workspace
-  int32_t* count;     // [2]: rows with a target; parts of the vocabulary for dh
-  int32_t* slot;      // [B]: their place among them, or -1
-  int32_t* row;       // [Bp]: the inverse
-  int32_t* loc;       // [Bp]: target's row of W, or -1
-  RowTerm* term;      // [Bp]
-  __bf16* hz;         // [Bp][Dp]: their hidden states, zeros behind them
-  __bf16* dz;         // [Bp][ldz]
-  float* slab;        // [max_splits][B][D] or null
-  // targets by tile of 256 vocabulary rows
-  int32_t* first;     // [V]: first place whose target the row is, or -1
-  int32_t* list;      // [Bp]: places that have a target here, by tile
-  int2* tile;         // [tiles]: begin and end in `list`
-  float* side;        // [Bp][D]: dW rows of targets, at their first place
-  int32_t Dp, Bp, ldz;
-  int32_t v0, nv;     // the slice: rows v0 .. v0 + nv of W
-  int32_t max_splits, hidden_tb, first_slice;
-};
 
 // A row counts where it has a token; a token of another shard still gives
 // every row of this one a gradient.
@@ -165,31 +130,23 @@ __global__ __launch_bounds__(256) void grad_gather_kernel(GradArgs a) {
   RowTerm t = {0.0f, 0.0f, 0.0f, 0.0f};
   int loc = -1;
   if (b < a.B) {
-    const float inv_t = score_inv_t(a.temperature, b);
-    const float g = a.grad[b] * inv_t;
-    t.c = inv_t * 1.44269504088896341f;
-    t.lse2 = a.lse[b] * 1.44269504088896341f;
-    t.coef = -g;
     loc = target_row(a.ids[b], a.vocab_offset, a.V);
-    t.target = loc >= 0 ? -expm1f(a.logprob[b]) * g : 0.0f;
+    if (a.grad != nullptr) {
+      const float inv_t = score_inv_t(a.temperature, b);
+      const float g = a.grad[b] * inv_t;
+      t.c = inv_t * 1.44269504088896341f;
+      t.lse2 = a.lse[b] * 1.44269504088896341f;
+      t.coef = -g;
+      t.target = loc >= 0 ? -expm1f(a.logprob[b]) * g : 0.0f;
+    }
   }
   a.term[at] = t;
   a.loc[at] = loc;
 }
 
-__device__ __forceinline__ uint64_t pack_bf16(float x0, float x1, float x2, float x3) {
-  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-  const bf16x4 v = {static_cast<__bf16>(x0), static_cast<__bf16>(x1), static_cast<__bf16>(x2),
-                    static_cast<__bf16>(x3)};
-  return __builtin_bit_cast(uint64_t, v);
-}
-
 // The places that have a target in one tile of 256 vocabulary rows, in order,
 // and each row's first one.  Every block reads all targets, twice: B ints
 // against the B * 256 * D products of the tile (3 to 6 us).
-constexpr int kTargetTile = 256;
-constexpr int kTargetThreads = 1024;
-
 __global__ __launch_bounds__(kTargetThreads) void grad_targets_kernel(GradArgs a) {
   constexpr int kWaves = kTargetThreads / kWave;
   __shared__ int32_t s_before[kWaves], s_in[kWaves];
@@ -488,64 +445,6 @@ __global__ __launch_bounds__(GROUPS * kWave) void grad_slabs_kernel(GradArgs a) 
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-constexpr int32_t kMaxGradB = 1 << 22;
-constexpr int32_t kMaxGradD = 1 << 20;
-// dz of one slice of the vocabulary.
-constexpr int64_t kSliceBytes = int64_t{1} << 30;
-constexpr int32_t kMaxSlice = 1 << 18;
-
-int32_t target_tiles(int32_t V) {
-  return static_cast<int32_t>((static_cast<int64_t>(V) + kTargetTile - 1) / kTargetTile);
-}
-
-struct GradPlan {
-  int32_t Bp, Dp, slice, splits, TB;
-  bool slabs;
-  size_t count, slot, row, loc, term, hz, dz, slab, first, list, tile, side, total;
-  GradPlan(int32_t B, int32_t D, int32_t V) {
-    TB = tile_tokens(B);
-    Bp = static_cast<int32_t>(round_up(B, 256));
-    Dp = static_cast<int32_t>(round_up(D, 64));
-    int64_t s = kSliceBytes / (2 * static_cast<int64_t>(Bp)) / 256 * 256;
-    s = s < 256 ? 256 : s > kMaxSlice ? kMaxSlice : s;
-    const int64_t whole = static_cast<int64_t>(round_up(V, 256));
-    if (s >= whole) {
-      s = whole;
-    } else {  // equal slices
-      const int64_t k = (whole + s - 1) / s;
-      s = static_cast<int64_t>(round_up((whole + k - 1) / k, 256));
-    }
-    slice = static_cast<int32_t>(s);
-    // at most as many parts for dh as make four rounds of its tiles, of at least
-    // 256 vocabulary rows, with slabs of no more than 512 MiB
-    const int64_t tiles = static_cast<int64_t>((B + TB - 1) / TB) * ((D + 255) / 256);
-    const int64_t rows = slice < V ? slice : V;
-    int64_t p = (1024 + tiles - 1) / tiles;
-    p = std::min({p, rows / 256, (int64_t{512} << 20) / (4 * static_cast<int64_t>(B) * D)});
-    splits = static_cast<int32_t>(p < 1 ? 1 : p);
-    slabs = splits > 1 || slice < V;
-    size_t at = 0;
-    auto take = [&](size_t bytes) {
-      const size_t o = at;
-      at += round_up(bytes, 256);
-      return o;
-    };
-    count = take(8);
-    slot = take(4ull * B);
-    row = take(4ull * Bp);
-    loc = take(4ull * Bp);
-    term = take(sizeof(RowTerm) * Bp);
-    hz = take(2ull * Bp * Dp);
-    dz = take(2ull * Bp * slice);
-    slab = take(slabs ? 4ull * splits * B * D : 0);
-    first = take(4ull * V);
-    list = take(4ull * Bp);
-    tile = take(sizeof(int2) * target_tiles(V));
-    side = take(4ull * Bp * D);
-    total = at;
-  }
-};
-
 unsigned padded_grid(int64_t tiles) { return static_cast<unsigned>((tiles + 7) / 8 * 8); }
 
 // K-major operands take ring slots of 32 k, four or five deep (their rows are as
@@ -622,31 +521,74 @@ hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
 }
 
 hipError_t run_grad(GradArgs& a, const GradPlan& p, hipStream_t s) {
-  grad_rows_kernel<<<1, kScanThreads, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
+  hipError_t e = launch_grad_rows(a, s);
   if (e != hipSuccess) return e;
-  grad_gather_kernel<<<a.B + 256, 256, 0, s>>>(a);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (a.dW != nullptr) {
-    grad_targets_kernel<<<target_tiles(a.V), kTargetThreads, 0, s>>>(a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
+  if ((e = launch_grad_targets(a, s)) != hipSuccess) return e;
   for (int32_t v0 = 0; v0 < a.V; v0 += p.slice) {
     a.v0 = v0;
     a.nv = a.V - v0 < p.slice ? a.V - v0 : p.slice;
     a.first_slice = v0 == 0;
     if (a.B > 0) e = launch_logits(a, s);
     if (e != hipSuccess) return e;
-    if (a.dW != nullptr && (e = launch_weights(a, s)) != hipSuccess) return e;
-    if (a.dh != nullptr && (e = launch_hidden(a, s)) != hipSuccess) return e;
+    if ((e = launch_grad_products(a, s)) != hipSuccess) return e;
     if (a.V - v0 <= p.slice) break;  // (v0 + slice may not fit in 32 bits)
   }
+  return launch_grad_finish(a, s);
+}
+
+}  // namespace
+
+void grad_workspace(GradArgs& a, const GradPlan& p, char* ws) {
+  a.count = reinterpret_cast<int32_t*>(ws + p.count);
+  a.slot = reinterpret_cast<int32_t*>(ws + p.slot);
+  a.row = reinterpret_cast<int32_t*>(ws + p.row);
+  a.loc = reinterpret_cast<int32_t*>(ws + p.loc);
+  a.term = reinterpret_cast<RowTerm*>(ws + p.term);
+  a.hz = reinterpret_cast<__bf16*>(ws + p.hz);
+  a.dz = reinterpret_cast<__bf16*>(ws + p.dz);
+  a.slab = p.slabs ? reinterpret_cast<float*>(ws + p.slab) : nullptr;
+  a.first = reinterpret_cast<int32_t*>(ws + p.first);
+  a.list = reinterpret_cast<int32_t*>(ws + p.list);
+  a.tile = reinterpret_cast<int2*>(ws + p.tile);
+  a.side = reinterpret_cast<float*>(ws + p.side);
+  a.Dp = p.Dp;
+  a.Bp = p.Bp;
+  a.ldz = p.slice;
+  a.v0 = a.nv = 0;
+  a.max_splits = p.splits;
+  a.hidden_tb = p.TB;
+  a.first_slice = 1;
+}
+
+hipError_t launch_grad_rows(const GradArgs& a, hipStream_t s) {
+  grad_rows_kernel<<<1, kScanThreads, 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  grad_gather_kernel<<<a.B + 256, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_targets(const GradArgs& a, hipStream_t s) {
+  if (a.dW == nullptr) return hipSuccess;
+  grad_targets_kernel<<<target_tiles(a.V), kTargetThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_products(const GradArgs& a, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  if (a.dW != nullptr) e = launch_weights(a, s);
+  if (e == hipSuccess && a.dh != nullptr) e = launch_hidden(a, s);
+  return e;
+}
+
+hipError_t launch_grad_finish(const GradArgs& a, hipStream_t s) {
+  hipError_t e = hipSuccess;
   if (a.dW != nullptr && a.B > 0) {
     const int chunks = (a.D + 2047) / 2048;
     grad_target_rows_kernel<<<dim3(a.B, chunks < 64 ? chunks : 64), 256, 0, s>>>(a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  if (a.dh != nullptr && p.slabs) {
+  if (a.dh != nullptr && a.slab != nullptr) {
     const dim3 grid(a.B, (a.D + 4 * kWave - 1) / (4 * kWave));
     // few blocks share out the slabs (4 rows of 1024: the call's dh 35.0 us by
     // sixteen groups, 39.3 by one), many need not (300 rows of 4096: 256, 243)
@@ -673,12 +615,6 @@ bool grad_grids_fit(int32_t B, int32_t D, int32_t V, const GradPlan& p, bool dh,
                   grid_fits(target_tiles(V), kTargetThreads)));
 }
 
-bool grad_sizes_ok(int32_t B, int32_t D, int32_t V) {
-  return B >= 0 && D >= 8 && D % 8 == 0 && V >= 1 && B <= kMaxGradB && D <= kMaxGradD &&
-         V <= kMaxVocab;
-}
-
-}  // namespace
 }  // namespace fs
 
 extern "C" {
@@ -740,25 +676,7 @@ FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_
   a.ids = token_ids;
   a.dh = B > 0 ? static_cast<__bf16*>(grad_h) : nullptr;
   a.dW = static_cast<__bf16*>(grad_W);
-  a.count = reinterpret_cast<int32_t*>(ws + p.count);
-  a.slot = reinterpret_cast<int32_t*>(ws + p.slot);
-  a.row = reinterpret_cast<int32_t*>(ws + p.row);
-  a.loc = reinterpret_cast<int32_t*>(ws + p.loc);
-  a.term = reinterpret_cast<RowTerm*>(ws + p.term);
-  a.hz = reinterpret_cast<__bf16*>(ws + p.hz);
-  a.dz = reinterpret_cast<__bf16*>(ws + p.dz);
-  a.slab = p.slabs ? reinterpret_cast<float*>(ws + p.slab) : nullptr;
-  a.first = reinterpret_cast<int32_t*>(ws + p.first);
-  a.list = reinterpret_cast<int32_t*>(ws + p.list);
-  a.tile = reinterpret_cast<int2*>(ws + p.tile);
-  a.side = reinterpret_cast<float*>(ws + p.side);
-  a.Dp = p.Dp;
-  a.Bp = p.Bp;
-  a.ldz = p.slice;
-  a.v0 = a.nv = 0;
-  a.max_splits = p.splits;
-  a.hidden_tb = p.TB;
-  a.first_slice = 1;
+  grad_workspace(a, p, ws);
   const hipError_t e = run_grad(a, p, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? FS_OK : hip_fail(e, "log-probability gradient launch");
 }
