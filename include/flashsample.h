@@ -336,6 +336,79 @@ FS_API fs_status fs_sample_unfused(const void* h, const void* W, int32_t B, int3
                             float* out_maxval, void* workspace, size_t workspace_bytes,
                             void* stream);
 
+/* ---- the LM head in 8-bit floating point ----
+ *
+ * Weights and hidden states as e4m3 values (no infinities, largest 448) with a
+ * scale for each block of 128 columns -- and of 128 rows, for W --, products in
+ * 8 bits, sums in fp32: half the bytes of a decode step and up to twice the rate
+ * of a batch.  A scale is the power of two 2^e with the least e >= -110 for which
+ * no finite entry of its block exceeds 448 * 2^e (e = 0 for a block of zeros),
+ * stored as the byte e + 127 (e8m0); values are rounded to nearest even; entries
+ * that are not finite become NaN.  The last block of a row or of the vocabulary
+ * may be short.
+ *   z[b][v] = sum over blocks k of  2^(eh[b][k] + eW[v / 128][k]) *
+ *             sum_{d in k} qh[b][d] qW[v][d]
+ * h is given in bf16 and quantised by the call.  Up to 32 rows (D up to 5120; 16
+ * rows up to 8192) the products are exact and summed in fp32; more rows take the
+ * 8-bit matrix instructions, which round a product to 13 bits below the largest
+ * of eight neighbouring ones: 1.5e-5 of the logits' spread (but for the tokens' own
+ * logits in fs_token_logprobs_fp8, which are exact products there too).
+ *   D            a multiple of 64 up to 16384; V up to 2^31 - 513; B up to 2^22
+ *                (FS_ERR_UNSUPPORTED beyond, and where a launch would hold 2^32
+ *                threads)
+ *   W_packed     the values in fragment order (below), 16-byte aligned
+ *   W_scale      bytes [ceil(V / 128)][ceil(D / 128)], device
+ *   workspace    >= fs_fp8_workspace_bytes(B, D, V) bytes (0 for invalid sizes);
+ *                contents on entry ignored
+ * NaN or infinite entries of h or W give NaN in the logits that they enter (for
+ * the sampler undefined ids).  All calls are asynchronous on `stream`, allocate
+ * nothing, give equal bits for equal calls and may be captured into graphs; calls
+ * that overlap need distinct workspaces and outputs.  Outputs and workspaces
+ * overlap neither one another nor an input. */
+
+/* Quantises W (bf16 [V][D], 16-byte aligned).
+ *   packed       zero: out_q is e4m3 [V][D] row-major (D % 8 == 0); nonzero: in the
+ *                fragment order that the products read (D % 64 == 0), rows in
+ *                groups of 16 and 64 columns at a time: byte
+ *                ((g * D/64 + s) * 64 + l) * 16 + j holds
+ *                W[16 g + l mod 16][64 s + 16 (l / 16) + j], zero past row V
+ *   out_q        16-byte aligned, q_bytes >= fs_fp8_weights_bytes(V, D, packed)
+ *                (0 for invalid sizes)
+ *   out_scale    bytes [ceil(V / 128)][ceil(D / 128)]
+ * fs_pack_weights_fp8 takes row-major values (a checkpoint's, with scales of the
+ * above kind) into fragment order. */
+FS_API size_t fs_fp8_weights_bytes(int32_t V, int32_t D, int32_t packed);
+FS_API fs_status fs_quantize_weights_fp8(const void* W, int32_t V, int32_t D, int32_t packed,
+                                         void* out_q, size_t q_bytes, void* out_scale,
+                                         void* stream);
+FS_API fs_status fs_pack_weights_fp8(const void* q, int32_t V, int32_t D, void* out_packed,
+                                     size_t packed_bytes, void* stream);
+
+FS_API size_t fs_fp8_workspace_bytes(int32_t B, int32_t D, int32_t V);
+
+/* The logits: out_logits [B] rows of V, row_pitch elements apart (>= V; what lies
+ * between rows is left as it is), bf16 (rounded once) or with out_fp32 nonzero
+ * fp32.  Rows that start 16-byte aligned are written fastest. */
+FS_API fs_status fs_logits_fp8(const void* h, const void* W_packed, const void* W_scale, int32_t B,
+                               int32_t D, int32_t V, int32_t out_fp32, void* out_logits,
+                               int64_t row_pitch, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* fs_token_logprobs on the 8-bit head: same arguments and outputs otherwise. */
+FS_API fs_status fs_token_logprobs_fp8(const void* h, const void* W_packed, const void* W_scale,
+                                       int32_t B, int32_t D, int32_t V, int32_t vocab_offset,
+                                       const float* temperature, const int32_t* token_ids,
+                                       float* out_logprob, float* out_lse, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/* fs_sample on the 8-bit head: same noise field and outputs; vocab_offset a
+ * multiple of 4.  Its (score, id) pairs of shards merge with fs_merge. */
+FS_API fs_status fs_sample_fp8(const void* h, const void* W_packed, const void* W_scale, int32_t B,
+                               int32_t D, int32_t V, int32_t vocab_offset,
+                               const float* temperature, uint64_t seed, uint64_t step,
+                               int32_t* out_ids, float* out_maxval, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* ---- training on sampled tokens ----
  *
  * What a user does with the tokens that the samplers above return: score them

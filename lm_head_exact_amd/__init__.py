@@ -16,7 +16,8 @@ _BINDING_NAMES = ("sample", "sample_partial", "merge", "sample_partial_lse", "me
                   "token_logprobs", "token_logprobs_workspace_bytes", "token_logprobs_backward",
                   "token_logprobs_backward_workspace_bytes", "policy_loss", "preference_loss",
                   "loss_workspace_bytes", "clip_grad_norm", "cross_entropy",
-                  "cross_entropy_workspace_bytes")
+                  "cross_entropy_workspace_bytes", "quantize_weights_fp8", "pack_weights_fp8",
+                  "fp8_workspace_bytes", "logits_fp8", "token_logprobs_fp8", "sample_fp8")
 __all__ = list(_BINDING_NAMES)
 
 

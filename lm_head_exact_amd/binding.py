@@ -92,6 +92,15 @@ def lib():
         ("fs_token_logprobs_backward_workspace_bytes", [i32, i32, i32], sz),
         ("fs_token_logprobs_backward", [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp,
                                         sz, vp], ctypes.c_int),
+        ("fs_fp8_weights_bytes", [i32, i32, i32], sz),
+        ("fs_quantize_weights_fp8", [vp, i32, i32, i32, vp, sz, vp, vp], ctypes.c_int),
+        ("fs_pack_weights_fp8", [vp, i32, i32, vp, sz, vp], ctypes.c_int),
+        ("fs_fp8_workspace_bytes", [i32, i32, i32], sz),
+        ("fs_logits_fp8", [vp, vp, vp, i32, i32, i32, i32, vp, i64, vp, sz, vp], ctypes.c_int),
+        ("fs_token_logprobs_fp8", [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp],
+         ctypes.c_int),
+        ("fs_sample_fp8", [vp, vp, vp, i32, i32, i32, i32, vp, u64, u64, vp, vp, vp, sz, vp],
+         ctypes.c_int),
         ("fs_cross_entropy_workspace_bytes", [i32, i32, i32, i32], sz),
         ("fs_cross_entropy", [vp, vp, i32, i32, i32, vp, f64, f64, i32, f64, vp, vp, vp, vp, vp, sz,
                               vp], ctypes.c_int),
@@ -1009,3 +1018,161 @@ def clip_grad_norm(grads, max_norm: float, out=None, norm: Optional[torch.Tensor
     if out is not None or max_norm != math.inf:  # (an infinite limit in place: the norm alone)
         torch.autograd.graph.increment_version(outs)
     return norm
+
+
+# ---- the LM head in 8-bit floating point ----
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def quantize_weights_fp8(W: torch.Tensor, packed: bool = True, out=None):
+    """fs_quantize_weights_fp8 of W (bf16 [V][D]): returns (values, scales).  The
+    scales are powers of two, one per block of 128 x 128 (float8_e8m0fnu [ceil(V /
+    128)][ceil(D / 128)]); the values float8_e4m3fn, in the fragment order that
+    logits_fp8, sample_fp8 and token_logprobs_fp8 read (1-D; D % 64 == 0), or with
+    packed false row-major [V][D].  out: (values, scales) to write into."""
+    _req(W, "W", torch.bfloat16, 2)
+    V, D = W.shape
+    _int32(V, D)
+    dev = W.device
+    need = int(lib().fs_fp8_weights_bytes(V, D, int(packed)))
+    if need == 0 and V > 0:
+        _check(lib().fs_quantize_weights_fp8(None, V, D, int(packed), None, 0, None, None))
+    q, scale = (None, None) if out is None else out
+    q = _out(q, "values", (need,) if packed else (V, D), _E4M3, dev)
+    scale = _out(scale, "scales", (_blocks(V), _blocks(D)), _E8M0, dev)
+    if out is not None:
+        _apart((q, scale), (W,))
+    _call(lib().fs_quantize_weights_fp8, dev, _addr(W), V, D, int(packed), _addr(q), _nbytes(q),
+          _addr(scale))
+    if out is not None:
+        _changed(q, scale)
+    return q, scale
+
+
+def pack_weights_fp8(q: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """fs_pack_weights_fp8: row-major e4m3 weights [V][D] in the fragment order of
+    the 8-bit products (once, as at model load)."""
+    _req(q, "q", _E4M3, 2)
+    V, D = q.shape
+    _int32(V, D)
+    given, need = out, int(lib().fs_fp8_weights_bytes(V, D, 1))
+    if need == 0:
+        _check(lib().fs_pack_weights_fp8(None, V, D, None, 0, None))
+    out = _out(out, "out", (need,), _E4M3, q.device)
+    if given is not None:
+        _apart((out,), (q,))
+    _call(lib().fs_pack_weights_fp8, q.device, _addr(q), V, D, _addr(out), _nbytes(out))
+    if given is not None:
+        _changed(out)
+    return out
+
+
+def fp8_workspace_bytes(B: int, D: int, V: int) -> int:
+    _int32(B, D, V)
+    return int(lib().fs_fp8_workspace_bytes(B, D, V))
+
+
+def _fp8_head(h, W_packed, W_scale, V, vocab_offset, workspace):
+    """Checks of the 8-bit products: (device, B, D, workspace)."""
+    _req(h, "h", torch.bfloat16, 2)
+    if isinstance(W_packed, torch.Tensor) and W_packed.dim() == 2:
+        raise ValueError("W_packed must be in fragment order (quantize_weights_fp8, pack_weights_fp8)")
+    _req(W_packed, "W_packed", _E4M3, 1)
+    _req(W_scale, "W_scale", _E8M0, 2)
+    B, D = h.shape
+    _int32(B, D, V, vocab_offset)
+    need = int(lib().fs_fp8_weights_bytes(V, D, 1))
+    if need and W_packed.numel() != need:
+        raise ValueError(f"W_packed holds {W_packed.numel()} bytes; {need} are those of {V} x {D}")
+    if V > 0 and D > 0 and tuple(W_scale.shape) != (_blocks(V), _blocks(D)):
+        raise ValueError(f"W_scale must have shape {(_blocks(V), _blocks(D))} (got {tuple(W_scale.shape)})")
+    dev = h.device
+    if W_packed.device != dev or W_scale.device != dev:
+        raise ValueError("all tensors must be on one device")
+    return dev, B, D, _workspace(workspace, fp8_workspace_bytes(B, D, V), dev)
+
+
+def logits_fp8(h: torch.Tensor, W_packed: torch.Tensor, W_scale: torch.Tensor, V: int,
+               dtype=torch.float32, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """fs_logits_fp8: logits [B][V] (fp32 or bf16) of hidden states h (bf16 [B][D],
+    quantised by the call) and the 8-bit head of quantize_weights_fp8.  out: a
+    tensor [B][V] of either type to write into, whose rows may lie further apart
+    than V.  Carries no graph."""
+    dev, B, D, ws = _fp8_head(h, W_packed, W_scale, V, 0, workspace)
+    given = out
+    if out is None:
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"dtype must be torch.float32 or torch.bfloat16 (got {dtype})")
+        out = torch.empty(B, V, dtype=dtype, device=dev)
+    else:
+        if not isinstance(out, torch.Tensor) or out.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("out must be an fp32 or bf16 tensor")
+        if tuple(out.shape) != (B, V) or out.device != dev:
+            raise ValueError(f"out must have shape {(B, V)} and be on h's device")
+        if (V > 1 and out.stride(1) != 1) or (B > 1 and out.stride(0) < V):
+            raise ValueError("out must have contiguous rows that do not overlap")
+    pitch = out.stride(0) if B > 1 else V
+    if given is not None or workspace is not None:
+        _apart_rows(out, ws, (h, W_packed, W_scale))
+    _call(lib().fs_logits_fp8, dev, _addr(h), _addr(W_packed), _addr(W_scale), B, D, V,
+          int(out.dtype == torch.float32), _addr(out), pitch, _addr(ws), _nbytes(ws))
+    if given is not None:
+        _changed(out)
+    return out
+
+
+def _apart_rows(out, ws, read):
+    """_apart for an output whose rows may lie apart: its whole span counts."""
+    n = out.numel() and (out.shape[0] - 1) * out.stride(0) + out.shape[1]
+    _apart((torch.as_strided(out, (n,), (1,)), ws), read)
+
+
+def token_logprobs_fp8(h: torch.Tensor, W_packed: torch.Tensor, W_scale: torch.Tensor, V: int,
+                       temperature: Optional[torch.Tensor], token_ids: torch.Tensor,
+                       vocab_offset: int = 0, out=None, workspace: Optional[torch.Tensor] = None):
+    """fs_token_logprobs_fp8: token_logprobs on the 8-bit head of
+    quantize_weights_fp8 (what a rollout stores when it samples with sample_fp8):
+    (logprob, lse), which carry no graph."""
+    dev, B, D, ws = _fp8_head(h, W_packed, W_scale, V, vocab_offset, workspace)
+    _row(temperature, "temperature", torch.float32, B, dev)
+    if token_ids is None:
+        raise TypeError("token_ids must be a tensor")
+    _row(token_ids, "token_ids", torch.int32, B, dev)
+    lp, lse = (None, None) if out is None else out
+    lp = _out(lp, "logprob", (B,), torch.float32, dev)
+    lse = _out(lse, "lse", (B,), torch.float32, dev)
+    if out is not None or workspace is not None:
+        _apart((lp, lse, ws), (h, W_packed, W_scale, temperature, token_ids))
+    _call(lib().fs_token_logprobs_fp8, dev, _addr(h), _addr(W_packed), _addr(W_scale), B, D, V,
+          int(vocab_offset), _addr(temperature), _addr(token_ids), _addr(lp), _addr(lse), _addr(ws),
+          _nbytes(ws))
+    if out is not None:
+        _changed(*out)
+    return lp, lse
+
+
+def sample_fp8(h: torch.Tensor, W_packed: torch.Tensor, W_scale: torch.Tensor, V: int,
+               temperature: torch.Tensor, seed: int, step: int, vocab_offset: int = 0, out=None,
+               workspace: Optional[torch.Tensor] = None):
+    """fs_sample_fp8: sample on the 8-bit head of quantize_weights_fp8, with the same
+    noise field: (ids int32 [B], winning scores fp32 [B])."""
+    dev, B, D, ws = _fp8_head(h, W_packed, W_scale, V, vocab_offset, workspace)
+    if temperature is None:
+        raise TypeError("temperature must be a tensor")
+    _row(temperature, "temperature", torch.float32, B, dev)
+    ids, val = (None, None) if out is None else out
+    ids = _out(ids, "ids", (B,), torch.int32, dev)
+    val = _out(val, "maxval", (B,), torch.float32, dev)
+    if out is not None or workspace is not None:
+        _apart((ids, val, ws), (h, W_packed, W_scale, temperature))
+    _call(lib().fs_sample_fp8, dev, _addr(h), _addr(W_packed), _addr(W_scale), B, D, V,
+          int(vocab_offset), _addr(temperature), seed, step, _addr(ids), _addr(val), _addr(ws),
+          _nbytes(ws))
+    if out is not None:
+        _changed(*out)
+    return ids, val

@@ -17,7 +17,10 @@ LIB = os.path.join(HERE, "libflashsample.so")
 SOURCES = ["fs_configs_dma_a.hip", "fs_configs_dma_b.hip", "fs_configs_dma_ntl.hip", "fs_configs_lds.hip",
            "fs_configs_small.hip", "fs_fused.hip", "fs_api.hip", "fs_unfused.hip",
            "fs_online.hip", "fs_pack.hip", "fs_loss.hip", "fs_clip.hip",
-           "fs_logprob.hip", "fs_logprob_grad.hip", "fs_cross_entropy.hip"]
+           "fs_logprob.hip", "fs_logprob_grad.hip", "fs_cross_entropy.hip",
+           "fs_fp8.hip", "fs_fp8_quantize.hip", "fs_fp8_stream_logits.hip", "fs_fp8_stream_scores.hip",
+           "fs_fp8_stream_samples.hip", "fs_fp8_tile_logits.hip", "fs_fp8_tile_scores.hip",
+           "fs_fp8_tile_samples.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

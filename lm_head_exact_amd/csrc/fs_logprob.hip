@@ -437,17 +437,22 @@ fs_status run_score(const char* who, const void* h, const void* W, int32_t B, in
     e = packed ? launch_tiles<kFrag>(a, s) : launch_tiles<kKC>(a, s);
   }
   if (e != hipSuccess) return hip_fail(e, "log-probability launch");
-  // wide rows of the partials for many tokens (8192 tokens on 32000 rows of 256:
-  // the call 205 us, 210 by eight), many threads per token for few
-  if (B >= 2048)
-    score_close_kernel<64><<<(B + 63) / 64, kCloseThreads, 0, s>>>(a, logprob, lse);
-  else
-    score_close_kernel<8><<<(B + 7) / 8, kCloseThreads, 0, s>>>(a, logprob, lse);
-  e = hipGetLastError();
+  e = launch_score_close(a, logprob, lse, s);
   return e == hipSuccess ? FS_OK : hip_fail(e, "log-probability merge launch");
 }
 
 }  // namespace
+
+hipError_t launch_score_close(const ScoreArgs& a, float* logprob, float* lse, hipStream_t stream) {
+  // wide rows of the partials for many tokens (8192 tokens on 32000 rows of 256:
+  // the call 205 us, 210 by eight), many threads per token for few
+  if (a.B >= 2048)
+    score_close_kernel<64><<<(a.B + 63) / 64, kCloseThreads, 0, stream>>>(a, logprob, lse);
+  else
+    score_close_kernel<8><<<(a.B + 7) / 8, kCloseThreads, 0, stream>>>(a, logprob, lse);
+  return hipGetLastError();
+}
+
 }  // namespace fs
 
 extern "C" {

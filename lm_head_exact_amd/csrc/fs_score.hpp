@@ -62,15 +62,16 @@ __device__ __forceinline__ float exponent_offset(float mz, float c) {
 }
 
 // Folds the wave's logits of one token into (m, s): z[i][r] is vocabulary row
-// row0 + 16 i + r + 4 kb.  All values are in registers, so the maximum comes
-// first and each logit costs one multiply-add and one exp2.  `plain` (the
-// same on all lanes): no row of the wave is outside [0, V) or any of its
-// tokens' target, so nothing is excluded.
-template <int MR, class Z>
+// row0 + QS i + r + 4 kb, kb the lane's place among the QS / 4 that share the
+// token (QS 16 for 16 x 16 MFMA tiles, 8 for 32 x 32).  All values are in
+// registers, so the maximum comes first and each logit costs one multiply-add and
+// one exp2.  `plain` (the same on all lanes): no row of the wave is outside [0, V)
+// or any of its tokens' target, so nothing is excluded.
+template <int MR, int QS = 16, class Z>
 __device__ __forceinline__ void fold_logits(const Z& z, int row0, int32_t V, int loc, bool plain,
                                             float inv_t, float& m, float& s, float& zt,
                                             bool& has_zt) {
-  const int kb = (threadIdx.x & (kWave - 1)) >> 4;
+  const int kb = (threadIdx.x & (kWave - 1)) / (256 / QS);
   const float c = inv_t * 1.44269504088896341f;  // log2(e) / T
   float mz = LseAcc::kMasked, sum = 0.0f;
   if (plain) {
@@ -92,7 +93,7 @@ __device__ __forceinline__ void fold_logits(const Z& z, int row0, int32_t V, int
     static_for<MR>([&](auto i) FS_INLINE {
       const f32x4 x = z(i);
       static_for<4>([&](auto r) FS_INLINE {
-        const int v = row0 + 16 * static_cast<int>(i) + 4 * kb + static_cast<int>(r);
+        const int v = row0 + QS * static_cast<int>(i) + 4 * kb + static_cast<int>(r);
         if (v == loc && loc >= 0) {
           zt = x[decltype(r)::value] * inv_t;
           has_zt = true;
@@ -104,7 +105,7 @@ __device__ __forceinline__ void fold_logits(const Z& z, int row0, int32_t V, int
     static_for<MR>([&](auto i) FS_INLINE {
       const f32x4 x = z(i);
       static_for<4>([&](auto r) FS_INLINE {
-        const int v = row0 + 16 * static_cast<int>(i) + 4 * kb + static_cast<int>(r);
+        const int v = row0 + QS * static_cast<int>(i) + 4 * kb + static_cast<int>(r);
         // the exponential of an excluded row may be anything: not added
         const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[decltype(r)::value], c, -off));
         sum += keep(v) ? e : 0.0f;
@@ -113,6 +114,9 @@ __device__ __forceinline__ void fold_logits(const Z& z, int row0, int32_t V, int
   }
   pair_merge(m, s, mz == LseAcc::kMasked ? mz : mz * inv_t, sum);
 }
+
+// The partials of each token into its log-probability and log-sum-exp.
+hipError_t launch_score_close(const ScoreArgs& a, float* logprob, float* lse, hipStream_t stream);
 
 // ---- tiles of the logits (W is operand A, h operand B) ----
 // L: the layout of W.  Tall: 256 vocabulary rows by 64, 128 or 256 tokens.
