@@ -306,16 +306,17 @@ __device__ void sum_rows(const XentArgs& x) {
 
 __global__ __launch_bounds__(1024) void xent_stats_kernel(XentArgs x) { sum_rows<1024>(x); }
 
-// Kept exponentials of one slice into dz, in place: 64 places by 1024 vocabulary
-// rows per block.  Each place's factors for the block's partials are made once, in
-// LDS; a wave then takes half a row, 16 bytes per lane.  Bound by reading and
-// writing dz.  The first slice's grid has one block more, which makes the stats.
-constexpr int kScaleRows = 64, kScaleCols = 1024;
+// Kept exponentials of one slice into dz, in place: 16 places by 1024 vocabulary
+// rows per block (of 64 places 513 rows on a shard filled half the CUs).  Each
+// place's factors for the block's partials are made once, in LDS; two waves then
+// take a row, 16 bytes per lane.  Bound by reading and writing dz (4096 rows of
+// 128256, three quarters with a target: 1.6 GB).  The first slice's grid has one
+// block more per column, the first of which makes the stats.
+constexpr int kScaleRows = 16, kScaleCols = 1024;
 
 __global__ __launch_bounds__(256) void xent_scale_kernel(XentArgs x) {
   typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
   __shared__ float s_fac[kScaleCols / 16][kScaleRows];
-  __shared__ int32_t s_loc[kScaleRows];
   const GradArgs& a = x.g;
   if (a.first_slice && blockIdx.x == gridDim.x - 1) {
     if (blockIdx.y == 0) sum_rows<256>(x);
@@ -324,51 +325,55 @@ __global__ __launch_bounds__(256) void xent_scale_kernel(XentArgs x) {
   const int n = *a.count;
   const int r0 = blockIdx.x * kScaleRows, c0 = blockIdx.y * kScaleCols;
   if (r0 >= n) return;
-  const int last = (a.nv + x.sub - 1) / x.sub;  // partials of the slice
-  for (int i = threadIdx.x; i < kScaleCols / x.sub * kScaleRows; i += 256) {
-    const int r = i % kScaleRows, t = c0 / x.sub + i / kScaleRows, p = r0 + r;
-    float f = 0.0f;  // (places behind the last: dz is 0)
-    if (p < n && t < last) {
-      const float m = x.part[static_cast<size_t>(a.v0 / x.sub + t) * a.Bp + p].x;
-      const RowTerm term = a.term[p];
-      f = __builtin_amdgcn_exp2f(__builtin_fmaf(m, kLog2e, -term.lse2)) * term.coef * 0x1p-15f;
-    }
-    s_fac[i / kScaleRows][r] = f;
+  const int lane_col = (threadIdx.x % 128) * 8, c = c0 + lane_col, half = threadIdx.x / 128;
+  const bool mine = c < (a.nv + 7) / 8 * 8;
+  constexpr int kEach = kScaleRows / 2;  // rows of a thread
+  u32x4* at = reinterpret_cast<u32x4*>(a.dz + static_cast<size_t>(r0 + half) * a.ldz + c);
+  const size_t step = static_cast<size_t>(a.ldz) / 4;  // two rows
+  f16x8 e[kEach];
+  if (mine) {
+#pragma unroll
+    for (int u = 0; u < kEach; ++u)
+      e[u] = __builtin_bit_cast(f16x8, __builtin_nontemporal_load(at + u * step));
   }
-  if (threadIdx.x < kScaleRows) {
-    const int p = r0 + static_cast<int>(threadIdx.x);
-    s_loc[threadIdx.x] = p < n ? a.loc[p] - a.v0 : -1;
+  {  // a thread's row of the factors is threadIdx.x mod 16
+    const int r = threadIdx.x % kScaleRows, p = min(r0 + r, n - 1);
+    const int t0 = c0 / x.sub, count = min((a.nv + x.sub - 1) / x.sub - t0, kScaleCols / x.sub);
+    const RowTerm term = a.term[p];
+    constexpr int kMost = kScaleCols / 16 * kScaleRows / 256;
+    float m[kMost];
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+      const int t = min(static_cast<int>(threadIdx.x) / kScaleRows + k * (256 / kScaleRows), count - 1);
+      m[k] = x.part[static_cast<size_t>(a.v0 / x.sub + t0 + t) * a.Bp + p].x;
+    }
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) {
+      const int t = threadIdx.x / kScaleRows + k * (256 / kScaleRows);
+      const float f =
+          __builtin_amdgcn_exp2f(__builtin_fmaf(m[k], kLog2e, -term.lse2)) * term.coef * 0x1p-15f;
+      if (t < kScaleCols / x.sub) s_fac[t][r] = r0 + r < n ? f : 0.0f;  // (behind the last place: 0)
+    }
   }
   __syncthreads();
+  if (!mine) return;
   const float uniform = uniform_term(x, upstream(x, n));
-  const int lane_col = (threadIdx.x % 128) * 8, c = c0 + lane_col;
-  if (c >= (a.nv + 7) / 8 * 8) return;
   const int fac = lane_col / x.sub;
-  constexpr int kAhead = 4;
-  for (int r = threadIdx.x / 128; r < kScaleRows; r += 2 * kAhead) {
-    u32x4* at[kAhead];
-    f16x8 e[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      at[u] = reinterpret_cast<u32x4*>(a.dz + static_cast<size_t>(r0 + r + 2 * u) * a.ldz + c);
-      e[u] = __builtin_bit_cast(f16x8, *at[u]);
+  for (int u = 0; u < kEach; ++u) {
+    const int row = 2 * u + half, p = r0 + row;
+    const float f = s_fac[fac][row];
+    float d[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d[j] = static_cast<float>(e[u][j]) * f;
+    if (x.smoothing > 0.0f && p < n) {
+      const int loc = a.loc[p] - a.v0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] += c + j < a.nv && c + j != loc ? uniform : 0.0f;
     }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int row = r + 2 * u;
-      const float f = s_fac[fac][row];
-      float d[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = static_cast<float>(e[u][j]) * f;
-      if (x.smoothing > 0.0f && r0 + row < n) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          d[j] += c + j < a.nv && c + j != s_loc[row] ? uniform : 0.0f;
-      }
-      const uint64_t lo = pack_bf16(d[0], d[1], d[2], d[3]), hi = pack_bf16(d[4], d[5], d[6], d[7]);
-      *at[u] = u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
-                     static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
-    }
+    const uint64_t lo = pack_bf16(d[0], d[1], d[2], d[3]), hi = pack_bf16(d[4], d[5], d[6], d[7]);
+    at[u * step] = u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
+                         static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
   }
 }
 
