@@ -49,6 +49,11 @@ __device__ __forceinline__ uint32_t finite_max(uint32_t m, uint32_t bits) {
 __device__ __forceinline__ uint32_t finite_max2(uint32_t m, uint32_t pair) {
   return finite_max(finite_max(m, pair), pair >> 16);
 }
+// Both halves' magnitudes, whatever they are: two instructions per pair.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2 any_max2(u16x2 m, uint32_t pair) {
+  return __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, pair & 0x7FFF7FFFu));
+}
 
 // Two pairs of bf16 to four e4m3 bytes, each times `down`.  (Finite entries end
 // up at 448 at most; infinities and NaN convert to NaN.)

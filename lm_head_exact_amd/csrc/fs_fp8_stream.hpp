@@ -23,7 +23,7 @@ namespace fs {
 //
 // The partial sums of the waves meet in LDS; the wave whose turn it is adds them
 // in wave order and hands the 16 rows' logits to its output.
-template <int OUT, int NT, int NW, int KS, int P, bool WHOLE>
+template <int OUT, int NT, int NW, int KS, int P, bool WHOLE, int C = 1>
 __global__ __launch_bounds__(NW * kWave) void fp8_stream_kernel(Fp8Args a) {
   static_assert(KS % P == 0, "the load ring must tile a group");
   static_assert(KS % 2 == 0, "a wave holds whole blocks");
@@ -80,6 +80,10 @@ __global__ __launch_bounds__(NW * kWave) void fp8_stream_kernel(Fp8Args a) {
     }
   });
 
+  // The block's t-th group: C neighbouring ones, then those of the next sweep.
+  auto nth = [&](int t) FS_INLINE {
+    return (t / C * G + static_cast<int>(blockIdx.x)) * C + t % C;
+  };
   // The lane's 16 bytes of the wave's step s of group t (clamped to the last group).
   auto group = [&](int t) FS_INLINE {
     return a.w + (static_cast<size_t>(min(t, ngroups - 1)) * steps + (WHOLE ? step0 : 0)) * 1024 +
@@ -104,13 +108,12 @@ __global__ __launch_bounds__(NW * kWave) void fp8_stream_kernel(Fp8Args a) {
     m[n] = LseAcc::kMasked;
     s_[n] = 0.0f;
   });
-  int g = blockIdx.x;
-  const uint8_t* wp = group(g);
-  const uint8_t* wn = group(g + G);
-  int sc = scales(g), sc_next = scales(g + G);
+  const uint8_t* wp = group(nth(0));
+  const uint8_t* wn = group(nth(1));
+  int sc = scales(nth(0)), sc_next = scales(nth(1));
   u32x4 ring[P];
   static_for<P>([&](auto p) FS_INLINE { ring[p] = load(wp, p); });
-  for (int it = 0; g < ngroups; g += G, ++it) {
+  for (int it = 0, g = nth(0); g < ngroups; ++it, g = nth(it)) {
     f32x4 acc[NT];
     static_for<NT>([&](auto n) FS_INLINE { acc[n] = f32x4{0.f, 0.f, 0.f, 0.f}; });
     int live = whole_steps;
@@ -129,9 +132,9 @@ __global__ __launch_bounds__(NW * kWave) void fp8_stream_kernel(Fp8Args a) {
       else ring[slot] = load(wn, s + P - KS);
     });
     wp = wn;
-    wn = group(g + 2 * G);
+    wn = group(nth(it + 2));
     sc = sc_next;
-    sc_next = scales(g + 2 * G);
+    sc_next = scales(nth(it + 2));
     const int par = it & 1;
     static_for<NT>([&](auto n) FS_INLINE {
       red[((par * NW + wave) * NT + n) * kWave + lane] = acc[n];
@@ -212,39 +215,49 @@ __global__ __launch_bounds__(NW * kWave) void fp8_stream_kernel(Fp8Args a) {
   }
 }
 
-template <int OUT, int NT, int NW, int KS, int P, bool WHOLE = false>
+template <int OUT, int NT, int NW, int KS, int P, int C = 1, bool WHOLE = false>
 hipError_t launch_fp8_shape(Fp8Args& a, hipStream_t stream) {
   if constexpr (!WHOLE)
-    if (a.D == 64 * NW * KS) return launch_fp8_shape<OUT, NT, NW, KS, P, true>(a, stream);
-  const auto kernel = fp8_stream_kernel<OUT, NT, NW, KS, P, WHOLE>;
+    if (a.D == 64 * NW * KS) return launch_fp8_shape<OUT, NT, NW, KS, P, C, true>(a, stream);
+  const auto kernel = fp8_stream_kernel<OUT, NT, NW, KS, P, WHOLE, C>;
   constexpr size_t smem = 2ull * NW * NT * kWave * sizeof(f32x4);
   static_assert(smem <= 64 * 1024, "LDS");
   static OccupancyCache cache;
   int slots = resident_blocks(kernel, NW * kWave, smem, cache);
   if (slots <= 0) return hipErrorInvalidDevice;
   slots = slots < kMaxFp8StreamBlocks ? slots : kMaxFp8StreamBlocks;
-  const int groups = fp8_groups(a.V);
-  a.S = groups < slots ? groups : slots;
+  const int clusters = (fp8_groups(a.V) + C - 1) / C;
+  a.S = clusters < slots ? clusters : slots;
   kernel<<<a.S, NW * kWave, smem, stream>>>(a);
   return hipGetLastError();
 }
 
-// Waves per block, steps per wave and loads ahead, by row length.
+// Waves per block, steps per wave, loads ahead and neighbouring groups per sweep, by
+// row length; 128256 rows, us.  One row of 4096: sixteen waves taking 128 KB (two
+// groups) in a row 78.6, one group 83.6, eight waves 82.3 to 85.  32 rows there: eight
+// waves four loads ahead and two groups 84, one group 87.7, a whole group ahead 92,
+// sixteen waves 86.  5120: five ahead 97.8, ten 100.9; 6144: sixteen waves three ahead
+// 115, six 119, eight waves 119; 8192: sixteen waves four ahead 155, eight ahead (they
+// spill) 176, eight waves 158 to 163.  The logits of more than 16 rows are written
+// faster where a row's lines fill in one block: fp32 32 rows of 4096 by two groups 98,
+// by one 103, by four 101; bf16 by four 93, two 96, one 101.  (Without the stores
+// 83 to 85: their 16 MB fall on 32 pages of memory at a time.)
 template <int OUT>
 hipError_t launch_fp8_rows(Fp8Args& a, hipStream_t stream) {
   const int32_t D = a.D;
   if (a.B <= 16) {
     if (D <= 1024) return launch_fp8_shape<OUT, 1, 8, 2, 2>(a, stream);
     if (D <= 2048) return launch_fp8_shape<OUT, 1, 8, 4, 4>(a, stream);
-    if (D <= 4096) return launch_fp8_shape<OUT, 1, 16, 4, 4>(a, stream);
-    if (D <= 5120) return launch_fp8_shape<OUT, 1, 8, 10, 10>(a, stream);
-    if (D <= 6144) return launch_fp8_shape<OUT, 1, 16, 6, 6>(a, stream);
-    return launch_fp8_shape<OUT, 1, 8, 16, 8>(a, stream);
+    if (D <= 4096) return launch_fp8_shape<OUT, 1, 16, 4, 4, 2>(a, stream);
+    if (D <= 5120) return launch_fp8_shape<OUT, 1, 8, 10, 5>(a, stream);
+    if (D <= 6144) return launch_fp8_shape<OUT, 1, 16, 6, 3>(a, stream);
+    return launch_fp8_shape<OUT, 1, 16, 8, 4>(a, stream);
   }
-  if (D <= 1024) return launch_fp8_shape<OUT, 2, 8, 2, 2>(a, stream);
-  if (D <= 2048) return launch_fp8_shape<OUT, 2, 8, 4, 4>(a, stream);
-  if (D <= 4096) return launch_fp8_shape<OUT, 2, 8, 8, 8>(a, stream);
-  return launch_fp8_shape<OUT, 2, 8, 10, 5>(a, stream);
+  constexpr int C = OUT == kLogitsF32 ? 2 : OUT == kLogitsBf16 ? 4 : 1;
+  if (D <= 1024) return launch_fp8_shape<OUT, 2, 8, 2, 2, C>(a, stream);
+  if (D <= 2048) return launch_fp8_shape<OUT, 2, 8, 4, 4, C>(a, stream);
+  if (D <= 4096) return launch_fp8_shape<OUT, 2, 8, 8, 4, C == 1 ? 2 : C>(a, stream);
+  return launch_fp8_shape<OUT, 2, 8, 10, 5, C>(a, stream);
 }
 
 }  // namespace fs
