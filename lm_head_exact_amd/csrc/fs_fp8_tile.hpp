@@ -32,8 +32,8 @@ namespace fs {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 template <int WA_, int WB_, int MR_, int NT_, int S_>
-struct Fp8Tile : Tile<kFrag, kKC, WA_, WB_, 2 * MR_, 2 * NT_, S_, 64> {
-  using Base = Tile<kFrag, kKC, WA_, WB_, 2 * MR_, 2 * NT_, S_, 64>;
+struct Fp8Tile : Tile<kFrag, kKC, WA_, WB_, 2 * MR_, 2 * NT_, S_, 64, false, true> {
+  using Base = Tile<kFrag, kKC, WA_, WB_, 2 * MR_, 2 * NT_, S_, 64, false, true>;
   static constexpr int WA = WA_, WB = WB_, MR = MR_, NT = NT_, S = S_;
   static constexpr int TA = Base::TA, TB = Base::TB, NW = Base::NW;
   static_assert(128 % (32 * MR) == 0, "a wave's rows lie in one block of scales");

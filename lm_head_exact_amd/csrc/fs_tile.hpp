@@ -55,7 +55,7 @@ struct Operand {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 template <int LA_, int LB_, int WA_, int WB_, int MR_, int NT_, int S_, int BK_ = 64,
-          bool NTA_ = false>
+          bool NTA_ = false, bool ROWS32_ = false>
 struct Tile {
   static constexpr int LA = LA_, LB = LB_;
   static_assert(LB != kFrag, "W is operand A");
@@ -104,8 +104,10 @@ struct Tile {
   }
 
   // The permutation of 16-byte pieces in a KC row.
+  // (ROWS32: for reads of 32 rows, 16 lanes of which go together: rows of which two
+  // are alike modulo 8, one of each two from 16 on.)
   __device__ __forceinline__ static int kc_swizzle(int r) {
-    return BK == 64 ? r & 7 : (r >> 1) & 3;
+    return BK != 64 ? (r >> 1) & 3 : ROWS32_ ? (r & 7) ^ ((r >> 4) & 1) : r & 7;
   }
   // The permutation of 32-byte units in a KM row.
   __device__ __forceinline__ static int km_swizzle(int k) { return (k & 3) | ((k >> 1) & 4); }
