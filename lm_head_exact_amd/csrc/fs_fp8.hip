@@ -6,28 +6,6 @@
 
 namespace fs {
 
-// The tile rule of the bf16 products, without the tiles whose ring leaves no room for
-// the call's scales (KB bytes per token) in LDS.
-LogitsTile fp8_tile(int32_t B, int32_t D, int32_t V) {
-  const size_t KB = static_cast<size_t>(quant_blocks(D));
-  LogitsTile best = LogitsTile::kShort64;
-  int64_t least = INT64_MAX;
-  for (const TileShape& c : kTileShapes) {
-    const size_t ring = c.tile == LogitsTile::kTall256   ? 2
-                        : c.tile == LogitsTile::kTall128 ? 3
-                        : c.tile == LogitsTile::kTall64  ? 3
-                        : c.tile == LogitsTile::kShort64 ? 3
-                                                         : 2;
-    if (ring * (c.rows + c.tokens) * 128 + KB * (c.tokens + (c.rows + 127) / 128) > 160 * 1024) continue;
-    const int64_t cost = tile_cost(c, B, V);
-    if (cost < least) {
-      least = cost;
-      best = c.tile;
-    }
-  }
-  return best;
-}
-
 namespace {
 
 struct Fp8Layout {

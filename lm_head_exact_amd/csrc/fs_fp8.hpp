@@ -109,8 +109,58 @@ inline bool fp8_streams(int32_t B, int32_t D) {
 }
 constexpr int kMaxFp8StreamBlocks = 2048;
 
-// Tiles: the one for a call, its vocabulary rows, tokens and threads.
-LogitsTile fp8_tile(int32_t B, int32_t D, int32_t V);
+// Tiles: the bf16 products' shapes but 64 x 128, with their ring's slots of 128 k.
+struct Fp8TileShape {
+  LogitsTile tile;
+  int32_t rows, tokens, slots;
+};
+constexpr Fp8TileShape kFp8TileShapes[] = {
+    {LogitsTile::kTall64, 256, 64, 3},    {LogitsTile::kTall128, 256, 128, 3},
+    {LogitsTile::kTall256, 256, 256, 2},  {LogitsTile::kShort64, 64, 64, 3},
+    {LogitsTile::kShort256, 128, 128, 2}};
+constexpr size_t kFp8Lds = 160 * 1024;
+
+// LDS of a tile: the ring, and the scales of its tokens and of its blocks of rows.
+inline size_t fp8_lds(const Fp8TileShape& c, int32_t D) {
+  return static_cast<size_t>(c.slots) * (c.rows + c.tokens) * kQuantBlock +
+         static_cast<size_t>(quant_blocks(D)) * (c.tokens + (c.rows + 127) / 128);
+}
+
+// Microseconds of a grid of c's blocks on 16032 rows of 8192, by rounds of 256 blocks
+// (one block of the tall tiles per CU; of 128 x 128 two, of 64 x 64 three).  Measured
+// there: 256 x 64 39 and 70 (one round, two), 256 x 128 46 to 56 and 101 to 121, 256 x
+// 256 78 to 103 and 188 to 201, 64 x 64 25, 31, 54, 76 and 110 (rounds 1, 2, 4, 6, 9),
+// 128 x 128 55, 55, 103 and 122 (1 to 4).  Over 72 calls (40 to 2048 tokens on 2001 to
+// 151936 rows of 1024 to 8192) the tile that it takes is 1.2% behind the best one on
+// average, by the bf16 products' costs 6%; at most 15%, where memory bounds the call (100
+// tokens on 32064 rows of 4096: 31 us by 256 x 64, 27 by 256 x 128).
+inline int64_t fp8_tile_cost(const Fp8TileShape& c, int64_t B, int64_t V) {
+  const int64_t blocks = (V + c.rows - 1) / c.rows * ((B + c.tokens - 1) / c.tokens);
+  const int64_t rounds = (blocks + 255) / 256;
+  switch (c.tile) {
+    case LogitsTile::kTall64: return 38 * rounds;
+    case LogitsTile::kTall128: return 57 * rounds;
+    case LogitsTile::kTall256: return 100 * rounds;
+    case LogitsTile::kShort64: return rounds == 1 ? 25 : 5 + 12 * rounds;
+    default: return 60 * ((rounds + 1) / 2);
+  }
+}
+
+// The tile for a call: the cheapest whose scales fit in LDS beside its ring (64 x 64
+// always does).
+inline LogitsTile fp8_tile(int32_t B, int32_t D, int32_t V) {
+  LogitsTile best = LogitsTile::kShort64;
+  int64_t least = INT64_MAX;
+  for (const Fp8TileShape& c : kFp8TileShapes) {
+    if (fp8_lds(c, D) > kFp8Lds) continue;
+    const int64_t cost = fp8_tile_cost(c, B, V);
+    if (cost < least) {
+      least = cost;
+      best = c.tile;
+    }
+  }
+  return best;
+}
 
 hipError_t launch_quantize_weights(const __bf16* W, int32_t V, int32_t D, bool packed, uint8_t* q,
                                    uint8_t* scale, hipStream_t stream);

@@ -43,10 +43,7 @@ struct Fp8Tile : Tile<kFrag, kKC, WA_, WB_, 2 * MR_, 2 * NT_, S_, 64, false, tru
   using Base::kStage;
   using Base::kStageA;
 
-  // LDS: the ring, the tokens' scales [KB][TB], the rows' [kVB][KB].
-  static constexpr size_t smem_bytes(int KB) {
-    return Base::kSmemBytes + static_cast<size_t>(KB) * (TB + kVB);
-  }
+  // LDS (fp8_lds): the ring, the tokens' scales [KB][TB], the rows' [kVB][KB].
 
   // Fragment f (32 rows) of step s of the staged tile at `buf`: lane (li, kb) gets row
   // li and bytes 64 s + 32 kb + 0..31.
@@ -341,36 +338,36 @@ void fp8_tile_kernel(Fp8Args a) {
   }
 }
 
-// ---- tiles: the training products' shapes ----
-template <LogitsTile> struct Fp8Shape;
-template <> struct Fp8Shape<LogitsTile::kTall64> { using T = Fp8Tile<8, 1, 1, 2, 3>; };
-template <> struct Fp8Shape<LogitsTile::kTall128> { using T = Fp8Tile<4, 2, 2, 2, 3>; };
-template <> struct Fp8Shape<LogitsTile::kTall256> { using T = Fp8Tile<2, 4, 4, 2, 2>; };
-template <> struct Fp8Shape<LogitsTile::kShort64> { using T = Fp8Tile<2, 2, 1, 1, 3>; };
-template <> struct Fp8Shape<LogitsTile::kShort128> { using T = Fp8Tile<2, 2, 1, 2, 2>; };
-template <> struct Fp8Shape<LogitsTile::kShort256> { using T = Fp8Tile<2, 2, 2, 2, 2>; };
+// ---- the tiles of kFp8TileShapes ----
+using Fp8Tall64 = Fp8Tile<8, 1, 1, 2, 3>;
+using Fp8Tall128 = Fp8Tile<4, 2, 2, 2, 3>;
+using Fp8Tall256 = Fp8Tile<2, 4, 4, 2, 2>;
+using Fp8Short64 = Fp8Tile<2, 2, 1, 1, 3>;
+using Fp8Short256 = Fp8Tile<2, 2, 2, 2, 2>;
 
-template <class T, int OUT>
+template <class T, int SHAPE, int OUT>
 hipError_t launch_fp8_tile(Fp8Args& a, hipStream_t stream) {
+  constexpr Fp8TileShape c = kFp8TileShapes[SHAPE];
+  static_assert(T::TA == c.rows && T::TB == c.tokens && T::S == c.slots, "the shape of the rule");
+  static_assert(T::kThreads == (T::TA == kTallRows ? 512 : 256), "threads_of");
   a.S = static_cast<int32_t>((static_cast<int64_t>(a.V) + T::TA - 1) / T::TA);
   static SmemRaised raised;
-  const hipError_t e = raise_smem(&fp8_tile_kernel<T, OUT>, 160 * 1024, raised);
+  const hipError_t e = raise_smem(&fp8_tile_kernel<T, OUT>, kFp8Lds, raised);
   if (e != hipSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(a.S) * ((a.B + T::TB - 1) / T::TB);
   fp8_tile_kernel<T, OUT><<<static_cast<unsigned>((tiles + 7) / 8 * 8), T::kThreads,
-                            T::smem_bytes(a.KB), stream>>>(a);
+                            fp8_lds(c, a.D), stream>>>(a);
   return hipGetLastError();
 }
 
 template <int OUT>
 hipError_t launch_fp8_tiles(Fp8Args& a, hipStream_t stream) {
   switch (fp8_tile(a.B, a.D, a.V)) {
-    case LogitsTile::kTall64: return launch_fp8_tile<Fp8Shape<LogitsTile::kTall64>::T, OUT>(a, stream);
-    case LogitsTile::kTall128: return launch_fp8_tile<Fp8Shape<LogitsTile::kTall128>::T, OUT>(a, stream);
-    case LogitsTile::kTall256: return launch_fp8_tile<Fp8Shape<LogitsTile::kTall256>::T, OUT>(a, stream);
-    case LogitsTile::kShort64: return launch_fp8_tile<Fp8Shape<LogitsTile::kShort64>::T, OUT>(a, stream);
-    case LogitsTile::kShort128: return launch_fp8_tile<Fp8Shape<LogitsTile::kShort128>::T, OUT>(a, stream);
-    default: return launch_fp8_tile<Fp8Shape<LogitsTile::kShort256>::T, OUT>(a, stream);
+    case LogitsTile::kTall64: return launch_fp8_tile<Fp8Tall64, 0, OUT>(a, stream);
+    case LogitsTile::kTall128: return launch_fp8_tile<Fp8Tall128, 1, OUT>(a, stream);
+    case LogitsTile::kTall256: return launch_fp8_tile<Fp8Tall256, 2, OUT>(a, stream);
+    case LogitsTile::kShort64: return launch_fp8_tile<Fp8Short64, 3, OUT>(a, stream);
+    default: return launch_fp8_tile<Fp8Short256, 4, OUT>(a, stream);
   }
 }
 

@@ -66,7 +66,7 @@ SHAPES = [  # streaming kernels: every row length's, one and two tiles of 16 tok
     # tiles; ragged in every direction
     (33, 64, 255), (64, 192, 257), (65, 128, 256), (128, 320, 511), (129, 320, 513), (257, 192, 1025),
     (20, 5184, 60), (17, 8192, 50), (33, 16384, 40)]
-# one shape per tile: 256 x 64, 256 x 128, 256 x 256, 128 x 128, 64 x 128, 64 x 64
+# one shape per tile: 256 x 64, 256 x 128, 256 x 256, 128 x 128, 64 x 64
 TILES = [(200, 64, 16032), (500, 64, 16001), (1000, 64, 16030), (3833, 128, 2161), (513, 192, 2001),
          (60, 64, 803)]
 
