@@ -130,7 +130,7 @@ FS_API fs_status fs_quantize_weights_fp8(const void* W, int32_t V, int32_t D, in
   if (q_bytes < need)
     return fail(FS_ERR_WORKSPACE, "%s: buffer of %zu bytes is below the %zu required", who, q_bytes,
                 need);
-  if (!grid_fits(static_cast<int64_t>(quant_blocks(V)) * ((quant_blocks(D) + 3) / 4), 256))
+  if (!grid_fits(static_cast<int64_t>(quant_blocks(V)) * ((quant_blocks(D) + 3) / 4), 1024))
     return fail(FS_ERR_UNSUPPORTED, "%s: D=%d, V=%d exceed the launch grid", who, D, V);
   if (start_launches()) return injected_failure(who);
   const hipError_t e = launch_quantize_weights(

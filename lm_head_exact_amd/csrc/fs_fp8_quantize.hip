@@ -4,38 +4,40 @@
 namespace fs {
 namespace {
 
-// One wave per block of 128 x 128, four blocks side by side per thread block, so
-// that a row is read 1 KB at a time, and neighbouring thread blocks along the rows. A
-// lane holds, for each group of 16 rows and 64 columns, the 16 values that are its
-// piece of the fragment order: the whole block stays in registers between the
-// maximum and the conversion, all its loads in flight at once.  Bound by memory: two
-// bytes read and one written per value.  128256 x 4096: 283 us, 5.6 TB/s (a copy runs
-// at 5.2); 325 to 350 with thread blocks down the columns, 319 with stores through the
-// caches.  Row-major, whose lanes store 64 bytes of a row at a time, 317.
+// Four waves per block of 128 x 128, four blocks side by side per thread block, so
+// that a row is read 1 KB at a time, and neighbouring thread blocks along the rows.
+// A wave has two groups of 16 rows; a lane holds, for each group and 64 columns, the
+// 16 values that are its piece of the fragment order, in registers between the
+// maximum and the conversion.  Bound by memory: two bytes read and one written per
+// value.  128256 x 4096: 270 us, 5.8 TB/s (a copy runs at 5.2), stores past the caches;
+// 283 by one wave per block, whose few waves also take 7 us on 1000 x 256 (5 here), 299
+// with one block per thread block, 325 with neighbours down the columns.  Row-major,
+// whose lanes store 64 bytes of a row at a time, 317.
+constexpr int kQuantThreads = 1024;
+
 template <bool PACKED>
-__global__ __launch_bounds__(256) void quantize_weights_kernel(const __bf16* __restrict__ W,
-                                                               int32_t V, int32_t D,
-                                                               uint8_t* __restrict__ q,
-                                                               uint8_t* __restrict__ scale) {
-  constexpr int kGroups = kQuantBlock / 16, kSteps = kQuantBlock / 64;
+__global__ __launch_bounds__(kQuantThreads) void quantize_weights_kernel(
+    const __bf16* __restrict__ W, int32_t V, int32_t D, uint8_t* __restrict__ q,
+    uint8_t* __restrict__ scale) {
+  constexpr int kWaves = kQuantThreads / kWave, kAcross = kWaves / 4;
+  constexpr int kGroups = 2, kSteps = kQuantBlock / 64;
+  __shared__ uint32_t s_max[kWaves];
   const int lane = threadIdx.x & (kWave - 1), li = lane & 15, kb = lane >> 4;
-  const int KB = quant_blocks(D);
-  const int across = (KB + 3) / 4;
-  const int cb = static_cast<int>(blockIdx.x % across) * 4 + (threadIdx.x >> 6);  // block of columns
-  if (cb >= KB) return;
-  const int64_t vb = blockIdx.x / across;  // block of rows
+  const int wave = threadIdx.x >> 6;
+  const int KB = quant_blocks(D), across = (KB + kAcross - 1) / kAcross;
+  const int cb = static_cast<int>(blockIdx.x % across) * kAcross + wave / 4;  // block of columns
+  const int64_t vb = blockIdx.x / across;                                     // and of rows
+  const int64_t group0 = vb * (kQuantBlock / 16) + wave % 4 * kGroups;
   const int k0 = cb * kQuantBlock + 16 * kb;
   u32x4 x[kGroups][kSteps][2];
-  uint32_t m = 0;
   static_for<kGroups>([&](auto g) FS_INLINE {
     static_for<kSteps>([&](auto s) FS_INLINE {
-      const int64_t v = vb * kQuantBlock + 16 * static_cast<int>(g) + li;
+      const int64_t v = (group0 + static_cast<int>(g)) * 16 + li;
       const int k = k0 + 64 * static_cast<int>(s);
       static_for<2>([&](auto j) FS_INLINE {
         const int kj = k + 8 * static_cast<int>(j);
         x[g][s][j] = u32x4{0u, 0u, 0u, 0u};
-        if (v < V && kj < D)
-          x[g][s][j] = *reinterpret_cast<const u32x4*>(W + v * D + kj);
+        if (v < V && kj < D) x[g][s][j] = *reinterpret_cast<const u32x4*>(W + v * D + kj);
       });
     });
   });
@@ -50,7 +52,7 @@ __global__ __launch_bounds__(256) void quantize_weights_kernel(const __bf16* __r
   };
   u16x2 any = {0, 0};
   fold([&](uint32_t pair) FS_INLINE { any = any_max2(any, pair); });
-  m = max(static_cast<uint32_t>(any[0]), static_cast<uint32_t>(any[1]));
+  uint32_t m = max(static_cast<uint32_t>(any[0]), static_cast<uint32_t>(any[1]));
   if (__ballot(m >= 0x7F80) != 0) {  // something is not finite: once more without it
     m = 0;
     fold([&](uint32_t pair) FS_INLINE { m = finite_max2(m, pair); });
@@ -58,15 +60,20 @@ __global__ __launch_bounds__(256) void quantize_weights_kernel(const __bf16* __r
 #pragma unroll
   for (int d = kWave / 2; d >= 1; d >>= 1)
     m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d, kWave)));
+  if (lane == 0) s_max[wave] = m;
+  __syncthreads();
+  if (cb >= KB) return;
+  const int w0 = wave / 4 * 4;
+  m = max(max(s_max[w0], s_max[w0 + 1]), max(s_max[w0 + 2], s_max[w0 + 3]));
   const int byte = scale_byte(m);
   const float down = scale_down(byte);
-  if (lane == 0) scale[vb * KB + cb] = static_cast<uint8_t>(byte);
+  if (lane == 0 && wave % 4 == 0) scale[vb * KB + cb] = static_cast<uint8_t>(byte);
   static_for<kGroups>([&](auto g) FS_INLINE {
     static_for<kSteps>([&](auto s) FS_INLINE {
       const u32x4 a = x[g][s][0], b = x[g][s][1];
       const u32x4 y = {to_e4m3(a[0], a[1], down), to_e4m3(a[2], a[3], down),
                        to_e4m3(b[0], b[1], down), to_e4m3(b[2], b[3], down)};
-      const int64_t group = vb * kGroups + static_cast<int>(g);
+      const int64_t group = group0 + static_cast<int>(g);
       const int k = k0 + 64 * static_cast<int>(s);
       if constexpr (PACKED) {  // (D is a multiple of 64)
         const int step = cb * kSteps + static_cast<int>(s);
@@ -173,8 +180,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(Fp8Args a) {
 hipError_t launch_quantize_weights(const __bf16* W, int32_t V, int32_t D, bool packed, uint8_t* q,
                                    uint8_t* scale, hipStream_t stream) {
   const unsigned grid = static_cast<unsigned>(quant_blocks(V)) * ((quant_blocks(D) + 3) / 4);
-  if (packed) quantize_weights_kernel<true><<<grid, 256, 0, stream>>>(W, V, D, q, scale);
-  else quantize_weights_kernel<false><<<grid, 256, 0, stream>>>(W, V, D, q, scale);
+  if (packed) quantize_weights_kernel<true><<<grid, kQuantThreads, 0, stream>>>(W, V, D, q, scale);
+  else quantize_weights_kernel<false><<<grid, kQuantThreads, 0, stream>>>(W, V, D, q, scale);
   return hipGetLastError();
 }
 
