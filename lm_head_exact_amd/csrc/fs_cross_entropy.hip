@@ -468,7 +468,6 @@ hipError_t run_xent(XentArgs& x, const XentPlan& p, hipStream_t s) {
   };
   hipError_t e = launch_grad_rows(a, s);
   if (e != hipSuccess) return e;
-  if ((e = launch_grad_targets(a, s)) != hipSuccess) return e;
   if (a.B > 0) {
     for (int i = 0; i < p.g.slices; ++i) {
       slice(i);

@@ -130,11 +130,10 @@ bool grad_grids_fit(int32_t B, int32_t D, int32_t V, const GradPlan& p, bool dh,
 // Sets the workspace's arrays and the sizes that follow from the plan.
 void grad_workspace(GradArgs& a, const GradPlan& p, char* ws);
 
-// Rows with a target, their places and the parts that dh is taken in; then copies
-// of their hidden states and, with a gradient, their terms; dh of the others is 0.
+// Rows with a target, their places and the parts that dh is taken in; copies of their
+// hidden states and, with a gradient, their terms; dh of the others is 0; for dW the
+// targets by tile of the vocabulary.
 hipError_t launch_grad_rows(const GradArgs& a, hipStream_t stream);
-// Targets by tile of the vocabulary, for dW.
-hipError_t launch_grad_targets(const GradArgs& a, hipStream_t stream);
 // dW and dh of the slice v0, nv from its dz.
 hipError_t launch_grad_products(const GradArgs& a, hipStream_t stream);
 // The targets' terms and the parts of dh, once every slice is through.

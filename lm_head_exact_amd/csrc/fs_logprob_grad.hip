@@ -105,12 +105,8 @@ __global__ __launch_bounds__(kScanThreads) void grad_rows_kernel(GradArgs a) {
 // Row b < B: its terms and a copy of its hidden state at its place, or a zero
 // gradient.  Rows B .. B + 255: zeros up to the next multiple of 256 places.
 // Copies 64 MB (4096 rows of 4096, read and written) in 12 us.
-__global__ __launch_bounds__(256) void grad_gather_kernel(GradArgs a) {
-  const int b = blockIdx.x;
-  const int n = *a.count;
-  int at;
+__device__ void gather_row(const GradArgs& a, int b, int at, int n) {
   if (b < a.B) {
-    at = a.slot[b];
     if (at < 0) {
       if (a.dh != nullptr)
         for (int k = threadIdx.x * 8; k < a.D; k += 256 * 8)
@@ -121,7 +117,6 @@ __global__ __launch_bounds__(256) void grad_gather_kernel(GradArgs a) {
       *reinterpret_cast<bf16x8*>(a.hz + static_cast<size_t>(at) * a.Dp + k) =
           k < a.D ? load_frag(a.h + static_cast<size_t>(b) * a.D + k) : zero_frag();
   } else {
-    at = n + (b - a.B);
     if (at >= (n + 255) / 256 * 256) return;
     for (int k = threadIdx.x * 8; k < a.Dp; k += 256 * 8)
       *reinterpret_cast<bf16x8*>(a.hz + static_cast<size_t>(at) * a.Dp + k) = zero_frag();
@@ -142,6 +137,11 @@ __global__ __launch_bounds__(256) void grad_gather_kernel(GradArgs a) {
   }
   a.term[at] = t;
   a.loc[at] = loc;
+}
+
+__global__ __launch_bounds__(256) void grad_gather_kernel(GradArgs a) {
+  const int b = blockIdx.x, n = *a.count;
+  gather_row(a, b, b < a.B ? a.slot[b] : n + (b - a.B), n);
 }
 
 // The places that have a target in one tile of 256 vocabulary rows, in order,
@@ -199,6 +199,94 @@ __global__ __launch_bounds__(kTargetThreads) void grad_targets_kernel(GradArgs a
   if (threadIdx.x < kTargetTile && v < a.V)
     a.first[v] = s_first[threadIdx.x] == 0x7FFFFFFF ? -1 : s_first[threadIdx.x];
   if (threadIdx.x == 0) a.tile[blockIdx.x] = int2{begin, begin + all};
+}
+
+// Rows, gather and targets in one launch for up to kFewRows rows (4 rows on 1000 x
+// 256: 40 us a call, 45 by three launches; 513 rows on a shard 379, 383): every block counts the
+// ids before its own instead of waiting for one block's scan.  Blocks 0 .. B + 255
+// gather, the others (for dW) take a tile of 256 vocabulary rows each.
+constexpr int kFewRows = 1024, kFewThreads = 256;
+
+__global__ __launch_bounds__(kFewThreads) void grad_few_rows_kernel(GradArgs a) {
+  constexpr int kWaves = kFewThreads / kWave, kEach = kFewRows / kFewThreads;
+  __shared__ int32_t s_on[kEach][kWaves], s_hit[kEach][kWaves], s_less[kEach][kWaves];
+  __shared__ int32_t s_first[kTargetTile];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, t = threadIdx.x;
+  const int gathers = a.B + 256;
+  const bool targets = static_cast<int>(blockIdx.x) >= gathers;  // (block-uniform)
+  const int b = blockIdx.x, lo = (static_cast<int>(blockIdx.x) - gathers) * kTargetTile;
+  if (targets) s_first[t] = 0x7FFFFFFF;
+  // id u * 256 + t of every thread
+  uint64_t on[kEach], hit[kEach];
+  int loc[kEach];
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int i = u * kFewThreads + t;
+    const int32_t id = i < a.B ? a.ids[i] : -1;
+    loc[u] = has_token(id) ? target_row(id, a.vocab_offset, a.V) : -1;
+    // (targets below the tile, and rows before this block's)
+    const uint64_t less =
+        __ballot(targets ? loc[u] >= 0 && loc[u] < lo : has_token(id) && i < b);
+    on[u] = __ballot(has_token(id));
+    hit[u] = __ballot(targets && loc[u] >= lo && loc[u] - lo < kTargetTile);
+    if (lane == 0) {
+      s_on[u][wave] = __popcll(on[u]);
+      s_hit[u][wave] = __popcll(hit[u]);
+      s_less[u][wave] = __popcll(less);
+    }
+  }
+  __syncthreads();
+  int n = 0, before = 0;
+#pragma unroll
+  for (int u = 0; u < kEach; ++u)
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      n += s_on[u][w];
+      before += s_less[u][w];
+    }
+  if (targets) {
+    const uint64_t below = (uint64_t{1} << lane) - 1;
+    int place = 0, at = before;
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      int my_place = place, my_at = at;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        my_place += w < wave ? s_on[u][w] : 0;
+        my_at += w < wave ? s_hit[u][w] : 0;
+        place += s_on[u][w];
+        at += s_hit[u][w];
+      }
+      if (hit[u] >> lane & 1) {
+        const int p = my_place + __popcll(on[u] & below);
+        a.list[my_at + __popcll(hit[u] & below)] = p;
+        atomicMin(&s_first[loc[u] - lo], p);  // (the minimum does not depend on the order)
+      }
+    }
+    __syncthreads();
+    const int v = lo + t;
+    if (v < a.V) a.first[v] = s_first[t] == 0x7FFFFFFF ? -1 : s_first[t];
+    if (t == 0) a.tile[lo / kTargetTile] = int2{before, at};
+    return;
+  }
+  if (b == gathers - 1) {  // (a block with next to nothing to gather)
+    uint64_t best = ~0ull;
+    for (int parts = t + 1; parts <= a.max_splits; parts += kFewThreads)
+      best = min(best, hidden_cost(a, n, parts) << 12 | parts);
+    __shared__ unsigned long long s_best;
+    if (t == 0) s_best = ~0ull;
+    __syncthreads();
+    atomicMin(&s_best, static_cast<unsigned long long>(best));
+    __syncthreads();
+    if (t == 0) {
+      a.count[0] = n;
+      a.count[1] = static_cast<int32_t>(s_best & 4095);
+    }
+  }
+  const bool mine = b < a.B && has_token(a.ids[min(b, a.B - 1)]);
+  if (b < a.B && t == 0) a.slot[b] = mine ? before : -1;
+  if (mine && t == 0) a.row[before] = b;
+  gather_row(a, b, b < a.B ? (mine ? before : -1) : n + (b - a.B), n);
 }
 
 // dz of one slice: logits of a tile of vocabulary rows by rows with a target,
@@ -523,7 +611,6 @@ hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
 hipError_t run_grad(GradArgs& a, const GradPlan& p, hipStream_t s) {
   hipError_t e = launch_grad_rows(a, s);
   if (e != hipSuccess) return e;
-  if ((e = launch_grad_targets(a, s)) != hipSuccess) return e;
   for (int32_t v0 = 0; v0 < a.V; v0 += p.slice) {
     a.v0 = v0;
     a.nv = a.V - v0 < p.slice ? a.V - v0 : p.slice;
@@ -561,15 +648,16 @@ void grad_workspace(GradArgs& a, const GradPlan& p, char* ws) {
 }
 
 hipError_t launch_grad_rows(const GradArgs& a, hipStream_t s) {
+  if (a.B <= kFewRows) {
+    const int64_t blocks = a.B + 256ll + (a.dW != nullptr ? target_tiles(a.V) : 0);
+    grad_few_rows_kernel<<<static_cast<unsigned>(blocks), kFewThreads, 0, s>>>(a);
+    return hipGetLastError();
+  }
   grad_rows_kernel<<<1, kScanThreads, 0, s>>>(a);
-  const hipError_t e = hipGetLastError();
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   grad_gather_kernel<<<a.B + 256, 256, 0, s>>>(a);
-  return hipGetLastError();
-}
-
-hipError_t launch_grad_targets(const GradArgs& a, hipStream_t s) {
-  if (a.dW == nullptr) return hipSuccess;
+  if ((e = hipGetLastError()) != hipSuccess || a.dW == nullptr) return e;
   grad_targets_kernel<<<target_tiles(a.V), kTargetThreads, 0, s>>>(a);
   return hipGetLastError();
 }
