@@ -357,7 +357,7 @@ FS_API fs_status fs_sample_unfused(const void* h, const void* W, int32_t B, int3
  *                (FS_ERR_UNSUPPORTED beyond, and where a launch would hold 2^32
  *                threads)
  *   W_packed     the values in fragment order (below), 16-byte aligned
- *   W_scale      bytes [ceil(V / 128)][ceil(D / 128)], device
+ *   W_scale      bytes [ceil(V / 128)][ceil(D / 128)], device: 17 to 247
  *   workspace    >= fs_fp8_workspace_bytes(B, D, V) bytes (0 for invalid sizes);
  *                contents on entry ignored
  * NaN or infinite entries of h or W give NaN in the logits that they enter (for
@@ -496,8 +496,8 @@ FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_
  *   grad_h = dz W,  grad_W = dz^T h
  * Rows without a target (negative, as -100) have loss and gradient 0 and count
  * in no mean; their h is not used (it may be NaN).  A target of V or more has
- * probability 0: its row's loss is +inf, and the gradient that of the other
- * entries.
+ * probability 0: its row's loss is +inf (unless s is 1, where no target counts), and
+ * the gradient that of the other entries.
  *   h, W         bf16 [B][D] and [V][D], D % 8 == 0: sizes as
  *                fs_token_logprobs_backward takes them; the whole vocabulary
  *   targets      int32 [B], device
@@ -516,7 +516,9 @@ FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_
  *                holds two bytes per row and vocabulary entry, up to 4 GiB (a
  *                larger batch takes a slice of the vocabulary at a time and makes
  *                the logits twice), and what fs_token_logprobs_backward holds
- *                beside dz; contents on entry ignored
+ *                beside dz; without gradients a copy of h; and 12 bytes per row and
+ *                16 to 128 vocabulary entries (the more rows, the more entries);
+ *                contents on entry ignored
  * Logits of -inf have probability 0; NaN or +inf among a row's give NaN.  B == 0
  * sets the stats and grad_W to 0. */
 FS_API size_t fs_cross_entropy_workspace_bytes(int32_t B, int32_t D, int32_t V, int32_t grads);

@@ -264,8 +264,9 @@ __global__ __launch_bounds__(kCloseThreads) void xent_close_kernel(XentArgs x) {
   const float sm = x.smoothing, up = upstream(x, n);
   float loss = nll, own = 0.0f;
   const float lift = x.z_loss > 0.0f ? 1.0f + 2.0f * x.z_loss * lse : 1.0f;
-  if (sm > 0.0f)
-    loss = (1.0f - sm) * nll + sm * (lse - static_cast<float>(red_z[0][c] / a.V));
+  if (sm > 0.0f)  // (at 1 the target does not count, not even one of probability 0)
+    loss = (sm < 1.0f ? (1.0f - sm) * nll : 0.0f) +
+           sm * (lse - static_cast<float>(red_z[0][c] / a.V));
   if (x.z_loss > 0.0f) loss += x.z_loss * lse * lse;
   if (here) {
     own = expm1f(-nll);

@@ -44,6 +44,7 @@ def cross_entropy(h, W, targets, label_smoothing=0.0, z_loss=0.0, reduction="mea
                     torch.zeros((), dtype=F64, device=dev))
     lift = (1 + 2 * lam * lse)[:, None]
     p = torch.exp(z - lse[:, None])
+    nll = torch.where(on, nll, torch.zeros_like(nll))
     own = torch.expm1(-nll) + 2 * lam * lse * torch.exp(-nll) + s - s / V
     size = lift.abs() * p + s / V
     size = torch.where(hot, (-torch.expm1(-nll) + 2 * lam * lse.abs() * torch.exp(-nll) + s)[:, None], size)

@@ -52,6 +52,9 @@ def check(h, W, t, got, want, smoothing=0.0, z_loss=0.0, e=None, **_):
                 float((2 * lse * (e + 2.0 ** -22 * (1 + lse)) + 2.0 ** -22 * lse ** 2)[on].sum()) / n]
         for i in range(3):
             w = float(want["stats"][i])
+            if math.isinf(w):   # (the mean of lse - z_y of a target of probability 0)
+                assert float(stats[i]) == w
+                continue
             assert abs(float(stats[i]) - w) <= tol3[i] + 2.0 ** -23 * abs(w), (i, float(stats[i]), w)
     top = float(lse[on].max()) if on.any() else 0.0
     for x, w, bound in ((gh, want["grad_h"], want["bound_h"]), (gw, want["grad_W"], want["bound_W"])):
@@ -173,6 +176,17 @@ def test_targets_past_the_vocabulary():
     got = case(h, W, t, z_loss=1e-3)
     assert torch.isposinf(got[1][5]) and torch.isposinf(got[1][9]) and torch.isposinf(got[0][0])
     assert torch.isfinite(got[2]).all() and torch.isfinite(got[3]).all()
+
+
+def test_smoothing_alone():
+    """At 1 no target counts, not even one of probability 0."""
+    h, W, t = make(30, 64, 300, seed=17)
+    t[3], t[4] = 300, 10
+    t[5] = -1
+    got = case(h, W, t, smoothing=1.0, z_loss=1e-3)
+    assert torch.isfinite(got[1]).all()
+    got = case(h, W, torch.full_like(t, 10 ** 6), smoothing=1.0, reduction="sum")
+    assert torch.isfinite(got[0][0]) and torch.isposinf(got[0][1])
 
 
 def test_certain_targets_keep_their_digits():
