@@ -11,17 +11,24 @@
 // is nearly certain.  Rows without a target are dropped before the products.
 //
 // Three products of 2 B V D operations.  The gradient needs lse, which needs all
-// of a row's logits; what the first product leaves is therefore kept in 16 bits
-// (for up to kKeptBytes; beyond that the logits are made a second time, a slice
-// of the vocabulary after the other, in a fourth product).  Kept is not z, which
-// 16 bits would blur by percents of p, but exp(z - m) with m the largest logit of
-// the row within one wave's 16 to 128 vocabulary rows, and m itself in fp32 on the
-// side: with the pairs (m, sum) merged into lse, one pass over it makes
+// of a row's logits; what the first product leaves is therefore kept in 16 bits, for
+// up to kKeptBytes (beyond that the logits are made a second time, a slice of the
+// vocabulary after the other, in a fourth product: 4096 rows of 4096 on 128256, three
+// quarters with a target, 8.0 ms kept and 10.2 made twice; 16000 rows 42.1 and 54.0;
+// 513 rows on a shard of 16032 x 8192 387 and 484 us; 4 rows on 1000 x 256 41 and 43).
+// Kept is not z, which 16 bits would blur by percents of p, but exp(z - m) with m the
+// largest logit of the row within one wave's 16 to 128 vocabulary rows, and m itself
+// in fp32 on the side: with the pairs (m, sum) merged into lse, one pass over it makes
 //   dz = u lift exp(m - lse) * kept - u s / V
 // in bf16, in place.  fp16 with the largest value at 2^15: 11 bits down to 2^-29
 // of it and a value of 2^-39 of it lost, so that the one rounding that shows is
 // dz's to bf16, as in fs_token_logprobs_backward (bf16 would be rounded twice:
 // 2.4e-3 of dz instead of 1.7e-3).
+//
+// 4096 rows of 4096 on 128256, three quarters with a target: logits 2.6 to 2.7 ms, dW
+// 2.6, dh 2.4 (1.2 to 1.3 PFLOP/s each), scaling the kept exponentials 0.27 (5.8 TB/s),
+// everything else 0.12.  1777 rows of 5120 on 151936, the loss alone: 1.9 ms for the
+// 1333 rows that count.
 #include <cmath>
 
 #include "fs_grad.hpp"
