@@ -64,7 +64,8 @@ fs_status prepare(const char* who, const void* h, const void* W, const void* sca
     const LogitsTile t = fp8_tile(B, D, V);
     const int64_t tiles = (static_cast<int64_t>(V) + rows_of(t) - 1) / rows_of(t) *
                           ((B + tokens_of(t) - 1) / tokens_of(t));
-    if (!grid_fits(tiles + 7, threads_of(t)))
+    if (!grid_fits(tiles + 7, threads_of(t)) ||
+        !grid_fits(B, static_cast<int64_t>(round_up(round_up(D, kQuantBlock) / 16, 64))))
       return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, D=%d, V=%d exceed the launch grid", who, B, D, V);
   }
   if (B == 0) return FS_OK;

@@ -1,5 +1,6 @@
 // fs_fp8_quantize.hip -- bf16 weights and hidden states in 8-bit blocks.
 #include "fs_fp8.hpp"
+#include "fs_internal.hpp"
 
 namespace fs {
 namespace {
@@ -111,65 +112,68 @@ __global__ __launch_bounds__(256) void pack_fp8_kernel(const uint8_t* __restrict
   }
 }
 
-// Hidden states: one block per row, eight threads per 128 columns, 16 columns each.
+// Hidden states: one block per row, a thread per 16 columns, eight per 128.
 // TARGETS: also the logit of the row's token, with exact products summed in fp32.  The
 // tiles' instructions round theirs (fs_fp8_tile.hpp), which the log-sum-exp over
-// the other rows averages out but a single logit shows.
+// the other rows averages out but a single logit shows.  777 rows of 8192: 6 us; 1777
+// rows of 5120 with targets 16, bound by memory: a row's pieces of 16 bytes lie 256
+// apart in W, each in a line of its own.
 template <bool TARGETS>
-__global__ __launch_bounds__(256) void quantize_rows_kernel(Fp8Args a) {
-  __shared__ float s_sum[256 / kWave];
-  const int b = blockIdx.x, lane = threadIdx.x & (kWave - 1);
-  int loc = -1;
-  if constexpr (TARGETS) loc = target_row(a.ids[b], a.vocab_offset, a.V);
-  float z = 0.0f;
-  for (int k0 = 0; k0 < a.Dp; k0 += 256 * 16) {  // (block-uniform)
-    const int k = k0 + 16 * static_cast<int>(threadIdx.x);
-    u32x4 x[2];
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      x[j] = u32x4{0u, 0u, 0u, 0u};
-      if (k + 8 * j < a.D)
-        x[j] = *reinterpret_cast<const u32x4*>(a.h + static_cast<int64_t>(b) * a.D + k + 8 * j);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) m = finite_max2(m, x[j][c]);
+__global__ __launch_bounds__(1024) void quantize_rows_kernel(Fp8Args a) {
+  static_assert(kMaxFp8D <= 1024 * 16, "a thread per 16 columns");
+  __shared__ float s_sum[1024 / kWave];
+  const int b = blockIdx.x, lane = threadIdx.x & (kWave - 1), k = 16 * static_cast<int>(threadIdx.x);
+  const bool in = k < a.D;  // (D is a multiple of 64: sixteen columns are all inside or all past it)
+  u32x4 x[2] = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+  if (in) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(a.h + static_cast<int64_t>(b) * a.D + k);
+    x[0] = p[0];
+    x[1] = p[1];
+  }
+  int loc = -1, wbyte = 127;
+  u32x4 w = {0u, 0u, 0u, 0u};
+  if constexpr (TARGETS) {
+    loc = target_row(a.ids[b], a.vocab_offset, a.V);
+    if (loc >= 0 && in) {
+      const size_t step = static_cast<size_t>(loc / 16) * (a.D / 64) + k / 64;
+      w = *reinterpret_cast<const u32x4*>(a.w + (step * 64 + loc % 16 + 16 * (k / 16 % 4)) * 16);
+      wbyte = a.wscale[static_cast<size_t>(loc / kQuantBlock) * a.KB + k / kQuantBlock];
     }
+  }
+  uint32_t m = 0;
 #pragma unroll
-    for (int d = 4; d >= 1; d >>= 1)
-      m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d, kWave)));
-    const int byte = scale_byte(m);
-    const float down = scale_down(byte);
-    if (k < a.Dp) {  // (D is a multiple of 64: sixteen columns are all inside or all past it)
-      const u32x4 y = {to_e4m3(x[0][0], x[0][1], down), to_e4m3(x[0][2], x[0][3], down),
-                       to_e4m3(x[1][0], x[1][1], down), to_e4m3(x[1][2], x[1][3], down)};
-      *reinterpret_cast<u32x4*>(a.hq + static_cast<int64_t>(b) * a.Dp + k) = y;
-      const int kt = k / kQuantBlock;
-      if (threadIdx.x % 8 == 0)
-        a.hscale[static_cast<int64_t>(kt) * a.Bp + b] = static_cast<uint8_t>(byte);
-      if (TARGETS && loc >= 0 && k < a.D) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(
-            a.w + ((static_cast<size_t>(loc / 16) * (a.D / 64) + k / 64) * 64 + loc % 16 +
-                   16 * (k / 16 % 4)) * 16);
-        const float up = scale_up(byte);
-        const float wup = scale_up(a.wscale[static_cast<size_t>(loc / kQuantBlock) * a.KB + kt]);
+  for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const bf16x8 p = widen(y[2 * j], y[2 * j + 1], up), q = widen(w[2 * j], w[2 * j + 1], wup);
+    for (int c = 0; c < 4; ++c) m = finite_max2(m, x[j][c]);
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            z = __builtin_fmaf(static_cast<float>(p[c]), static_cast<float>(q[c]), z);
-        }
-      }
-    }
+  for (int d = 4; d >= 1; d >>= 1)
+    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d, kWave)));
+  const int byte = scale_byte(m);
+  const float down = scale_down(byte);
+  const u32x4 y = {to_e4m3(x[0][0], x[0][1], down), to_e4m3(x[0][2], x[0][3], down),
+                   to_e4m3(x[1][0], x[1][1], down), to_e4m3(x[1][2], x[1][3], down)};
+  if (k < a.Dp) {
+    *reinterpret_cast<u32x4*>(a.hq + static_cast<int64_t>(b) * a.Dp + k) = y;
+    if (threadIdx.x % 8 == 0)
+      a.hscale[static_cast<int64_t>(k / kQuantBlock) * a.Bp + b] = static_cast<uint8_t>(byte);
   }
   if constexpr (TARGETS) {
     if (loc < 0) return;  // (block-uniform)
+    float z = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const bf16x8 p = widen(y[2 * j], y[2 * j + 1], scale_up(byte));
+      const bf16x8 q = widen(w[2 * j], w[2 * j + 1], scale_up(wbyte));
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        z = __builtin_fmaf(static_cast<float>(p[c]), static_cast<float>(q[c]), z);
+    }
 #pragma unroll
     for (int d = kWave / 2; d >= 1; d >>= 1) z += __shfl_xor(z, d, kWave);
     if (lane == 0) s_sum[threadIdx.x / kWave] = z;
     __syncthreads();
     if (threadIdx.x == 0) {
-      for (int w = 1; w < 256 / kWave; ++w) z += s_sum[w];
+      for (int v = 1; v < static_cast<int>(blockDim.x) / kWave; ++v) z += s_sum[v];
       a.target[b] = z * score_inv_t(a.temperature, b);
     }
   }
@@ -195,8 +199,9 @@ hipError_t launch_pack_fp8(const uint8_t* q, int32_t V, int32_t D, uint8_t* pack
 }
 
 hipError_t launch_quantize_rows(const Fp8Args& a, hipStream_t stream) {
-  if (a.ids != nullptr) quantize_rows_kernel<true><<<a.B, 256, 0, stream>>>(a);
-  else quantize_rows_kernel<false><<<a.B, 256, 0, stream>>>(a);
+  const unsigned threads = static_cast<unsigned>(round_up(a.Dp / 16, kWave));
+  if (a.ids != nullptr) quantize_rows_kernel<true><<<a.B, threads, 0, stream>>>(a);
+  else quantize_rows_kernel<false><<<a.B, threads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -21,14 +21,16 @@ namespace fs {
 // what 8-bit ones would round (fs_fp8_tile.hpp).  h is quantised as it is loaded:
 // the four lanes that share a row hold a block's 128 columns between them.
 //
-// The partial sums of the waves meet in LDS; the wave whose turn it is adds them
-// in wave order and hands the 16 rows' logits to its output.
-template <int OUT, int NT, int NW, int KS, int P, bool WHOLE, int C = 1>
+// The partial sums of the waves meet in LDS, U groups at a time; the wave whose turn it
+// is adds a group's in wave order and hands the 16 rows' logits to its output.  A block
+// takes C neighbouring groups (a multiple of U), then those of the next sweep.
+template <int OUT, int NT, int NW, int KS, int P, bool WHOLE, int C, int U>
 __global__ __launch_bounds__(NW * kWave) void fp8_stream_kernel(Fp8Args a) {
   static_assert(KS % P == 0, "the load ring must tile a group");
   static_assert(KS % 2 == 0, "a wave holds whole blocks");
+  static_assert(C % U == 0, "groups that meet are neighbours");
   extern __shared__ __attribute__((aligned(16))) unsigned char dyn_smem[];
-  f32x4* red = reinterpret_cast<f32x4*>(dyn_smem);  // [2][NW][NT][kWave]
+  f32x4* red = reinterpret_cast<f32x4*>(dyn_smem);  // [2][NW][U * NT][kWave]
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int li = lane & 15, kb = lane >> 4;
@@ -113,37 +115,42 @@ __global__ __launch_bounds__(NW * kWave) void fp8_stream_kernel(Fp8Args a) {
   int sc = scales(nth(0)), sc_next = scales(nth(1));
   u32x4 ring[P];
   static_for<P>([&](auto p) FS_INLINE { ring[p] = load(wp, p); });
-  for (int it = 0, g = nth(0); g < ngroups; ++it, g = nth(it)) {
-    f32x4 acc[NT];
-    static_for<NT>([&](auto n) FS_INLINE { acc[n] = f32x4{0.f, 0.f, 0.f, 0.f}; });
+  for (int it = 0; nth(it * U) < ngroups; ++it) {
+    f32x4 acc[U][NT];
     int live = whole_steps;
     if constexpr (!WHOLE) asm volatile("" : "+s"(live));  // (compared anew: masks would fill registers)
-    static_for<KS>([&](auto st) FS_INLINE {
-      constexpr int s = decltype(st)::value, slot = s % P;
-      const float up = scale_up(__builtin_amdgcn_readlane(sc, s / 2));
-      u32x4 x = ring[slot];
-      if (!WHOLE && s >= live) x = u32x4{0u, 0u, 0u, 0u};
-      const bf16x8 w0 = widen(x[0], x[1], up), w1 = widen(x[2], x[3], up);
-      static_for<NT>([&](auto n) FS_INLINE {
-        acc[n] = mfma16(w0, hreg[s][0][n], acc[n]);
-        acc[n] = mfma16(w1, hreg[s][1][n], acc[n]);
+    static_for<U>([&](auto u) FS_INLINE {
+      static_for<NT>([&](auto n) FS_INLINE { acc[u][n] = f32x4{0.f, 0.f, 0.f, 0.f}; });
+      static_for<KS>([&](auto st) FS_INLINE {
+        constexpr int s = decltype(st)::value, slot = s % P;
+        const float up = scale_up(__builtin_amdgcn_readlane(sc, s / 2));
+        u32x4 x = ring[slot];
+        if (!WHOLE && s >= live) x = u32x4{0u, 0u, 0u, 0u};
+        const bf16x8 w0 = widen(x[0], x[1], up), w1 = widen(x[2], x[3], up);
+        static_for<NT>([&](auto n) FS_INLINE {
+          acc[u][n] = mfma16(w0, hreg[s][0][n], acc[u][n]);
+          acc[u][n] = mfma16(w1, hreg[s][1][n], acc[u][n]);
+        });
+        if constexpr (s + P < KS) ring[slot] = load(wp, s + P);
+        else ring[slot] = load(wn, s + P - KS);
       });
-      if constexpr (s + P < KS) ring[slot] = load(wp, s + P);
-      else ring[slot] = load(wn, s + P - KS);
+      wp = wn;
+      wn = group(nth(it * U + u + 2));
+      sc = sc_next;
+      sc_next = scales(nth(it * U + u + 2));
     });
-    wp = wn;
-    wn = group(nth(it + 2));
-    sc = sc_next;
-    sc_next = scales(nth(it + 2));
     const int par = it & 1;
-    static_for<NT>([&](auto n) FS_INLINE {
-      red[((par * NW + wave) * NT + n) * kWave + lane] = acc[n];
+    static_for<U * NT>([&](auto q) FS_INLINE {
+      red[((par * NW + wave) * U * NT + q) * kWave + lane] =
+          acc[decltype(q)::value / NT][decltype(q)::value % NT];
     });
     __syncthreads();
-    static_for<NT>([&](auto n) FS_INLINE {
-      if ((n + it) % NW == wave) {
-        f32x4 z = red[((par * NW + 0) * NT + n) * kWave + lane];
-        for (int w = 1; w < NW; ++w) z += red[((par * NW + w) * NT + n) * kWave + lane];
+    static_for<U * NT>([&](auto q) FS_INLINE {
+      constexpr std::integral_constant<int, decltype(q)::value % NT> n{};
+      const int g = nth(it * U + q / NT);
+      if ((q + it * U) % NW == wave && g < ngroups) {
+        f32x4 z = red[((par * NW + 0) * U * NT + q) * kWave + lane];
+        for (int w = 1; w < NW; ++w) z += red[((par * NW + w) * U * NT + q) * kWave + lane];
         const int row0 = g * 16, b = n * 16 + li, v0 = row0 + 4 * kb;
         if constexpr (OUT == kTokenScores) {
           float zt = 0.0f;
@@ -215,12 +222,12 @@ __global__ __launch_bounds__(NW * kWave) void fp8_stream_kernel(Fp8Args a) {
   }
 }
 
-template <int OUT, int NT, int NW, int KS, int P, int C = 1, bool WHOLE = false>
+template <int OUT, int NT, int NW, int KS, int P, int C = 1, int U = 1, bool WHOLE = false>
 hipError_t launch_fp8_shape(Fp8Args& a, hipStream_t stream) {
   if constexpr (!WHOLE)
-    if (a.D == 64 * NW * KS) return launch_fp8_shape<OUT, NT, NW, KS, P, C, true>(a, stream);
-  const auto kernel = fp8_stream_kernel<OUT, NT, NW, KS, P, WHOLE, C>;
-  constexpr size_t smem = 2ull * NW * NT * kWave * sizeof(f32x4);
+    if (a.D == 64 * NW * KS) return launch_fp8_shape<OUT, NT, NW, KS, P, C, U, true>(a, stream);
+  const auto kernel = fp8_stream_kernel<OUT, NT, NW, KS, P, WHOLE, C, U>;
+  constexpr size_t smem = 2ull * NW * U * NT * kWave * sizeof(f32x4);
   static_assert(smem <= 64 * 1024, "LDS");
   static OccupancyCache cache;
   int slots = resident_blocks(kernel, NW * kWave, smem, cache);
@@ -232,9 +239,11 @@ hipError_t launch_fp8_shape(Fp8Args& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Waves per block, steps per wave, loads ahead and neighbouring groups per sweep, by
-// row length; 128256 rows, us.  One row of 4096: sixteen waves taking 128 KB (two
-// groups) in a row 78.6, one group 83.6, eight waves 82.3 to 85.  32 rows there: eight
+// Waves per block, steps per wave, loads ahead, neighbouring groups per sweep and
+// groups that meet at a time, by row length; 128256 rows, us.  One row of 4096: sixteen
+// waves taking 128 KB (two groups) in a row that meet together 77.5, one by one 79 to 81,
+// one group at a time 83.6, eight waves 79.5 to 85 (meeting in twos costs 32 rows 1 to 4,
+// one row of 8192 10, and is alike elsewhere).  32 rows there: eight
 // waves four loads ahead and two groups 84, one group 87.7, a whole group ahead 92,
 // sixteen waves 86.  5120: five ahead 97.8, ten 100.9; 6144: sixteen waves three ahead
 // 115, six 119, eight waves 119; 8192: sixteen waves four ahead 155, eight ahead (they
@@ -248,7 +257,7 @@ hipError_t launch_fp8_rows(Fp8Args& a, hipStream_t stream) {
   if (a.B <= 16) {
     if (D <= 1024) return launch_fp8_shape<OUT, 1, 8, 2, 2>(a, stream);
     if (D <= 2048) return launch_fp8_shape<OUT, 1, 8, 4, 4>(a, stream);
-    if (D <= 4096) return launch_fp8_shape<OUT, 1, 16, 4, 4, 2>(a, stream);
+    if (D <= 4096) return launch_fp8_shape<OUT, 1, 16, 4, 4, 2, 2>(a, stream);
     if (D <= 5120) return launch_fp8_shape<OUT, 1, 8, 10, 5>(a, stream);
     if (D <= 6144) return launch_fp8_shape<OUT, 1, 16, 6, 3>(a, stream);
     return launch_fp8_shape<OUT, 1, 16, 8, 4>(a, stream);

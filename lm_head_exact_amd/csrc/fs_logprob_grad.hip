@@ -378,68 +378,6 @@ void grad_weights_kernel(GradArgs a) {
       [&](int r, int c) FS_INLINE { return v0 + r < a.nv && c0 + c < a.D; });
 }
 
-// The targets' rows of dW: what the product left on the side plus each target's
-// own term, in the order of the places, rounded once.  One block per place,
-// which has something to do where it is its target's first; a thread takes
-// eight columns.  The block looks through its tile's targets 256 at a time for
-// those that are its own, then adds these.  9 us for 513 rows, 25 for 4096.
-__global__ __launch_bounds__(256) void grad_target_rows_kernel(GradArgs a) {
-  constexpr int kThreads = 256, kWaves = kThreads / kWave, kAhead = 8;
-  __shared__ int32_t s_place[kThreads + kAhead];
-  __shared__ int32_t s_count[kWaves];
-  const int p = blockIdx.x;
-  if (p >= a.count[0]) return;
-  const int loc = a.loc[p];
-  if (loc < 0 || a.first[loc] != p) return;
-  const int2 range = a.tile[loc / kTargetTile];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  typedef float f32x8 __attribute__((ext_vector_type(8)));
-  const int span = gridDim.y * kThreads * 8;
-  for (int d0 = blockIdx.y * kThreads * 8; d0 < a.D; d0 += span) {  // uniform
-    const int d = d0 + static_cast<int>(threadIdx.x) * 8;
-    const bool in = d < a.D;
-    f32x8 x = {};
-    if (in) x = *reinterpret_cast<const f32x8*>(a.side + static_cast<size_t>(p) * a.D + d);
-    for (int i0 = range.x; i0 < range.y; i0 += kThreads) {
-      const int i = i0 + static_cast<int>(threadIdx.x);
-      const int q = i < range.y ? a.list[i] : -1;
-      const bool own = q >= 0 && a.loc[q] == loc;
-      const uint64_t votes = __ballot(own);
-      if (lane == 0) s_count[wave] = __popcll(votes);
-      __syncthreads();
-      int at = 0, n = 0;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        at += w < wave ? s_count[w] : 0;
-        n += s_count[w];
-      }
-      if (own) s_place[at + __popcll(votes & ((uint64_t{1} << lane) - 1))] = q;
-      __syncthreads();
-      for (int k0 = 0; in && k0 < n; k0 += kAhead) {
-        bf16x8 h[kAhead];
-        float t[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const int k = min(k0 + u, n - 1);
-          t[u] = k0 + u < n ? a.term[s_place[k]].target : 0.0f;
-          h[u] = load_frag(a.hz + static_cast<size_t>(s_place[k]) * a.Dp + d);
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-          if (k0 + u < n)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = __builtin_fmaf(t[u], static_cast<float>(h[u][j]), x[j]);
-      }
-      __syncthreads();  // s_place and s_count are free again
-    }
-    if (in) {
-      uint64_t* out = reinterpret_cast<uint64_t*>(a.dW + static_cast<size_t>(loc) * a.D + d);
-      out[0] = pack_bf16(x[0], x[1], x[2], x[3]);
-      out[1] = pack_bf16(x[4], x[5], x[6], x[7]);
-    }
-  }
-}
-
 // x + t * w for four consecutive columns of a row of W.
 __device__ __forceinline__ f32x4 add_target(f32x4 x, float t, const __bf16* w) {
   typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -501,33 +439,120 @@ void grad_hidden_kernel(GradArgs a) {
   });
 }
 
-// The slabs of each row and its target's term, added in a fixed order and
-// rounded once.  A block takes one row's 256 columns; its GROUPS groups of 64
-// threads split the slabs.  Bound by reading them (4096 rows of 4096, three
-// quarters of them with a token: 59 us).
-template <int GROUPS>
-__global__ __launch_bounds__(GROUPS * kWave) void grad_slabs_kernel(GradArgs a) {
-  __shared__ f32x4 s_sum[GROUPS][kWave];
-  const int b = blockIdx.x, lane = threadIdx.x & (kWave - 1), group = threadIdx.x / kWave;
-  if (b >= a.count[0]) return;
-  const int splits = a.count[1];
-  const int d = blockIdx.y * (kWave * 4) + lane * 4;
-  f32x4 x = {0.f, 0.f, 0.f, 0.f};
-  if (d < a.D) {
-    const float* p = a.slab + static_cast<size_t>(b) * a.D + d;
-    const size_t step = static_cast<size_t>(a.B) * a.D;
-#pragma unroll 4
-    for (int s = group; s < splits; s += GROUPS) x += *reinterpret_cast<const f32x4*>(p + s * step);
-  }
-  s_sum[group][lane] = x;
-  __syncthreads();
-  if (group != 0 || d >= a.D) return;
+// The targets' rows of dW: what the product left on the side plus each target's
+// own term, in the order of the places, rounded once.  One block per place (and part
+// y of ny of its columns), which has something to do where it is its target's first;
+// a thread takes eight columns.  The block looks through its tile's targets THREADS
+// at a time for those that are its own, then adds these.
+template <int THREADS>
+__device__ void finish_target_row(const GradArgs& a, int p, int y, int ny) {
+  constexpr int kWaves = THREADS / kWave, kAhead = 8;
+  __shared__ int32_t s_place[THREADS + kAhead];
+  __shared__ int32_t s_count[kWaves];
+  if (p >= a.count[0]) return;
+  const int loc = a.loc[p];
+  if (loc < 0 || a.first[loc] != p) return;
+  const int2 range = a.tile[loc / kTargetTile];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  typedef float f32x8 __attribute__((ext_vector_type(8)));
+  const int span = ny * THREADS * 8;
+  for (int d0 = y * THREADS * 8; d0 < a.D; d0 += span) {  // uniform
+    const int d = d0 + static_cast<int>(threadIdx.x) * 8;
+    const bool in = d < a.D;
+    f32x8 x = {};
+    if (in) x = *reinterpret_cast<const f32x8*>(a.side + static_cast<size_t>(p) * a.D + d);
+    for (int i0 = range.x; i0 < range.y; i0 += THREADS) {
+      const int i = i0 + static_cast<int>(threadIdx.x);
+      const int q = i < range.y ? a.list[i] : -1;
+      const bool own = q >= 0 && a.loc[q] == loc;
+      const uint64_t votes = __ballot(own);
+      if (lane == 0) s_count[wave] = __popcll(votes);
+      __syncthreads();
+      int at = 0, n = 0;
 #pragma unroll
-  for (int g = 1; g < GROUPS; ++g) x += s_sum[g][lane];
+      for (int w = 0; w < kWaves; ++w) {
+        at += w < wave ? s_count[w] : 0;
+        n += s_count[w];
+      }
+      if (own) s_place[at + __popcll(votes & ((uint64_t{1} << lane) - 1))] = q;
+      __syncthreads();
+      for (int k0 = 0; in && k0 < n; k0 += kAhead) {
+        bf16x8 h[kAhead];
+        float t[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int k = min(k0 + u, n - 1);
+          t[u] = k0 + u < n ? a.term[s_place[k]].target : 0.0f;
+          h[u] = load_frag(a.hz + static_cast<size_t>(s_place[k]) * a.Dp + d);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (k0 + u < n)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __builtin_fmaf(t[u], static_cast<float>(h[u][j]), x[j]);
+      }
+      __syncthreads();  // s_place and s_count are free again
+    }
+    if (in) {
+      uint64_t* out = reinterpret_cast<uint64_t*>(a.dW + static_cast<size_t>(loc) * a.D + d);
+      out[0] = pack_bf16(x[0], x[1], x[2], x[3]);
+      out[1] = pack_bf16(x[4], x[5], x[6], x[7]);
+    }
+  }
+}
+
+// The slabs of columns d .. d + 3 of place b and its target's term, added in a fixed
+// order and rounded once.
+template <int GROUPS>
+__device__ f32x4 sum_slabs(const GradArgs& a, int b, int d, int group) {
+  f32x4 x = {0.f, 0.f, 0.f, 0.f};
+  const int splits = a.count[1];
+  const float* p = a.slab + static_cast<size_t>(b) * a.D + d;
+  const size_t step = static_cast<size_t>(a.B) * a.D;
+#pragma unroll 4
+  for (int s = group; s < splits; s += GROUPS) x += *reinterpret_cast<const f32x4*>(p + s * step);
+  return x;
+}
+__device__ __forceinline__ void finish_hidden(const GradArgs& a, int b, int d, f32x4 x) {
   const int loc = a.loc[b];
   if (loc >= 0) x = add_target(x, a.term[b].target, a.W + static_cast<size_t>(loc) * a.D + d);
   *reinterpret_cast<uint64_t*>(a.dh + static_cast<size_t>(a.row[b]) * a.D + d) =
       pack_bf16(x[0], x[1], x[2], x[3]);
+}
+
+// What is left of both gradients, side by side in one launch: blocks (place, y) make
+// the targets' rows of dW for y below `chunks`, and above that add up dh's slabs, a
+// wave or GROUPS waves for 256 columns.  Bound by reading the slabs (4096 rows of 4096,
+// three quarters of them with a token: 73 us; 25 and 59 one after the other; 513 rows on
+// a shard 16, 9 and 12; 4 rows on 1000 x 256 37.0 us a call, 39.6 by two launches).  GROUPS 16
+// where the blocks are few (4 rows of 1024: the call's dh 35.0 us by sixteen groups,
+// 39.3 by one; 300 rows of 4096: 256, 243).
+template <int GROUPS>
+__global__ __launch_bounds__(GROUPS == 1 ? 256 : GROUPS * kWave) void grad_finish_kernel(
+    GradArgs a, int32_t chunks) {
+  constexpr int kThreads = GROUPS == 1 ? 256 : GROUPS * kWave;
+  const int b = blockIdx.x, lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  if (static_cast<int>(blockIdx.y) < chunks) {  // (block-uniform)
+    finish_target_row<kThreads>(a, b, blockIdx.y, chunks);
+    return;
+  }
+  if (b >= a.count[0]) return;
+  const int at = static_cast<int>(blockIdx.y) - chunks;
+  if constexpr (GROUPS == 1) {
+    const int d = (at * (kThreads / kWave) + wave) * (kWave * 4) + lane * 4;
+    if (d < a.D) finish_hidden(a, b, d, sum_slabs<1>(a, b, d, 0));
+  } else {
+    __shared__ f32x4 s_sum[GROUPS][kWave];
+    const int d = at * (kWave * 4) + lane * 4;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    if (d < a.D) x = sum_slabs<GROUPS>(a, b, d, wave);
+    s_sum[wave][lane] = x;
+    __syncthreads();
+    if (wave != 0 || d >= a.D) return;
+#pragma unroll
+    for (int g = 1; g < GROUPS; ++g) x += s_sum[g][lane];
+    finish_hidden(a, b, d, x);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -670,22 +695,17 @@ hipError_t launch_grad_products(const GradArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_grad_finish(const GradArgs& a, hipStream_t s) {
-  hipError_t e = hipSuccess;
-  if (a.dW != nullptr && a.B > 0) {
-    const int chunks = (a.D + 2047) / 2048;
-    grad_target_rows_kernel<<<dim3(a.B, chunks < 64 ? chunks : 64), 256, 0, s>>>(a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  if (a.dh != nullptr && a.slab != nullptr) {
-    const dim3 grid(a.B, (a.D + 4 * kWave - 1) / (4 * kWave));
-    // few blocks share out the slabs (4 rows of 1024: the call's dh 35.0 us by
-    // sixteen groups, 39.3 by one), many need not (300 rows of 4096: 256, 243)
-    if (static_cast<int64_t>(grid.x) * grid.y <= 512)
-      grad_slabs_kernel<16><<<grid, 16 * kWave, 0, s>>>(a);
-    else grad_slabs_kernel<1><<<grid, kWave, 0, s>>>(a);
-    e = hipGetLastError();
-  }
-  return e;
+  const bool rows = a.dW != nullptr && a.B > 0, slabs = a.dh != nullptr && a.slab != nullptr;
+  if (!rows && !slabs) return hipSuccess;
+  const int units = (a.D + 4 * kWave - 1) / (4 * kWave);
+  const bool few = slabs && static_cast<int64_t>(a.B) * units <= 512;
+  const int threads = few ? 16 * kWave : 256;
+  const int parts = (a.D + 8 * threads - 1) / (8 * threads);
+  const int chunks = !rows ? 0 : parts < 64 ? parts : 64;
+  const dim3 grid(a.B, chunks + (!slabs ? 0 : few ? units : (units + 3) / 4));
+  if (few) grad_finish_kernel<16><<<grid, threads, 0, s>>>(a, chunks);
+  else grad_finish_kernel<1><<<grid, threads, 0, s>>>(a, chunks);
+  return hipGetLastError();
 }
 
 // Whether every launch's grid holds fewer than 2^32 threads: the products' (the
