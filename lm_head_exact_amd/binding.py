@@ -1096,13 +1096,35 @@ def _fp8_head(h, W_packed, W_scale, V, vocab_offset, workspace):
     return dev, B, D, _workspace(workspace, fp8_workspace_bytes(B, D, V), dev)
 
 
+class _NoGradient(torch.autograd.Function):
+    """Results of the 8-bit products of an h that requires a gradient."""
+
+    @staticmethod
+    def forward(ctx, h, name, call):
+        ctx.name = name
+        return call()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.name}: no gradient leads through the 8-bit head")
+
+
+def _records(h, out) -> bool:
+    return (out is None and isinstance(h, torch.Tensor) and h.requires_grad
+            and torch.is_grad_enabled())
+
+
 def logits_fp8(h: torch.Tensor, W_packed: torch.Tensor, W_scale: torch.Tensor, V: int,
                dtype=torch.float32, out: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """fs_logits_fp8: logits [B][V] (fp32 or bf16) of hidden states h (bf16 [B][D],
     quantised by the call) and the 8-bit head of quantize_weights_fp8.  out: a
     tensor [B][V] of either type to write into, whose rows may lie further apart
-    than V.  Carries no graph."""
+    than V.  No gradient leads through the 8-bit head: where torch records them and h
+    requires one, the backward pass of the result raises."""
+    if _records(h, out):
+        return _NoGradient.apply(h, "logits_fp8", lambda: logits_fp8(h, W_packed, W_scale, V, dtype,
+                                                                     None, workspace))
     dev, B, D, ws = _fp8_head(h, W_packed, W_scale, V, 0, workspace)
     given = out
     if out is None:
@@ -1137,7 +1159,11 @@ def token_logprobs_fp8(h: torch.Tensor, W_packed: torch.Tensor, W_scale: torch.T
                        vocab_offset: int = 0, out=None, workspace: Optional[torch.Tensor] = None):
     """fs_token_logprobs_fp8: token_logprobs on the 8-bit head of
     quantize_weights_fp8 (what a rollout stores when it samples with sample_fp8):
-    (logprob, lse), which carry no graph."""
+    (logprob, lse).  No gradient leads through the 8-bit head: where torch records
+    them and h requires one, the backward pass of the results raises."""
+    if _records(h, out):
+        return _NoGradient.apply(h, "token_logprobs_fp8", lambda: token_logprobs_fp8(
+            h, W_packed, W_scale, V, temperature, token_ids, vocab_offset, None, workspace))
     dev, B, D, ws = _fp8_head(h, W_packed, W_scale, V, vocab_offset, workspace)
     _row(temperature, "temperature", torch.float32, B, dev)
     if token_ids is None:

@@ -136,6 +136,32 @@ def test_logits_made_twice(smoothing):
     check(h, W, t, got, want, smoothing=smoothing, z_loss=1e-3, e=e)
 
 
+@pytest.mark.parametrize("B", [255, 256, 257, 1023, 1024, 1025, 2047, 2048])
+def test_row_counts_where_kernels_change(B):
+    """Places in one launch or three, and the merge of the pairs; equal targets and
+    targets at the ends of the vocabulary's tiles of 256 rows."""
+    h, W, t = make(B, 72, 600, seed=18, ignore=0.3)
+    t[5:B:7] = torch.tensor([0, 255, 256, 511, 512, 599, -100, 17], dtype=torch.int32).repeat(B)[:len(t[5:B:7])]
+    case(h, W, t, z_loss=1e-3)
+    hd, Wd, td = h.cuda(), W.cuda(), t.cuda()
+    _, _, gh, gw = fs.cross_entropy(hd, Wd, td, reduction="sum")
+    lp, lse = fs.token_logprobs(hd, Wd, None, td)
+    for need_h, need_W in ((True, True), (False, True)):
+        bh, bw = fs.token_logprobs_backward(hd, Wd, None, td, lp, lse, -torch.ones_like(lp), 0, need_h, need_W)
+        assert (gw.double() - bw.double()).norm() <= 2.0 ** -7 * bw.double().norm()
+        assert bh is None or (gh.double() - bh.double()).norm() <= 2.0 ** -7 * bh.double().norm()
+
+
+def test_nothing_carries_a_graph():
+    h, W, t = (x.cuda() for x in make(8, 64, 100, seed=19))
+    h.requires_grad_(True)
+    assert not any(x.requires_grad for x in fs.cross_entropy(h, W, t))
+    fs.cross_entropy(h, W, t)
+    gh = fs.cross_entropy(h, W, t)[2]
+    h.backward(gh)
+    assert torch.equal(h.grad, gh)
+
+
 @pytest.mark.parametrize("need_h,need_W", [(True, False), (False, True)])
 def test_one_gradient(need_h, need_W):
     h, W, t = make(150, 96, 800, seed=4)

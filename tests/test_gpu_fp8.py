@@ -301,6 +301,28 @@ def test_given_outputs_and_refusals(B):
         fs.token_logprobs_fp8(*c.args, T, ids, vocab_offset=2 ** 32)
 
 
+@pytest.mark.parametrize("B", [4, 40])
+def test_no_gradient_leads_through(B):
+    """Results of an h that requires a gradient equal the others; their backward pass
+    raises.  Nothing is recorded without gradients or into given outputs."""
+    c = Head(B, 128, 200, seed=13)
+    h = c.args[0].clone().requires_grad_(True)
+    _, ids = targets(B, 200, 0)
+    ids = ids.cuda()
+    z, want = fs.logits_fp8(h, *c.args[1:]), fs.logits_fp8(*c.args)
+    lp, lse = fs.token_logprobs_fp8(h, *c.args[1:], None, ids)
+    wlp, wlse = fs.token_logprobs_fp8(*c.args, None, ids)
+    assert torch.equal(z, want) and torch.equal(lp, wlp) and torch.equal(lse, wlse)
+    for y in (z, lp, lse):
+        with pytest.raises(RuntimeError, match="8-bit head"):
+            y.sum().backward()
+    assert h.grad is None
+    with torch.no_grad():
+        assert not fs.logits_fp8(h, *c.args[1:]).requires_grad
+    assert not fs.logits_fp8(h, *c.args[1:], out=torch.empty_like(want)).requires_grad
+    assert not fs.sample_fp8(h, *c.args[1:], torch.ones(B, device="cuda"), 1, 2)[1].requires_grad
+
+
 @pytest.mark.parametrize("B", [12, 70])
 def test_graph_replays(B):
     """Quantising, sampling, scoring and logits in one graph, replayed on new weights."""
