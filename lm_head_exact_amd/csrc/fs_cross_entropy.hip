@@ -400,9 +400,14 @@ int wave_rows(LogitsTile t) {
   }
 }
 
-bool keeps(int32_t B, int32_t V) {
-  return 2 * static_cast<int64_t>(round_up(B, 256)) * static_cast<int64_t>(round_up(V, 256)) <=
-         kKeptBytes;
+// Where D is small and the rows many, the fourth product costs less than the memory
+// that the kept exponentials pass through (4096 rows on 20000, us kept and made twice:
+// D = 64 278 and 248, 128 292 and 266, 256 324 and 320, 384 365 and 380, 1024 605 and 696;
+// of 300 rows on 30000, which the caches hold, kept wins from D = 64 on: 74 and 78).
+bool keeps(int32_t B, int32_t D, int32_t V) {
+  return (D > 256 || B <= 512) &&
+         2 * static_cast<int64_t>(round_up(B, 256)) * static_cast<int64_t>(round_up(V, 256)) <=
+             kKeptBytes;
 }
 
 struct XentPlan {
@@ -412,7 +417,7 @@ struct XentPlan {
   int32_t S, sub;
   size_t part, zsum, zt, rows, total;
   XentPlan(int32_t B, int32_t D, int32_t V, bool grads)
-      : keep(keeps(B, V)), g(B, D, V, keep) {
+      : keep(keeps(B, D, V)), g(B, D, V, keep, true) {
     tile = logits_tile(B, g.slice < V ? g.slice : V, true);
     sub = wave_rows(tile);
     // the last slice's tiles may end before it does

@@ -7,6 +7,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 
 #include "fs_host.hpp"
 #include "fs_internal.hpp"
@@ -43,9 +44,10 @@ struct GradArgs {
   int32_t* list;      // [Bp]: places that have a target here, by tile
   int2* tile;         // [tiles]: begin and end in `list`
   float* side;        // [Bp][D]: dW rows of targets, at their first place
+  float* wslab;       // [w_splits][V][D] where the rows are taken in parts for dW, or null
   int32_t Dp, Bp, ldz;
   int32_t v0, nv;     // the slice: rows v0 .. v0 + nv of W
-  int32_t max_splits, hidden_tb, first_slice;
+  int32_t max_splits, hidden_tb, first_slice, w_splits;
 };
 
 constexpr int kTargetTile = 256;
@@ -68,14 +70,29 @@ inline int32_t target_tiles(int32_t V) {
   return static_cast<int32_t>((static_cast<int64_t>(V) + kTargetTile - 1) / kTargetTile);
 }
 
+// Parts of the rows for dW.  Its tiles of 256 vocabulary rows by 128 columns are few
+// where both are small, and many rows leave each a long way: 6922 rows of 488 on 1633
+// take 111 us in 28 blocks (a call 218 us, 139 in parts; 3990 of 256 on 1933 144 and 104,
+// 8192 of 1024 on 4000 347 and 301).  A block's 32 rows take about half a microsecond;
+// every part writes and reads V x D in fp32 at about 5 TB/s, and one launch more adds
+// them up: taken where that saves a few microseconds.
+inline int32_t weight_splits(int32_t B, int32_t D, int32_t V) {
+  const int64_t tiles = (static_cast<int64_t>(V) + 255) / 256 * ((D + 127) / 128);
+  if (tiles >= 256 || B < 512) return 1;
+  const double whole = B / 64.0, each = 1.6e-6 * V * D;
+  const int64_t s = std::min<int64_t>({static_cast<int64_t>(std::sqrt(whole / each)), 512 / tiles,
+                                       B / 256});
+  return s > 1 && whole - whole / s - each * s > 8.0 ? static_cast<int32_t>(s) : 1;
+}
+
 // Sizes and workspace of a call.  `whole`: dz is kept for the whole vocabulary, in
 // slices of up to kMaxSlice rows one behind the other, instead of one slice of
-// kSliceBytes at a time.
+// kSliceBytes at a time.  `parts`: dW may take the rows in parts.
 struct GradPlan {
-  int32_t Bp, Dp, slice, slices, splits, TB;
+  int32_t Bp, Dp, slice, slices, splits, TB, w_splits;
   bool slabs;
-  size_t count, slot, row, loc, term, hz, dz, slab, first, list, tile, side, total;
-  GradPlan(int32_t B, int32_t D, int32_t V, bool whole_dz = false) {
+  size_t count, slot, row, loc, term, hz, dz, slab, first, list, tile, side, wslab, total;
+  GradPlan(int32_t B, int32_t D, int32_t V, bool whole_dz = false, bool parts = false) {
     TB = tile_tokens(B);
     Bp = static_cast<int32_t>(round_up(B, 256));
     Dp = static_cast<int32_t>(round_up(D, 64));
@@ -98,6 +115,7 @@ struct GradPlan {
     p = std::min({p, rows / 256, (int64_t{512} << 20) / (4 * static_cast<int64_t>(B) * D)});
     splits = static_cast<int32_t>(p < 1 ? 1 : p);
     slabs = splits > 1 || slice < V;
+    w_splits = parts && slices == 1 ? weight_splits(B, D, V) : 1;
     size_t at = 0;
     auto take = [&](size_t bytes) {
       const size_t o = at;
@@ -115,7 +133,8 @@ struct GradPlan {
     first = take(4ull * V);
     list = take(4ull * Bp);
     tile = take(sizeof(int2) * target_tiles(V));
-    side = take(4ull * Bp * D);
+    side = take(w_splits > 1 ? 0 : 4ull * Bp * D);
+    wslab = take(w_splits > 1 ? 4ull * w_splits * V * D : 0);
     total = at;
   }
 };

@@ -334,23 +334,42 @@ void grad_logits_kernel(GradArgs a) {
       [&](int, int) FS_INLINE { return true; });
 }
 
-// dW of one slice: rows v of W, columns d, summed over the rows with a target.
-template <class T>
+// dW of one slice: rows v of W, columns d, summed over the rows with a target.  SPLIT:
+// over one part of them, into the part's slab.
+template <class T, bool SPLIT>
 __global__ __launch_bounds__(T::kThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void grad_weights_kernel(GradArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char dyn_smem[];
   const int n = *a.count;
-  int tile, dtile;
-  if (!xcd_tile<4>(blockIdx.x, (a.nv + T::TB - 1) / T::TB, (a.D + T::TA - 1) / T::TA, tile, dtile))
+  const int nd = (a.D + T::TA - 1) / T::TA;
+  int tile, at;
+  if (!xcd_tile<4>(blockIdx.x, (a.nv + T::TB - 1) / T::TB, SPLIT ? nd * a.w_splits : nd, tile, at))
     return;
-  const int a0 = dtile * T::TA, b0 = tile * T::TB;
+  const int a0 = (SPLIT ? at % nd : at) * T::TA, b0 = tile * T::TB;
   const Operand h = {a.hz, a.Dp, a.D, a.Bp};
   const Operand z = {a.dz, a.ldz, a.ldz, a.Bp};
+  const int nk = (n + T::BK - 1) / T::BK;
+  const int part = SPLIT ? at / nd : 0;
+  const int kt0 = SPLIT ? static_cast<int>(static_cast<int64_t>(nk) * part / a.w_splits) : 0;
+  const int kt1 = SPLIT ? static_cast<int>(static_cast<int64_t>(nk) * (part + 1) / a.w_splits) : nk;
   f32x4 acc[T::MR][T::NT];
-  if (n > 0) T::run(h, z, a0, b0, 0, (n + T::BK - 1) / T::BK, acc, dyn_smem);
+  if (kt0 < kt1) T::run(h, z, a0, b0, kt0, kt1, acc, dyn_smem);
   else zero_acc(acc);
   const int lane = threadIdx.x & (kWave - 1), li = lane & 15, kb = lane >> 4;
   const int d0 = a0 + T::wave_a() + 4 * kb;
+  if constexpr (SPLIT) {
+    static_for<T::NT>([&](auto n) FS_INLINE {
+      const int v = b0 + T::wave_b() + 16 * static_cast<int>(n) + li;
+      if (v < a.nv) {
+        float* slab = a.wslab + (static_cast<size_t>(part) * a.V + v) * a.D + d0;
+        static_for<T::MR>([&](auto m) FS_INLINE {
+          if (d0 + 16 * static_cast<int>(m) < a.D)
+            *reinterpret_cast<f32x4*>(slab + 16 * static_cast<int>(m)) = acc[m][n];
+        });
+      }
+    });
+    return;
+  }
   // rows that are a target go to the side in fp32, the others to dW
   int place[T::NT];
   static_for<T::NT>([&](auto n) FS_INLINE {
@@ -460,7 +479,11 @@ __device__ void finish_target_row(const GradArgs& a, int p, int y, int ny) {
     const int d = d0 + static_cast<int>(threadIdx.x) * 8;
     const bool in = d < a.D;
     f32x8 x = {};
-    if (in) x = *reinterpret_cast<const f32x8*>(a.side + static_cast<size_t>(p) * a.D + d);
+    if (in && a.w_splits == 1)
+      x = *reinterpret_cast<const f32x8*>(a.side + static_cast<size_t>(p) * a.D + d);
+    for (int s = 0; in && a.w_splits > 1 && s < a.w_splits; ++s)
+      x += *reinterpret_cast<const f32x8*>(
+          a.wslab + (static_cast<size_t>(s) * a.V + loc) * a.D + d);
     for (int i0 = range.x; i0 < range.y; i0 += THREADS) {
       const int i = i0 + static_cast<int>(threadIdx.x);
       const int q = i < range.y ? a.list[i] : -1;
@@ -498,6 +521,20 @@ __device__ void finish_target_row(const GradArgs& a, int p, int y, int ny) {
       out[0] = pack_bf16(x[0], x[1], x[2], x[3]);
       out[1] = pack_bf16(x[4], x[5], x[6], x[7]);
     }
+  }
+}
+
+// The rows of dW that are no target, from their parts: added in order, rounded once.
+__global__ __launch_bounds__(256) void grad_weight_slabs_kernel(GradArgs a) {
+  const int quads = a.D / 4;
+  const int64_t total = static_cast<int64_t>(a.V) * quads;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += 256ll * gridDim.x) {
+    if (a.first[i / quads] >= 0) continue;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < a.w_splits; ++s)
+      x += *reinterpret_cast<const f32x4*>(a.wslab + (s * total + i) * 4);
+    *reinterpret_cast<uint64_t*>(a.dW + i * 4) = pack_bf16(x[0], x[1], x[2], x[3]);
   }
 }
 
@@ -613,12 +650,12 @@ hipError_t launch_hidden(const GradArgs& a, hipStream_t stream) {
                               : launch_hidden<HiddenTile<256>::T>(a, stream);
 }
 
-template <class T>
+template <class T, bool SPLIT = false>
 hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
   static SmemRaised raised;
-  return launch_tiles(&grad_weights_kernel<T>, raised,
+  return launch_tiles(&grad_weights_kernel<T, SPLIT>, raised,
                       static_cast<int64_t>((a.nv + T::TB - 1) / T::TB) *
-                          ((a.D + T::TA - 1) / T::TA),
+                          ((a.D + T::TA - 1) / T::TA) * (SPLIT ? a.w_splits : 1),
                       T::kThreads, T::kSmemBytes, a, stream);
 }
 
@@ -628,6 +665,7 @@ hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
 // many rounds the tall blocks read less (2048 tokens on the whole of it 1793
 // against 1860 us, equal at 512).
 hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
+  if (a.w_splits > 1) return launch_weights<WeightsShort, true>(a, stream);
   const int64_t tall = static_cast<int64_t>((a.nv + 255) / 256) * ((a.D + 255) / 256);
   return a.B > 512 && tall >= 16 * 256 ? launch_weights<WeightsTall>(a, stream)
                                        : launch_weights<WeightsShort>(a, stream);
@@ -663,6 +701,8 @@ void grad_workspace(GradArgs& a, const GradPlan& p, char* ws) {
   a.list = reinterpret_cast<int32_t*>(ws + p.list);
   a.tile = reinterpret_cast<int2*>(ws + p.tile);
   a.side = reinterpret_cast<float*>(ws + p.side);
+  a.wslab = reinterpret_cast<float*>(ws + p.wslab);
+  a.w_splits = p.w_splits;
   a.Dp = p.Dp;
   a.Bp = p.Bp;
   a.ldz = p.slice;
@@ -697,6 +737,12 @@ hipError_t launch_grad_products(const GradArgs& a, hipStream_t s) {
 hipError_t launch_grad_finish(const GradArgs& a, hipStream_t s) {
   const bool rows = a.dW != nullptr && a.B > 0, slabs = a.dh != nullptr && a.slab != nullptr;
   if (!rows && !slabs) return hipSuccess;
+  if (rows && a.w_splits > 1) {
+    const int64_t blocks = (static_cast<int64_t>(a.V) * a.D / 4 + 255) / 256;
+    grad_weight_slabs_kernel<<<static_cast<unsigned>(blocks < 8192 ? blocks : 8192), 256, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   const int units = (a.D + 4 * kWave - 1) / (4 * kWave);
   const bool few = slabs && static_cast<int64_t>(a.B) * units <= 512;
   const int threads = few ? 16 * kWave : 256;

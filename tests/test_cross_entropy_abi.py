@@ -60,7 +60,8 @@ def test_workspace_sizes(L):
     f = L.fs_cross_entropy_workspace_bytes
     assert f(4, 7, 1000, 1) == 0 and f(4, 256, 0, 1) == 0 and f(-1, 256, 10, 1) == 0 and f(4, 1 << 21, 9, 1) == 0
     # exponentials are kept up to 4 GiB, then a slice of 1 GiB
-    assert f(16128, 64, 128256, 1) > 2 * 16128 * 128256
+    assert f(16128, 320, 128256, 1) > 2 * 16128 * 128256
+    assert f(512, 64, 128256, 1) > 2 * 512 * 128256
     assert f(1 << 17, 64, 128256, 1) < 2 * (1 << 17) * 128256 // 4
     # none of it for the loss alone
     assert f(4096, 64, 128256, 0) < 2 * 4096 * 128256 // 8

@@ -88,6 +88,8 @@ SHAPES = [(1, 8, 1), (1, 8, 17), (2, 40, 33), (5, 4096, 301), (16, 256, 1000), (
 # one shape per tile of the logits: 256 x 64, 256 x 128, 256 x 256, 128 x 128, 64 x 64, 64 x 128
 TILES = [(200, 64, 16032), (500, 72, 16001), (1000, 64, 16030), (3833, 96, 2161), (513, 136, 2001),
          (200, 32, 7000)]
+# and those of more than 512 rows again with rows long enough for the exponentials to be kept
+TILES += [(1000, 264, 16030), (3833, 320, 2161), (513, 328, 2001)]
 
 
 @pytest.mark.parametrize("B,D,V", SHAPES)
@@ -105,6 +107,19 @@ def test_every_tile(B, D, V, smoothing, z_loss):
     alone = run(h, W, t, smoothing=smoothing, z_loss=z_loss, need_h=False, need_W=False)
     assert alone[2] is None and alone[3] is None
     assert torch.allclose(alone[1], got[1], rtol=2.0 ** -20, atol=2.0 ** -20)
+
+
+# few tiles of dW and many rows: the rows in 4, 6 and 16 parts
+@pytest.mark.parametrize("B,D,V", [(1100, 136, 900), (3000, 1000, 777), (4100, 64, 300)])
+@pytest.mark.parametrize("ignore", [0.0, 0.9, 1.0])
+def test_rows_in_parts(B, D, V, ignore):
+    h, W, t = make(B, D, V, seed=21, ignore=ignore)
+    t[::3] = torch.where(t[::3] >= 0, torch.full_like(t[::3], V - 1), t[::3])   # one target many times
+    got = case(h, W, t, smoothing=0.1, z_loss=1e-3)
+    again = run(h, W, t, smoothing=0.1, z_loss=1e-3)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    alone = run(h, W, t, smoothing=0.1, z_loss=1e-3, need_h=False)
+    assert torch.equal(alone[3], got[3])
 
 
 @pytest.mark.parametrize("smoothing", [0.0, 0.1])
