@@ -388,7 +388,7 @@ FS_API size_t fs_fp8_workspace_bytes(int32_t B, int32_t D, int32_t V);
 
 /* The logits: out_logits [B] rows of V, row_pitch elements apart (>= V; what lies
  * between rows is left as it is), bf16 (rounded once) or with out_fp32 nonzero
- * fp32.  Rows that start 16-byte aligned are written fastest. */
+ * fp32.  Rows may start at any element. */
 FS_API fs_status fs_logits_fp8(const void* h, const void* W_packed, const void* W_scale, int32_t B,
                                int32_t D, int32_t V, int32_t out_fp32, void* out_logits,
                                int64_t row_pitch, void* workspace, size_t workspace_bytes,

@@ -185,7 +185,7 @@ FS_API fs_status fs_logits_fp8(const void* h, const void* W_packed, const void* 
   if (start_launches()) return injected_failure(who);
   a.out = out_logits;
   a.ld = row_pitch;
-  a.wide = aligned(out_logits, 16) && row_pitch * size % 16 == 0;
+  a.lines = aligned(out_logits, 128) && row_pitch * size % 128 == 0;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const hipError_t e = out_fp32 ? launch_product(a, stream_logits_f32, tile_logits_f32, s)
                                 : launch_product(a, stream_logits_bf16, tile_logits_bf16, s);

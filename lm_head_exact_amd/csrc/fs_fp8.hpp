@@ -96,10 +96,10 @@ struct Fp8Args {
   uint64_t seed, step;
   float* part_val;    // [B][S]
   int32_t* part_idx;  // [B][S]
-  // logits [B][V], rows ld elements apart; wide: every row starts 16-byte aligned
+  // logits [B][V], rows ld elements apart; lines: every row starts a line of 128 bytes
   void* out;
   int64_t ld;
-  bool wide;
+  bool lines;
   int32_t S;
 };
 

@@ -164,17 +164,20 @@ __global__ __launch_bounds__(NW * kWave) void fp8_stream_kernel(Fp8Args a) {
           push_four(best[n], z, v0, a.V, static_cast<uint32_t>(a.vocab_offset + v0),
                     static_cast<uint32_t>(b), a.step, greedy[n], inv_t[n], philox);
         } else if (b < a.B) {
+          // (rows may start at any element)
           const int64_t at = b * a.ld + v0;
           if constexpr (OUT == kLogitsF32) {
+            typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
             float* o = static_cast<float*>(a.out) + at;
-            if (a.wide && v0 + 4 <= a.V) *reinterpret_cast<f32x4*>(o) = z;
+            if (v0 + 4 <= a.V) *reinterpret_cast<f32x4u*>(o) = z;
             else static_for<4>([&](auto r) FS_INLINE { if (v0 + r < a.V) o[r] = z[decltype(r)::value]; });
           } else {
             typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+            typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(2)));
             __bf16* o = static_cast<__bf16*>(a.out) + at;
             const bf16x4 y = {static_cast<__bf16>(z[0]), static_cast<__bf16>(z[1]),
                               static_cast<__bf16>(z[2]), static_cast<__bf16>(z[3])};
-            if (a.wide && v0 + 4 <= a.V) *reinterpret_cast<bf16x4*>(o) = y;
+            if (v0 + 4 <= a.V) *reinterpret_cast<u32x2u*>(o) = __builtin_bit_cast(u32x2u, y);
             else static_for<4>([&](auto r) FS_INLINE { if (v0 + r < a.V) o[r] = y[decltype(r)::value]; });
           }
         }
