@@ -514,9 +514,11 @@ FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_
  *   workspace    >= fs_cross_entropy_workspace_bytes(B, D, V, grads) bytes (0 for
  *                invalid sizes), grads nonzero where a gradient is wanted.  It
  *                holds two bytes per row and vocabulary entry, up to 4 GiB (a
- *                larger batch takes a slice of the vocabulary at a time and makes
- *                the logits twice), and what fs_token_logprobs_backward holds
- *                beside dz; without gradients a copy of h; and 12 bytes per row and
+ *                larger batch, and one of more than 512 rows with D <= 256, takes a
+ *                slice of the vocabulary at a time and makes the logits twice); what
+ *                fs_token_logprobs_backward holds beside dz; V x D in fp32 for each
+ *                of the parts that many rows on a small head are taken in; without
+ *                gradients a copy of h alone; and 12 bytes per row and
  *                16 to 128 vocabulary entries (the more rows, the more entries);
  *                contents on entry ignored
  * Logits of -inf have probability 0; NaN or +inf among a row's give NaN.  B == 0

@@ -16,6 +16,7 @@
 // vocabulary after the other, in a fourth product: 4096 rows of 4096 on 128256, three
 // quarters with a target, 8.0 ms kept and 10.2 made twice; 16000 rows 42.1 and 54.0;
 // 513 rows on a shard of 16032 x 8192 387 and 484 us; 4 rows on 1000 x 256 41 and 43).
+// Many short rows take that fourth product too (keeps()).
 // Kept is not z, which 16 bits would blur by percents of p, but exp(z - m) with m the
 // largest logit of the row within one wave's 16 to 128 vocabulary rows, and m itself
 // in fp32 on the side: with the pairs (m, sum) merged into lse, one pass over it makes
