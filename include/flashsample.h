@@ -519,8 +519,9 @@ FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_
  *                fs_token_logprobs_backward holds beside dz; V x D in fp32 for each
  *                of the parts that many rows on a small head are taken in; without
  *                gradients a copy of h alone; and 12 bytes per row and
- *                16 to 128 vocabulary entries (the more rows, the more entries);
- *                contents on entry ignored
+ *                16 to 128 vocabulary entries (the more rows, the more entries;
+ *                without gradients up to 16 KiB for each of 32 rows); contents on
+ *                entry ignored
  * Logits of -inf have probability 0; NaN or +inf among a row's give NaN.  B == 0
  * sets the stats and grad_W to 0. */
 FS_API size_t fs_cross_entropy_workspace_bytes(int32_t B, int32_t D, int32_t V, int32_t grads);

@@ -213,16 +213,17 @@ void xent_logits_kernel(XentArgs x) {
 // ---------------------------------------------------------------------------
 constexpr int kCloseThreads = 1024;
 
-template <int COLS>
+// ROWS: the partials are those of all rows in their own order (no gradient).
+template <int COLS, bool ROWS>
 __global__ __launch_bounds__(kCloseThreads) void xent_close_kernel(XentArgs x) {
   constexpr int kSplit = kCloseThreads / COLS, kUnroll = 8;
   __shared__ float2 red[kSplit][COLS];
   __shared__ double red_z[kSplit][COLS];
   const GradArgs& a = x.g;
-  const int n = *a.count;
+  const int n = ROWS ? a.B : *a.count, ld = ROWS ? a.B : a.Bp;
   const int c = threadIdx.x % COLS, y = threadIdx.x / COLS;
   const int64_t p = static_cast<int64_t>(blockIdx.x) * COLS + c;
-  if (y == 0 && p < a.B && a.slot[p] < 0) x.losses[p] = 0.0f;  // (p is a row here)
+  if (!ROWS && y == 0 && p < a.B && a.slot[p] < 0) x.losses[p] = 0.0f;  // (p is a row here)
   if (static_cast<int64_t>(blockIdx.x) * COLS >= n) return;     // (block-uniform)
   const int64_t pc = p < n ? p : n - 1;
   float m = LseAcc::kMasked, s = 0.0f;
@@ -232,13 +233,13 @@ __global__ __launch_bounds__(kCloseThreads) void xent_close_kernel(XentArgs x) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int t = t0 + u * kSplit;
-      q[u] = t < x.S ? x.part[static_cast<size_t>(t) * a.Bp + pc] : float2{LseAcc::kMasked, 0.0f};
+      q[u] = t < x.S ? x.part[static_cast<size_t>(t) * ld + pc] : float2{LseAcc::kMasked, 0.0f};
     }
     if (x.zsum != nullptr) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int t = t0 + u * kSplit;
-        zs += t < x.S ? x.zsum[static_cast<size_t>(t) * a.Bp + pc] : 0.0f;
+        zs += t < x.S ? x.zsum[static_cast<size_t>(t) * ld + pc] : 0.0f;
       }
     }
 #pragma unroll
@@ -258,10 +259,15 @@ __global__ __launch_bounds__(kCloseThreads) void xent_close_kernel(XentArgs x) {
     __syncthreads();
   }
   if (y != 0 || p >= n) return;
+  if (ROWS && !has_token(a.ids[p])) {
+    x.losses[p] = 0.0f;
+    x.rows[p] = float4{0.0f, 0.0f, 0.0f, 0.0f};
+    return;
+  }
   const float2 q = red[0][c];
   // log-sum-exp of the rows other than the target (-inf where there are none)
   const float rest = q.y == 0.0f ? -INFINITY : q.x + logf(q.y);
-  const bool here = a.loc[p] >= 0;
+  const bool here = (ROWS ? target_row(a.ids[p], 0, a.V) : a.loc[p]) >= 0;
   float nll = INFINITY, lse = rest;  // a target past V has probability 0
   if (here) {
     const float zt = x.zt[p], d = rest - zt;
@@ -269,7 +275,7 @@ __global__ __launch_bounds__(kCloseThreads) void xent_close_kernel(XentArgs x) {
     nll = d != d ? d : soft;  // (fmaxf alone would drop a NaN)
     lse = d != d ? d : zt == -INFINITY ? rest : zt + soft;
   }
-  const float sm = x.smoothing, up = upstream(x, n);
+  const float sm = x.smoothing;
   float loss = nll, own = 0.0f;
   const float lift = x.z_loss > 0.0f ? 1.0f + 2.0f * x.z_loss * lse : 1.0f;
   if (sm > 0.0f)  // (at 1 the target does not count, not even one of probability 0)
@@ -281,39 +287,44 @@ __global__ __launch_bounds__(kCloseThreads) void xent_close_kernel(XentArgs x) {
     if (x.z_loss > 0.0f) own += 2.0f * x.z_loss * lse * expf(-nll);
     if (sm > 0.0f) own += sm * (1.0f - 1.0f / static_cast<float>(a.V));
   }
-  x.losses[a.row[p]] = loss;
-  x.rows[p] = float4{loss, nll, lse * lse, 0.0f};
+  x.losses[ROWS ? p : a.row[p]] = loss;
+  x.rows[p] = float4{loss, nll, lse * lse, 1.0f};
+  if (ROWS) return;
+  const float up = upstream(x, n);
   a.term[p] = RowTerm{kLog2e, lse * kLog2e, up * lift, up * own};
 }
 
 // The loss and the two means over the rows with a target, in a fixed order by
 // one block.
-template <int THREADS>
+template <int THREADS, bool ROWS>
 __device__ void sum_rows(const XentArgs& x) {
-  __shared__ double red[3][THREADS];
-  const int n = *x.g.count, t = threadIdx.x;
-  double v[3] = {0.0, 0.0, 0.0};
+  __shared__ double red[4][THREADS];
+  const int places = ROWS ? x.g.B : *x.g.count, t = threadIdx.x;
+  double v[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll 4
-  for (int64_t p = t; p < n; p += THREADS) {
+  for (int64_t p = t; p < places; p += THREADS) {
     const float4 r = x.rows[p];
     v[0] += r.x;
     v[1] += r.y;
     v[2] += r.z;
+    v[3] += r.w;
   }
 #pragma unroll
-  for (int i = 0; i < 3; ++i) red[i][t] = v[i];
+  for (int i = 0; i < 4; ++i) red[i][t] = v[i];
   __syncthreads();
 #pragma unroll
   for (int k = THREADS / 2; k >= 1; k >>= 1) {
     if (t < k)
 #pragma unroll
-      for (int i = 0; i < 3; ++i) red[i][t] += red[i][t + k];
+      for (int i = 0; i < 4; ++i) red[i][t] += red[i][t + k];
     __syncthreads();
   }
-  if (t < 3) x.stats[t] = static_cast<float>(red[t][0] / (t == 0 && !x.mean ? 1.0 : n > 0 ? n : 1));
+  if (t < 3)
+    x.stats[t] = static_cast<float>(red[t][0] / (t == 0 && !x.mean ? 1.0 : fmax(red[3][0], 1.0)));
 }
 
-__global__ __launch_bounds__(1024) void xent_stats_kernel(XentArgs x) { sum_rows<1024>(x); }
+template <bool ROWS>
+__global__ __launch_bounds__(1024) void xent_stats_kernel(XentArgs x) { sum_rows<1024, ROWS>(x); }
 
 // Kept exponentials of one slice into dz, in place: 16 places by 1024 vocabulary
 // rows per block (of 64 places 513 rows on a shard filled half the CUs).  Each
@@ -328,7 +339,7 @@ __global__ __launch_bounds__(256) void xent_scale_kernel(XentArgs x) {
   __shared__ float s_fac[kScaleCols / 16][kScaleRows];
   const GradArgs& a = x.g;
   if (a.first_slice && blockIdx.x == gridDim.x - 1) {
-    if (blockIdx.y == 0) sum_rows<256>(x);
+    if (blockIdx.y == 0) sum_rows<256, false>(x);
     return;
   }
   const int n = *a.count;
@@ -411,12 +422,21 @@ bool keeps(int32_t B, int32_t D, int32_t V) {
              kKeptBytes;
 }
 
+// The loss alone of up to 128 rows, without smoothing: the partials of fs_token_logprobs'
+// kernels, one pair per block, of all rows in their own order (one row on 128256 x 4096
+// 175 us, 200 by this file's tiles; on 57749 x 3896 84 and 117; 128 rows 116 and 127).
+// Beyond that, rows without a target are worth dropping first (160 rows on 128256 x
+// 4096, 60% without: 261 and 208; 256 rows that all have one 269 and 283).
+bool scores(int32_t B, int32_t D, int32_t V) { return B <= 128 && score_grid_fits(B, D, V); }
+
 struct XentPlan {
   bool keep;
   GradPlan g;
   LogitsTile tile;
   int32_t S, sub;
   size_t part, zsum, zt, rows, total;
+  // of scored rows: rows [B], then the partials
+  static size_t rows_at(int32_t B) { return round_up(sizeof(float4) * B, 256); }
   XentPlan(int32_t B, int32_t D, int32_t V, bool grads)
       : keep(keeps(B, D, V)), g(B, D, V, keep, true) {
     tile = logits_tile(B, g.slice < V ? g.slice : V, true);
@@ -435,6 +455,7 @@ struct XentPlan {
     zt = take(sizeof(float) * g.Bp);
     rows = take(sizeof(float4) * g.Bp);
     total = at;
+    if (!grads && scores(B, D, V)) total = std::max(total, rows_at(B) + ScoreLayout(B, D, V).total);
   }
 };
 
@@ -488,12 +509,12 @@ hipError_t run_xent(XentArgs& x, const XentPlan& p, hipStream_t s) {
       e = grads && p.keep ? launch_logits<kKeep>(x, p.tile, s) : launch_logits<kStats>(x, p.tile, s);
       if (e != hipSuccess) return e;
     }
-    if (a.B >= 2048) xent_close_kernel<64><<<(a.B + 63) / 64, kCloseThreads, 0, s>>>(x);
-    else xent_close_kernel<8><<<(a.B + 7) / 8, kCloseThreads, 0, s>>>(x);
+    if (a.B >= 2048) xent_close_kernel<64, false><<<(a.B + 63) / 64, kCloseThreads, 0, s>>>(x);
+    else xent_close_kernel<8, false><<<(a.B + 7) / 8, kCloseThreads, 0, s>>>(x);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (!grads || !p.keep || a.B == 0) {
-    xent_stats_kernel<<<1, 1024, 0, s>>>(x);
+    xent_stats_kernel<false><<<1, 1024, 0, s>>>(x);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (!grads) return hipSuccess;
@@ -504,6 +525,30 @@ hipError_t run_xent(XentArgs& x, const XentPlan& p, hipStream_t s) {
     if ((e = launch_grad_products(a, s)) != hipSuccess) return e;
   }
   return launch_grad_finish(a, s);
+}
+
+hipError_t run_scored(XentArgs& x, char* ws, hipStream_t s) {
+  GradArgs& a = x.g;
+  const ScoreLayout lay(a.B, a.D, a.V);
+  ScoreArgs c;
+  c.w = Operand{a.W, a.D, a.V, a.D};
+  c.h = Operand{a.h, a.D, a.B, a.D};
+  c.B = a.B;
+  c.D = a.D;
+  c.V = a.V;
+  c.vocab_offset = c.shift = 0;
+  c.temperature = nullptr;
+  c.ids = a.ids;
+  hipError_t e = launch_score_logits(c, ws + XentPlan::rows_at(a.B), lay, false, s);
+  if (e != hipSuccess) return e;
+  x.rows = reinterpret_cast<float4*>(ws);
+  x.part = c.part;
+  x.zt = c.target;
+  x.S = c.S;
+  xent_close_kernel<8, true><<<(a.B + 7) / 8, kCloseThreads, 0, s>>>(x);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  xent_stats_kernel<true><<<1, 1024, 0, s>>>(x);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -577,7 +622,9 @@ FS_API fs_status fs_cross_entropy(const void* h, const void* W, int32_t B, int32
   x.mean = mean != 0;
   x.losses = out_losses;
   x.stats = out_stats;
-  const hipError_t e = run_xent(x, p, static_cast<hipStream_t>(stream));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool scored = !a.dh && !a.dW && B > 0 && !x.zsum && scores(B, D, V);
+  const hipError_t e = scored ? run_scored(x, ws, s) : run_xent(x, p, s);
   return e == hipSuccess ? FS_OK : hip_fail(e, "cross-entropy launch");
 }
 

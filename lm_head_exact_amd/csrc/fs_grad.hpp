@@ -53,6 +53,10 @@ struct GradArgs {
 constexpr int kTargetTile = 256;
 constexpr int kTargetThreads = 1024;
 
+// A row counts where it has a token; a token of another shard still gives
+// every row of this one a gradient.
+__device__ __forceinline__ bool has_token(int32_t id) { return id >= 0; }
+
 __device__ __forceinline__ uint64_t pack_bf16(float x0, float x1, float x2, float x3) {
   typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
   const bf16x4 v = {static_cast<__bf16>(x0), static_cast<__bf16>(x1), static_cast<__bf16>(x2),

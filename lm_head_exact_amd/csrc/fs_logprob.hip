@@ -352,17 +352,6 @@ int32_t tile_count(int32_t B, int32_t V) {
 
 bool pads(int32_t B, int32_t D) { return !streams(B, D) && D % 64 != 0; }
 
-struct ScoreLayout {
-  size_t part, target, pad, total;
-  ScoreLayout(int32_t B, int32_t D, int32_t V) {
-    const size_t S = streams(B, D) ? kMaxStreamBlocks : tile_count(B, V);
-    target = round_up(sizeof(float2) * S * B, 256);
-    part = 0;
-    pad = target + round_up(sizeof(float) * B, 256);
-    total = pad + (pads(B, D) ? round_up(2 * static_cast<size_t>(B) * round_up(D, 64), 256) : 0);
-  }
-};
-
 fs_status check_score_shape(const char* who, int32_t B, int32_t D, int32_t V,
                             int32_t vocab_offset) {
   if (B < 0) return fail(FS_ERR_INVALID_ARG, "%s: B must be >= 0 (got %d)", who, B);
@@ -375,12 +364,8 @@ fs_status check_score_shape(const char* who, int32_t B, int32_t D, int32_t V,
   if (B > kMaxScoreB || D > kMaxScoreD || V > kMaxVocab)
     return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, D=%d, V=%d exceed the %d rows, %d elements or %d "
                 "entries a call can take", who, B, D, V, kMaxScoreB, kMaxScoreD, kMaxVocab);
-  if (!streams(B, D)) {  // (streaming grids are bounded by the device)
-    const LogitsTile t = logits_tile(B, V);
-    const int64_t S = (static_cast<int64_t>(V) + 3 + rows_of(t) - 1) / rows_of(t);
-    if (!grid_fits(grid_tiles(B, S, tokens_of(t)), threads_of(t)))
-      return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, V=%d exceed the launch grid", who, B, V);
-  }
+  if (!score_grid_fits(B, D, V))
+    return fail(FS_ERR_UNSUPPORTED, "%s: B=%d, V=%d exceed the launch grid", who, B, V);
   return FS_OK;
 }
 
@@ -408,7 +393,6 @@ fs_status run_score(const char* who, const void* h, const void* W, int32_t B, in
                 workspace_bytes, lay.total);
   if (start_launches()) return injected_failure(who);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  char* ws = static_cast<char*>(workspace);
   ScoreArgs a;
   a.B = B;
   a.D = D;
@@ -421,27 +405,45 @@ fs_status run_score(const char* who, const void* h, const void* W, int32_t B, in
   a.h = Operand{static_cast<const __bf16*>(h), D, B, D};
   a.temperature = temperature;
   a.ids = ids;
-  a.part = reinterpret_cast<float2*>(ws + lay.part);
-  a.target = reinterpret_cast<float*>(ws + lay.target);
-  hipError_t e;
-  if (streams(B, D)) {
-    e = packed ? launch_score_stream<true>(a, s) : launch_score_stream<false>(a, s);
-  } else {
-    if (pads(B, D)) {
-      const int32_t Dp = static_cast<int32_t>(round_up(D, 64));
-      __bf16* hp = reinterpret_cast<__bf16*>(ws + lay.pad);
-      pad_rows_kernel<<<2048, 256, 0, s>>>(a.h.p, B, D, Dp, hp);
-      if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "padding launch");
-      a.h = Operand{hp, Dp, B, Dp};
-    }
-    e = packed ? launch_tiles<kFrag>(a, s) : launch_tiles<kKC>(a, s);
-  }
+  hipError_t e = launch_score_logits(a, static_cast<char*>(workspace), lay, packed, s);
   if (e != hipSuccess) return hip_fail(e, "log-probability launch");
   e = launch_score_close(a, logprob, lse, s);
   return e == hipSuccess ? FS_OK : hip_fail(e, "log-probability merge launch");
 }
 
 }  // namespace
+
+ScoreLayout::ScoreLayout(int32_t B, int32_t D, int32_t V) {
+  const size_t S = streams(B, D) ? kMaxStreamBlocks : tile_count(B, V);
+  target = round_up(sizeof(float2) * S * B, 256);
+  part = 0;
+  pad = target + round_up(sizeof(float) * B, 256);
+  total = pad + (pads(B, D) ? round_up(2 * static_cast<size_t>(B) * round_up(D, 64), 256) : 0);
+}
+
+bool score_grid_fits(int32_t B, int32_t D, int32_t V) {
+  if (streams(B, D)) return true;  // (streaming grids are bounded by the device)
+  const LogitsTile t = logits_tile(B, V);
+  const int64_t S = (static_cast<int64_t>(V) + 3 + rows_of(t) - 1) / rows_of(t);
+  return grid_fits(grid_tiles(B, S, tokens_of(t)), threads_of(t));
+}
+
+hipError_t launch_score_logits(ScoreArgs& a, char* ws, const ScoreLayout& lay, bool packed,
+                               hipStream_t s) {
+  a.part = reinterpret_cast<float2*>(ws + lay.part);
+  a.target = reinterpret_cast<float*>(ws + lay.target);
+  if (streams(a.B, a.D))
+    return packed ? launch_score_stream<true>(a, s) : launch_score_stream<false>(a, s);
+  if (pads(a.B, a.D)) {
+    const int32_t Dp = static_cast<int32_t>(round_up(a.D, 64));
+    __bf16* hp = reinterpret_cast<__bf16*>(ws + lay.pad);
+    pad_rows_kernel<<<2048, 256, 0, s>>>(a.h.p, a.B, a.D, Dp, hp);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.h = Operand{hp, Dp, a.B, Dp};
+  }
+  return packed ? launch_tiles<kFrag>(a, s) : launch_tiles<kKC>(a, s);
+}
 
 hipError_t launch_score_close(const ScoreArgs& a, float* logprob, float* lse, hipStream_t stream) {
   // wide rows of the partials for many tokens (8192 tokens on 32000 rows of 256:

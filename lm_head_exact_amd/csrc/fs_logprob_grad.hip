@@ -36,10 +36,6 @@
 namespace fs {
 namespace {
 
-// A row counts where it has a token; a token of another shard still gives
-// every row of this one a gradient.
-__device__ __forceinline__ bool has_token(int32_t id) { return id >= 0; }
-
 constexpr int kScanThreads = 1024;
 
 // Estimated time of dh over `parts` parts of a slice's vocabulary rows, in k

@@ -115,6 +115,15 @@ __device__ __forceinline__ void fold_logits(const Z& z, int row0, int32_t V, int
   pair_merge(m, s, mz == LseAcc::kMasked ? mz : mz * inv_t, sum);
 }
 
+// Workspace of the partials and of padded hidden states.
+struct ScoreLayout {
+  size_t part, target, pad, total;
+  ScoreLayout(int32_t B, int32_t D, int32_t V);
+};
+bool score_grid_fits(int32_t B, int32_t D, int32_t V);
+// The partials: sets a's part, target and S (and h, where it is padded).
+hipError_t launch_score_logits(ScoreArgs& a, char* workspace, const ScoreLayout& lay, bool packed,
+                               hipStream_t stream);
 // The partials of each token into its log-probability and log-sum-exp.
 hipError_t launch_score_close(const ScoreArgs& a, float* logprob, float* lse, hipStream_t stream);
 

@@ -377,3 +377,29 @@ def test_agrees_with_the_log_probabilities():
     assert torch.allclose(losses, -lp, rtol=2.0 ** -20, atol=2.0 ** -22)
     for a, b in ((gh, bh), (gw, bw)):   # dz rounded apart in each, then the results
         assert (a.double() - b.double()).norm() <= 2.0 ** -7 * b.double().norm()
+
+
+@pytest.mark.parametrize("B,D,V", [(1, 8, 1), (1, 8192, 40), (16, 4104, 300), (17, 1000, 2049), (32, 5120, 500),
+                                   (33, 72, 700), (64, 128, 3001), (65, 64, 16), (128, 264, 5000), (129, 64, 999),
+                                   (200, 136, 16032), (256, 192, 20000), (257, 64, 20000)])
+@pytest.mark.parametrize("ignore", [0.0, 0.5])
+def test_loss_alone(B, D, V, ignore):
+    """Without gradients and smoothing few rows are scored where they lie: rows without a
+    target hold NaN, a target is past the vocabulary, the workspace is just large enough."""
+    h, W, t = make(B, D, V, seed=23, ignore=ignore)
+    h[t < 0] = math.nan
+    if ignore and B > 2:
+        t[B // 2] = V
+        h[B // 2] = 0.5
+    hz = torch.where((t >= 0)[:, None], h, torch.zeros_like(h))
+    for z_loss, reduction in ((0.0, "mean"), (1e-2, "sum")):
+        kw = dict(z_loss=z_loss, reduction=reduction)
+        n = fs.cross_entropy_workspace_bytes(B, D, V, False)
+        ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+        got = run(h, W, t, need_h=False, need_W=False, workspace=ws, **kw)
+        check(hz, W, t, got, head_ref.cross_entropy(hz, W, t, **kw), **kw)
+        again = run(h, W, t, need_h=False, need_W=False, **kw)
+        assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    none = torch.full_like(t, -100)
+    stats, losses, _, _ = run(torch.full_like(h, math.nan), W, none, need_h=False, need_W=False)
+    assert (stats == 0).all() and (losses == 0).all()
