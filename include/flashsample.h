@@ -351,8 +351,9 @@ FS_API fs_status fs_sample_unfused(const void* h, const void* W, int32_t B, int3
  * h is given in bf16 and quantised by the call.  Up to 32 rows (D up to 5120; 16
  * rows up to 8192) the products are exact and summed in fp32; more rows take the
  * 8-bit matrix instructions, which round a product to 13 bits below the largest
- * of eight neighbouring ones: 1.5e-5 of the logits' spread (but for the tokens' own
- * logits in fs_token_logprobs_fp8, which are exact products there too).
+ * of eight neighbouring ones: 1.5e-5 of the logits' spread.  fs_token_logprobs_fp8
+ * makes the tokens' own logits by exact products there too, and all of them where
+ * V is at most 8192.
  *   D            a multiple of 64 up to 16384; V up to 2^31 - 513; B up to 2^22
  *                (FS_ERR_UNSUPPORTED beyond, and where a launch would hold 2^32
  *                threads)

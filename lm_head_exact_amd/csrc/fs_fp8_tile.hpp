@@ -22,6 +22,9 @@
 // first bit, two further none; those of other groups are exact).  On normal data that
 // is 1.5e-5 of a logit's spread, without a bias: a thousandth of what the values'
 // own four bits leave.
+// Exact products (EXACT) widen the same fragments to bf16, which holds four bits times a
+// power of two: four products of 16 k for one of 64, at half its rate.  Scores on few
+// entries take them (fs_fp8_tile_scores.hip).
 #pragma once
 
 #include "fs_fp8.hpp"
@@ -68,6 +71,8 @@ struct Fp8Tile : Tile<kFrag, kKC, WA_, WB_, 2 * MR_, 2 * NT_, S_, 64, false, tru
   // wave_a() + 32 m + 8 q + 4 (lane / 32) + r in element 4 q + r.  LDS is free for
   // reuse when it returns.  The loop is the training products': one barrier per slot,
   // before its last step's products, behind which the slot S ahead is staged.
+  // EXACT: by bf16 products of the widened bytes.
+  template <bool EXACT>
   __device__ __forceinline__ static void run(const Fp8Args& a, int a0, int b0,
                                              f32x16 (&acc)[MR][NT], unsigned char* smem) {
     static_for<MR>([&](auto m) FS_INLINE {
@@ -122,6 +127,23 @@ struct Fp8Tile : Tile<kFrag, kKC, WA_, WB_, 2 * MR_, 2 * NT_, S_, 64, false, tru
     };
     auto mma = [&](auto set) FS_INLINE {
       constexpr int x = decltype(set)::value;
+      if constexpr (EXACT) {
+        // 16 k at a time: eight of each half's 32, in both operands alike
+        static_for<4>([&](auto i) FS_INLINE {
+          constexpr int j = 2 * decltype(i)::value;
+          bf16x8 h[NT];
+          static_for<NT>([&](auto n) FS_INLINE {
+            h[n] = widen(fh[x][n][j], fh[x][n][j + 1], scale_up(sh[0][n]));
+          });
+          static_for<MR>([&](auto m) FS_INLINE {
+            const bf16x8 w = widen(fw[x][m][j], fw[x][m][j + 1], scale_up(sw[0]));
+            static_for<NT>([&](auto n) FS_INLINE {
+              acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, h[n], acc[m][n], 0, 0, 0);
+            });
+          });
+        });
+        return;
+      }
       static_for<MR>([&](auto m) FS_INLINE {
         static_for<NT>([&](auto n) FS_INLINE {
           acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
@@ -147,7 +169,7 @@ struct Fp8Tile : Tile<kFrag, kKC, WA_, WB_, 2 * MR_, 2 * NT_, S_, 64, false, tru
       read(I0{}, I0{}, from);
       read(I1{}, I1{}, from);
       mma(I0{});
-      interleave<0>();
+      if constexpr (!EXACT) interleave<0>();
       __builtin_amdgcn_sched_barrier(0);
     }(smem, smem + kStage);
     int slot = 0;
@@ -163,13 +185,13 @@ struct Fp8Tile : Tile<kFrag, kKC, WA_, WB_, 2 * MR_, 2 * NT_, S_, 64, false, tru
         read(I0{}, I0{}, from);
         stage(ahead, to);
         mma(I1{});
-        interleave<IA + IB>();
+        if constexpr (!EXACT) interleave<IA + IB>();
         __builtin_amdgcn_sched_barrier(0);
         sw[0] = sw[1];
         static_for<NT>([&](auto n) FS_INLINE { sh[0][n] = sh[1][n]; });
         read(I1{}, I1{}, from);
         mma(I0{});
-        interleave<0>();
+        if constexpr (!EXACT) interleave<0>();
         __builtin_amdgcn_sched_barrier(0);
       }(smem + next * kStage, smem + slot * kStage);
       slot = next;
@@ -194,7 +216,7 @@ struct Fp8Tile : Tile<kFrag, kKC, WA_, WB_, 2 * MR_, 2 * NT_, S_, 64, false, tru
   }
 };
 
-template <class T, int OUT>
+template <class T, int OUT, bool EXACT>
 __global__ __launch_bounds__(T::kThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void fp8_tile_kernel(Fp8Args a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char dyn_smem[];
@@ -202,7 +224,7 @@ void fp8_tile_kernel(Fp8Args a) {
   if (!xcd_tile<4>(blockIdx.x, a.S, (a.B + T::TB - 1) / T::TB, tile, btile)) return;
   const int a0 = tile * T::TA, b0 = btile * T::TB;
   f32x16 acc[T::MR][T::NT];
-  T::run(a, a0, b0, acc, dyn_smem);
+  T::template run<EXACT>(a, a0, b0, acc, dyn_smem);
 
   const int lane = threadIdx.x & (kWave - 1), li = lane & 31, kb = lane >> 5;
   const int row0 = a0 + T::wave_a(), col0 = b0 + T::wave_b();
@@ -350,29 +372,29 @@ using Fp8Tall256 = Fp8Tile<2, 4, 4, 2, 2>;
 using Fp8Short64 = Fp8Tile<2, 2, 1, 1, 3>;
 using Fp8Short256 = Fp8Tile<2, 2, 2, 2, 2>;
 
-template <class T, int SHAPE, int OUT>
+template <class T, int SHAPE, int OUT, bool EXACT>
 hipError_t launch_fp8_tile(Fp8Args& a, hipStream_t stream) {
   constexpr Fp8TileShape c = kFp8TileShapes[SHAPE];
   static_assert(T::TA == c.rows && T::TB == c.tokens && T::S == c.slots, "the shape of the rule");
   static_assert(T::kThreads == (T::TA == kTallRows ? 512 : 256), "threads_of");
   a.S = static_cast<int32_t>((static_cast<int64_t>(a.V) + T::TA - 1) / T::TA);
   static SmemRaised raised;
-  const hipError_t e = raise_smem(&fp8_tile_kernel<T, OUT>, kFp8Lds, raised);
+  const hipError_t e = raise_smem(&fp8_tile_kernel<T, OUT, EXACT>, kFp8Lds, raised);
   if (e != hipSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(a.S) * ((a.B + T::TB - 1) / T::TB);
-  fp8_tile_kernel<T, OUT><<<static_cast<unsigned>((tiles + 7) / 8 * 8), T::kThreads,
+  fp8_tile_kernel<T, OUT, EXACT><<<static_cast<unsigned>((tiles + 7) / 8 * 8), T::kThreads,
                             fp8_lds(c, a.D), stream>>>(a);
   return hipGetLastError();
 }
 
-template <int OUT>
+template <int OUT, bool EXACT = false>
 hipError_t launch_fp8_tiles(Fp8Args& a, hipStream_t stream) {
   switch (fp8_tile(a.B, a.D, a.V)) {
-    case LogitsTile::kTall64: return launch_fp8_tile<Fp8Tall64, 0, OUT>(a, stream);
-    case LogitsTile::kTall128: return launch_fp8_tile<Fp8Tall128, 1, OUT>(a, stream);
-    case LogitsTile::kTall256: return launch_fp8_tile<Fp8Tall256, 2, OUT>(a, stream);
-    case LogitsTile::kShort64: return launch_fp8_tile<Fp8Short64, 3, OUT>(a, stream);
-    default: return launch_fp8_tile<Fp8Short256, 4, OUT>(a, stream);
+    case LogitsTile::kTall64: return launch_fp8_tile<Fp8Tall64, 0, OUT, EXACT>(a, stream);
+    case LogitsTile::kTall128: return launch_fp8_tile<Fp8Tall128, 1, OUT, EXACT>(a, stream);
+    case LogitsTile::kTall256: return launch_fp8_tile<Fp8Tall256, 2, OUT, EXACT>(a, stream);
+    case LogitsTile::kShort64: return launch_fp8_tile<Fp8Short64, 3, OUT, EXACT>(a, stream);
+    default: return launch_fp8_tile<Fp8Short256, 4, OUT, EXACT>(a, stream);
   }
 }
 

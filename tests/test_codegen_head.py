@@ -56,7 +56,7 @@ def test_8_bit_tile_waits(kernels, monkeypatch):
         if "fp8_tile_kernel" in n:
             first = next(i for i, x in enumerate(lines) if re.match(r"\s*buffer_load\S* .*\blds\b", x))
             some[n] = (lines[first:], scratch)
-    assert len(some) == 20, sorted(some)
+    assert len(some) == 25, sorted(some)  # (scores by exact products too)
     monkeypatch.setattr(tiles, "_shape", shape)
     tiles.test_waits_cover_what_the_barriers_publish(some)
 

@@ -32,6 +32,9 @@ def rule(tmp_path_factory):
 
 def test_gpu_cases_take_every_tile(rule):
     assert [t[:2] for t in rule(gpu_tests.TILES)] == TILES
+    for few in (True, False):
+        assert {t[:2] for s, t in zip(gpu_tests.SCORE_TILES, rule(gpu_tests.SCORE_TILES))
+                if (s[2] <= 8192) == few} == set(TILES)
 
 
 def test_scales_fit_beside_the_ring(rule):

@@ -50,10 +50,11 @@ class Head:
         assert torch.equal(u8(s), self.wq[1]) and torch.equal(u8(q), fp8_ref.pack(self.wq[0]))
         self.args = (self.h.cuda(), q, s, V)
 
-    def logit_error(self, T=None):
-        """Largest error of a scaled logit, and of one of exact products."""
+    def logit_error(self, T=None, scores=False):
+        """Largest error of a scaled logit, and of one of exact products (tokens are
+        scored by those on up to 8192 entries)."""
         e = ref.logit_tolerance(self.hd, self.Wd, T)
-        if self.streams:
+        if self.streams or (scores and self.V <= 8192):
             return e, e
         m = fp8_ref.matrix_rounding(self.hq, self.wq) * ref.inv_temperature(T, self.h.shape[0])[:, None]
         return e + float(m.max()), e
@@ -128,7 +129,7 @@ def test_logits(B, D, V):
 def check_scores(c, T, ids, off, got):
     lp, lse = (x.cpu().double() for x in got)
     want_lp, want_lse = ref.logprobs(c.hd, c.Wd, T, ids, off)
-    e, exact = c.logit_error(T)
+    e, exact = c.logit_error(T, scores=True)
     assert ((lse - want_lse).abs() <= e + 2.0 ** -22 * (1 + want_lse.abs())).all()
     fin = torch.isfinite(want_lp)
     assert torch.equal(torch.isinf(lp) & (lp < 0), ~fin)
@@ -169,6 +170,19 @@ def test_samples(B, D, V, off):
     ids, val = fs.sample_fp8(*c.args, T.cuda(), 2 ** 40 + 7, 2 ** 33 + 5, vocab_offset=off)
     parity.check_rows(wl.bf16_bits(c.hd), wl.bf16_bits(c.Wd), T.numpy(), 2 ** 40 + 7, 2 ** 33 + 5, off,
                       ids.cpu().numpy(), val.cpu().numpy())
+
+# and for tokens' scores, by exact products (up to 8192 entries) and by the 8-bit ones
+SCORE_TILES = [(3000, 128, 700), (513, 64, 8192), (4000, 192, 2161), (3833, 128, 2161), (40, 128, 700),
+               (200, 128, 8193), (513, 64, 8193), (1000, 64, 8193), (40, 192, 8193), (648, 192, 10821)]
+
+
+@pytest.mark.parametrize("B,D,V", SCORE_TILES)
+def test_scores_by_every_tile(B, D, V):
+    """At temperatures down to 0.1, where few entries carry the log-sum-exp."""
+    c = Head(B, D, V, seed=12, wide=False)
+    T, ids = targets(B, V, 0)
+    T[1::3] = 0.1
+    check_scores(c, T, ids, 0, fs.token_logprobs_fp8(*c.args, T.cuda(), ids.cuda()))
 
 
 @pytest.mark.parametrize("B,D,V", TILES)
