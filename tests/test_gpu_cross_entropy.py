@@ -403,3 +403,24 @@ def test_loss_alone(B, D, V, ignore):
     none = torch.full_like(t, -100)
     stats, losses, _, _ = run(torch.full_like(h, math.nan), W, none, need_h=False, need_W=False)
     assert (stats == 0).all() and (losses == 0).all()
+
+
+@pytest.mark.parametrize("B,D,V", [(20, 512, 3000), (100, 200, 5000)])
+def test_loss_alone_in_a_graph(B, D, V):
+    """Replayed on new inputs, with eager work on another workspace between."""
+    h, W, t = (x.cuda() for x in make(B, D, V, seed=24))
+    ws = torch.empty(fs.cross_entropy_workspace_bytes(B, D, V, False), dtype=torch.uint8, device="cuda")
+    out = (torch.empty(3, device="cuda"), torch.empty(B, device="cuda"), None, None)
+    kw = dict(z_loss=1e-3, need_h=False, need_W=False)
+    fs.cross_entropy(h, W, t, out=out, workspace=ws, **kw)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fs.cross_entropy(h, W, t, out=out, workspace=ws, **kw)
+    for i in range(4):
+        h2, W2, t2 = make(B, D, V, seed=25 + i, ignore=0.3 * i)
+        h.copy_(h2), W.copy_(W2), t.copy_(t2)
+        want = fs.cross_entropy(h, W, t, **kw)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]), i
