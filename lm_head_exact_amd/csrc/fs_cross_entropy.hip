@@ -269,12 +269,7 @@ __global__ __launch_bounds__(kCloseThreads) void xent_close_kernel(XentArgs x) {
   const float rest = q.y == 0.0f ? -INFINITY : q.x + logf(q.y);
   const bool here = (ROWS ? target_row(a.ids[p], 0, a.V) : a.loc[p]) >= 0;
   float nll = INFINITY, lse = rest;  // a target past V has probability 0
-  if (here) {
-    const float zt = x.zt[p], d = rest - zt;
-    const float soft = fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d)));
-    nll = d != d ? d : soft;  // (fmaxf alone would drop a NaN)
-    lse = d != d ? d : zt == -INFINITY ? rest : zt + soft;
-  }
+  if (here) close_target(rest, x.zt[p], nll, lse);
   const float sm = x.smoothing;
   float loss = nll, own = 0.0f;
   const float lift = x.z_loss > 0.0f ? 1.0f + 2.0f * x.z_loss * lse : 1.0f;

@@ -236,12 +236,9 @@ __global__ __launch_bounds__(kCloseThreads) void score_close_kernel(ScoreArgs a,
   // log-sum-exp of the rows other than the target (-inf where there are none)
   const float rest = p.y == 0.0f ? -INFINITY : p.x + logf(p.y);
   if (target_row(id, a.vocab_offset, a.V) >= 0) {
-    const float zt = a.target[b], x = rest - zt;
-    const float soft = fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
-    // NaN logits give NaN (fmaxf alone would drop it)
-    logprob[b] = x != x ? x : -soft;
-    // (a target at -inf: the others' alone)
-    lse[b] = x != x ? x : zt == -INFINITY ? rest : zt + soft;
+    float nll;
+    close_target(rest, a.target[b], nll, lse[b]);
+    logprob[b] = -nll;
   } else {
     logprob[b] = id < 0 ? 0.0f : -INFINITY;
     lse[b] = rest;

@@ -14,6 +14,7 @@
 #pragma once
 
 #include <atomic>
+#include <cmath>
 
 #include "fs_tile.hpp"
 
@@ -52,6 +53,18 @@ __device__ __forceinline__ void pair_merge(float& m, float& s, float om, float o
 __device__ __forceinline__ void pair_xor(float& m, float& s, int mask) {
   const float om = __shfl_xor(m, mask, kWave), os = __shfl_xor(s, mask, kWave);
   pair_merge(m, s, om, os);
+}
+
+// -log p of a target whose (scaled) logit is zt, beside others whose log-sum-exp is rest
+// (-inf where there are none), and the log-sum-exp of all: log(1 + exp(rest - zt)), which
+// keeps its digits where the target is nearly certain.
+__device__ __forceinline__ void close_target(float rest, float zt, float& nll, float& lse) {
+  const float d = rest - zt;
+  const float soft = fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d)));
+  // (fmaxf alone would drop a NaN; exp(z - lse) of a target at +inf has no value either)
+  const bool none = d != d || zt == INFINITY;
+  nll = none ? NAN : soft;
+  lse = none ? NAN : zt == -INFINITY ? rest : zt + soft;
 }
 
 // What is taken from the exponents of a lane's logits, whose maximum is mz: 0
