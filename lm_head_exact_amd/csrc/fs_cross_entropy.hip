@@ -112,7 +112,7 @@ void xent_logits_kernel(XentArgs x) {
           static_for<4>([&](auto rc) FS_INLINE {
             constexpr int r = decltype(rc)::value;
             const int v = row0 + 16 * static_cast<int>(m) + r;
-            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(z[r], term[n].c, -term[n].lse2));
+            const float p = __builtin_amdgcn_exp2f((z[r] - term[n].lse) * kLog2e);
             d[r] = __builtin_fmaf(p, term[n].coef, uniform);
             d[r] = v == loc[n] || (!whole && v >= a.nv) ? 0.0f : d[r];
           });
@@ -122,7 +122,7 @@ void xent_logits_kernel(XentArgs x) {
     return;
   }
 
-  float mz[T::NT], off[T::NT], s[T::NT];
+  float mz[T::NT], s[T::NT];
   bool plain[T::NT];  // the same on all lanes: no row of the wave is left out of any token's sum
   const size_t at = static_cast<size_t>((a.v0 + wave_row) / x.sub) * a.Bp + b0 + T::wave_b();
   static_for<T::NT>([&](auto n) FS_INLINE {
@@ -158,7 +158,6 @@ void xent_logits_kernel(XentArgs x) {
     m = fmaxf(m, __shfl_xor(m, 16, kWave));
     m = fmaxf(m, __shfl_xor(m, 32, kWave));
     mz[n] = m;
-    off[n] = exponent_offset(m, kLog2e) - (MODE == kKeep ? 15.0f : 0.0f);
     s[n] = 0.0f;
   });
   // the exponentials of accumulator (m, n)
@@ -167,7 +166,9 @@ void xent_logits_kernel(XentArgs x) {
     const f32x4 z = acc[m][n];
     static_for<4>([&](auto rc) FS_INLINE {
       constexpr int r = decltype(rc)::value;
-      e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[r], kLog2e, -off[n]));
+      // (the difference first: it holds for logits of any size)
+      e[r] = __builtin_amdgcn_exp2f(
+          __builtin_fmaf(z[r] - mz[n], kLog2e, MODE == kKeep ? 15.0f : 0.0f));
     });
     if (!plain[n]) {
       static_for<4>([&](auto rc) FS_INLINE {
@@ -286,7 +287,7 @@ __global__ __launch_bounds__(kCloseThreads) void xent_close_kernel(XentArgs x) {
   x.rows[p] = float4{loss, nll, lse * lse, 1.0f};
   if (ROWS) return;
   const float up = upstream(x, n);
-  a.term[p] = RowTerm{kLog2e, lse * kLog2e, up * lift, up * own};
+  a.term[p] = RowTerm{1.0f, lse, up * lift, up * own};
 }
 
 // The loss and the two means over the rows with a target, in a fixed order by
@@ -366,7 +367,7 @@ __global__ __launch_bounds__(256) void xent_scale_kernel(XentArgs x) {
     for (int k = 0; k < kMost; ++k) {
       const int t = threadIdx.x / kScaleRows + k * (256 / kScaleRows);
       const float f =
-          __builtin_amdgcn_exp2f(__builtin_fmaf(m[k], kLog2e, -term.lse2)) * term.coef * 0x1p-15f;
+          __builtin_amdgcn_exp2f((m[k] - term.lse) * kLog2e) * term.coef * 0x1p-15f;
       if (t < kScaleCols / x.sub) s_fac[t][r] = r0 + r < n ? f : 0.0f;  // (behind the last place: 0)
     }
   }

@@ -17,8 +17,8 @@ namespace fs {
 
 // Per row that has a target, in order.
 struct RowTerm {
-  float c;       // log2(e) / T
-  float lse2;    // log2(e) * lse
+  float inv_t;   // 1 / T
+  float lse;     // of the scaled logits
   float coef;    // -g / T
   float target;  // g / T * (1 - p_target)
 };

@@ -125,8 +125,8 @@ __device__ void gather_row(const GradArgs& a, int b, int at, int n) {
     if (a.grad != nullptr) {
       const float inv_t = score_inv_t(a.temperature, b);
       const float g = a.grad[b] * inv_t;
-      t.c = inv_t * 1.44269504088896341f;
-      t.lse2 = a.lse[b] * 1.44269504088896341f;
+      t.inv_t = inv_t;
+      t.lse = a.lse[b];
       t.coef = -g;
       t.target = loc >= 0 ? -expm1f(a.logprob[b]) * g : 0.0f;
     }
@@ -321,7 +321,9 @@ void grad_logits_kernel(GradArgs a) {
         static_for<4>([&](auto rc) FS_INLINE {
           constexpr int r = decltype(rc)::value;
           const int v = row0 + 16 * static_cast<int>(m) + r;
-          d[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[r], term[n].c, -term[n].lse2)) * term[n].coef;
+          // (the difference first, rounded once: it holds for logits of any size)
+          const float x = __builtin_fmaf(z[r], term[n].inv_t, -term[n].lse);
+          d[r] = __builtin_amdgcn_exp2f(x * 1.44269504088896341f) * term[n].coef;
           d[r] = v == loc[n] || (!whole && v >= a.nv) ? 0.0f : d[r];
         });
         return pack_bf16(d[0], d[1], d[2], d[3]);
