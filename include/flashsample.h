@@ -523,8 +523,9 @@ FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int32_
  *                16 to 128 vocabulary entries (the more rows, the more entries;
  *                without gradients up to 16 KiB for each of 32 rows); contents on
  *                entry ignored
- * Logits of -inf have probability 0; NaN or +inf among a row's give NaN.  B == 0
- * sets the stats and grad_W to 0. */
+ * Logits of -inf have probability 0 (grad_W is 0 in their rows; grad_h, a product
+ * with W, takes 0 times its infinite entries: NaN); NaN or +inf among a row's give
+ * NaN.  B == 0 sets the stats and grad_W to 0. */
 FS_API size_t fs_cross_entropy_workspace_bytes(int32_t B, int32_t D, int32_t V, int32_t grads);
 FS_API fs_status fs_cross_entropy(const void* h, const void* W, int32_t B, int32_t D, int32_t V,
                                   const int32_t* targets, double label_smoothing, double z_loss,

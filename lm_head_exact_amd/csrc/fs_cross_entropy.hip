@@ -99,9 +99,13 @@ void xent_logits_kernel(XentArgs x) {
 
   if constexpr (MODE == kDirect) {
     const float uniform = uniform_term(x, upstream(x, n));
+    const bool full = b0 + T::TB <= n;
+    bool fill[T::NT];  // behind the last place: dz is 0 whatever the product with h = 0 gave
     RowTerm term[T::NT];
-    static_for<T::NT>([&](auto n) FS_INLINE {
-      term[n] = a.term[b0 + T::wave_b() + 16 * static_cast<int>(n) + li];
+    static_for<T::NT>([&](auto nc) FS_INLINE {
+      const int b = b0 + T::wave_b() + 16 * static_cast<int>(nc) + li;
+      term[nc] = a.term[b];
+      fill[nc] = !full && b >= n;
     });
     T::store_rows(
         dyn_smem,
@@ -114,7 +118,7 @@ void xent_logits_kernel(XentArgs x) {
             const int v = row0 + 16 * static_cast<int>(m) + r;
             const float p = __builtin_amdgcn_exp2f((z[r] - term[n].lse) * kLog2e);
             d[r] = __builtin_fmaf(p, term[n].coef, uniform);
-            d[r] = v == loc[n] || (!whole && v >= a.nv) ? 0.0f : d[r];
+            d[r] = v == loc[n] || (!whole && v >= a.nv) || fill[n] ? 0.0f : d[r];
           });
           return pack_bf16(d[0], d[1], d[2], d[3]);
         },
@@ -325,9 +329,11 @@ __global__ __launch_bounds__(1024) void xent_stats_kernel(XentArgs x) { sum_rows
 // Kept exponentials of one slice into dz, in place: 16 places by 1024 vocabulary
 // rows per block (of 64 places 513 rows on a shard filled half the CUs).  Each
 // place's factors for the block's partials are made once, in LDS; two waves then
-// take a row, 16 bytes per lane.  Bound by reading and writing dz (4096 rows of
-// 128256, three quarters with a target: 1.6 GB).  The first slice's grid has one
-// block more per column, the first of which makes the stats.
+// take a row, 16 bytes per lane.  The places that fill the last k tile of dW are set
+// to 0: theirs are of h = 0, NaN where a row of W has an infinite entry.  Bound by
+// reading and writing dz (4096 rows of 128256, three quarters with a target: 1.6 GB).
+// The first slice's grid has one block more per column, the first of which makes the
+// stats.
 constexpr int kScaleRows = 16, kScaleCols = 1024;
 
 __global__ __launch_bounds__(256) void xent_scale_kernel(XentArgs x) {
@@ -340,7 +346,7 @@ __global__ __launch_bounds__(256) void xent_scale_kernel(XentArgs x) {
   }
   const int n = *a.count;
   const int r0 = blockIdx.x * kScaleRows, c0 = blockIdx.y * kScaleCols;
-  if (r0 >= n) return;
+  if (r0 >= (n + kGradPlaces - 1) / kGradPlaces * kGradPlaces) return;
   const int lane_col = (threadIdx.x % 128) * 8, c = c0 + lane_col, half = threadIdx.x / 128;
   const bool mine = c < (a.nv + 7) / 8 * 8;
   constexpr int kEach = kScaleRows / 2;  // rows of a thread
@@ -368,7 +374,7 @@ __global__ __launch_bounds__(256) void xent_scale_kernel(XentArgs x) {
       const int t = threadIdx.x / kScaleRows + k * (256 / kScaleRows);
       const float f =
           __builtin_amdgcn_exp2f((m[k] - term.lse) * kLog2e) * term.coef * 0x1p-15f;
-      if (t < kScaleCols / x.sub) s_fac[t][r] = r0 + r < n ? f : 0.0f;  // (behind the last place: 0)
+      if (t < kScaleCols / x.sub) s_fac[t][r] = f;
     }
   }
   __syncthreads();
@@ -381,7 +387,7 @@ __global__ __launch_bounds__(256) void xent_scale_kernel(XentArgs x) {
     const float f = s_fac[fac][row];
     float d[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) d[j] = static_cast<float>(e[u][j]) * f;
+    for (int j = 0; j < 8; ++j) d[j] = p < n ? static_cast<float>(e[u][j]) * f : 0.0f;
     if (x.smoothing > 0.0f && p < n) {
       const int loc = a.loc[p] - a.v0;
 #pragma unroll
@@ -480,7 +486,8 @@ hipError_t launch_logits(const XentArgs& x, LogitsTile tile, hipStream_t stream)
 }
 
 hipError_t launch_scale(const XentArgs& x, hipStream_t stream) {
-  const dim3 grid((x.g.B + kScaleRows - 1) / kScaleRows + (x.g.first_slice ? 1 : 0),
+  const int blocks = (x.g.B + kGradPlaces - 1) / kGradPlaces * (kGradPlaces / kScaleRows);
+  const dim3 grid(blocks + (x.g.first_slice ? 1 : 0),
                   (x.g.nv + kScaleCols - 1) / kScaleCols);
   xent_scale_kernel<<<grid, 256, 0, stream>>>(x);
   return hipGetLastError();

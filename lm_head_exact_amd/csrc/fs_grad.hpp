@@ -50,6 +50,7 @@ struct GradArgs {
   int32_t max_splits, hidden_tb, first_slice, w_splits;
 };
 
+constexpr int kGradPlaces = 32;  // places that dW takes at a time: dz is 0 behind the last one
 constexpr int kTargetTile = 256;
 constexpr int kTargetThreads = 1024;
 

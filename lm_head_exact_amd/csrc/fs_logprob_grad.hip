@@ -303,13 +303,17 @@ void grad_logits_kernel(GradArgs a) {
   T::run(w, h, a0, b0, 0, a.Dp / T::BK, acc, dyn_smem);
   const int lane = threadIdx.x & (kWave - 1), li = lane & 15, kb = lane >> 4;
   const int row0 = a0 + T::wave_a() + 4 * kb;  // in the slice
-  const bool whole = a0 + T::TA <= a.nv;
+  const bool whole = a0 + T::TA <= a.nv, full = b0 + T::TB <= n;
   RowTerm term[T::NT];
   int loc[T::NT];
-  static_for<T::NT>([&](auto n) FS_INLINE {
-    const int b = b0 + T::wave_b() + 16 * static_cast<int>(n) + li;
-    term[n] = a.term[b];
-    loc[n] = a.loc[b] - a.v0;
+  // places behind the last one: 0, whatever their hidden states of 0 made of W's infinite
+  // entries (dW reads them where it fills a k tile)
+  bool fill[T::NT];
+  static_for<T::NT>([&](auto nc) FS_INLINE {
+    const int b = b0 + T::wave_b() + 16 * static_cast<int>(nc) + li;
+    term[nc] = a.term[b];
+    loc[nc] = a.loc[b] - a.v0;
+    fill[nc] = !full && b >= n;
   });
   __bf16* out = a.dz + static_cast<size_t>(b0 + T::wave_b()) * a.ldz + a0 + T::wave_a();
   T::store_rows(
@@ -324,7 +328,7 @@ void grad_logits_kernel(GradArgs a) {
           // (the difference first, rounded once: it holds for logits of any size)
           const float x = __builtin_fmaf(z[r], term[n].inv_t, -term[n].lse);
           d[r] = __builtin_amdgcn_exp2f(x * 1.44269504088896341f) * term[n].coef;
-          d[r] = v == loc[n] || (!whole && v >= a.nv) ? 0.0f : d[r];
+          d[r] = v == loc[n] || (!whole && v >= a.nv) || fill[n] ? 0.0f : d[r];
         });
         return pack_bf16(d[0], d[1], d[2], d[3]);
       },
@@ -606,6 +610,7 @@ template <> struct HiddenTile<128> { using T = Tile<kKM, kKC, 4, 2, 4, 4, 3>; };
 template <> struct HiddenTile<256> { using T = Tile<kKM, kKC, 2, 4, 8, 4, 4, 32>; };
 using WeightsTall = Tile<kKM, kKM, 2, 4, 8, 4, 5, 32>;   // 256 columns x 256 vocabulary rows
 using WeightsShort = Tile<kKM, kKM, 1, 4, 8, 4, 3, 32>;  // 128 x 256, 4 waves, two blocks per CU
+static_assert(WeightsTall::BK == kGradPlaces && WeightsShort::BK == kGradPlaces, "places of a k tile");
 
 template <class Kernel>
 hipError_t launch_tiles(Kernel kernel, SmemRaised& raised, int64_t tiles, int threads, size_t smem,

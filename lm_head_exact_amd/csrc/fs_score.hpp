@@ -75,9 +75,9 @@ __device__ __forceinline__ void close_target(float rest, float zt, float& nll, f
 // and one exp2: (z - mz) log2(e) / T holds for logits of any size, where z log2(e) / T
 // would leave fp32 from 2.4e38 T on, and lose the largest logit's own digits long before
 // (masks of the type's lowest value gave NaN).  The instruction more is 2 to 4% of a call
-// with rows of 64 (4096 tokens on 20000: 59.5 -> 61.3 us), nothing from 1024 on.  `plain` (the same on all
-// lanes): no row of the wave is outside [0, V) or any of its tokens' target, so nothing
-// is excluded.
+// with rows of 64 (4096 tokens on 20000: 59.5 -> 61.3 us), nothing from 1024 on.
+// `plain` (the same on all lanes): no row of the wave is outside [0, V) or any of its
+// tokens' target, so nothing is excluded.
 template <int MR, int QS = 16, class Z>
 __device__ __forceinline__ void fold_logits(const Z& z, int row0, int32_t V, int loc, bool plain,
                                             float inv_t, float& m, float& s, float& zt,
