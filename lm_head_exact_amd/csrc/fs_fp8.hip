@@ -1,6 +1,8 @@
 // fs_fp8.hip -- entry points of the LM head in 8-bit floating point.
 #include "fs_fp8.hpp"
 
+#include <algorithm>
+
 #include "fs_host.hpp"
 #include "fs_internal.hpp"
 
@@ -15,7 +17,8 @@ struct Fp8Layout {
     const bool streams = fp8_streams(B, D);
     Dp = static_cast<int32_t>(round_up(D, kQuantBlock));
     Bp = static_cast<int32_t>(round_up(B, 256));
-    const size_t S = streams ? kMaxFp8StreamBlocks
+    // (a streaming block takes a group of 16 rows at least)
+    const size_t S = streams ? std::min(kMaxFp8StreamBlocks, fp8_groups(V))
                              : (static_cast<size_t>(V) + rows_of(fp8_tile(B, D, V)) - 1) /
                                    rows_of(fp8_tile(B, D, V));
     size_t at = 0;

@@ -1,5 +1,6 @@
 // fs_logprob.hip -- log-probabilities of given tokens straight from hidden
 // states and the LM head (fs_token_logprobs): the B x V logits stay on chip.
+#include <algorithm>
 #include <cmath>
 
 #include "fs_host.hpp"
@@ -411,7 +412,9 @@ fs_status run_score(const char* who, const void* h, const void* W, int32_t B, in
 }  // namespace
 
 ScoreLayout::ScoreLayout(int32_t B, int32_t D, int32_t V) {
-  const size_t S = streams(B, D) ? kMaxStreamBlocks : tile_count(B, V);
+  // (a streaming block takes a group of 16 rows at least)
+  const int64_t groups = (static_cast<int64_t>(V) + 3 + 15) / 16;
+  const size_t S = streams(B, D) ? std::min<int64_t>(kMaxStreamBlocks, groups) : tile_count(B, V);
   target = round_up(sizeof(float2) * S * B, 256);
   part = 0;
   pad = target + round_up(sizeof(float) * B, 256);
