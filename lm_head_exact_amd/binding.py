@@ -1021,7 +1021,13 @@ def clip_grad_norm(grads, max_norm: float, out=None, norm: Optional[torch.Tensor
 
 
 # ---- the LM head in 8-bit floating point ----
-_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+def _fp8_types():
+    """(e4m3, e8m0): torch has the scales' type from 2.7 on, and the bf16 calls do not need it."""
+    try:
+        return torch.float8_e4m3fn, torch.float8_e8m0fnu
+    except AttributeError as e:
+        raise RuntimeError("the 8-bit head needs torch.float8_e4m3fn and torch.float8_e8m0fnu, which "
+                           f"torch {torch.__version__} does not have") from e
 
 
 def _blocks(n: int) -> int:
@@ -1034,6 +1040,7 @@ def quantize_weights_fp8(W: torch.Tensor, packed: bool = True, out=None):
     128)][ceil(D / 128)]); the values float8_e4m3fn, in the fragment order that
     logits_fp8, sample_fp8 and token_logprobs_fp8 read (1-D; D % 64 == 0), or with
     packed false row-major [V][D].  out: (values, scales) to write into."""
+    e4m3, e8m0 = _fp8_types()
     _req(W, "W", torch.bfloat16, 2)
     V, D = W.shape
     _int32(V, D)
@@ -1042,8 +1049,8 @@ def quantize_weights_fp8(W: torch.Tensor, packed: bool = True, out=None):
     if need == 0 and V > 0:
         _check(lib().fs_quantize_weights_fp8(None, V, D, int(packed), None, 0, None, None))
     q, scale = (None, None) if out is None else out
-    q = _out(q, "values", (need,) if packed else (V, D), _E4M3, dev)
-    scale = _out(scale, "scales", (_blocks(V), _blocks(D)), _E8M0, dev)
+    q = _out(q, "values", (need,) if packed else (V, D), e4m3, dev)
+    scale = _out(scale, "scales", (_blocks(V), _blocks(D)), e8m0, dev)
     if out is not None:
         _apart((q, scale), (W,))
     _call(lib().fs_quantize_weights_fp8, dev, _addr(W), V, D, int(packed), _addr(q), _nbytes(q),
@@ -1056,13 +1063,14 @@ def quantize_weights_fp8(W: torch.Tensor, packed: bool = True, out=None):
 def pack_weights_fp8(q: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """fs_pack_weights_fp8: row-major e4m3 weights [V][D] in the fragment order of
     the 8-bit products (once, as at model load)."""
-    _req(q, "q", _E4M3, 2)
+    e4m3, _ = _fp8_types()
+    _req(q, "q", e4m3, 2)
     V, D = q.shape
     _int32(V, D)
     given, need = out, int(lib().fs_fp8_weights_bytes(V, D, 1))
     if need == 0:
         _check(lib().fs_pack_weights_fp8(None, V, D, None, 0, None))
-    out = _out(out, "out", (need,), _E4M3, q.device)
+    out = _out(out, "out", (need,), e4m3, q.device)
     if given is not None:
         _apart((out,), (q,))
     _call(lib().fs_pack_weights_fp8, q.device, _addr(q), V, D, _addr(out), _nbytes(out))
@@ -1078,11 +1086,12 @@ def fp8_workspace_bytes(B: int, D: int, V: int) -> int:
 
 def _fp8_head(h, W_packed, W_scale, V, vocab_offset, workspace):
     """Checks of the 8-bit products: (device, B, D, workspace)."""
+    e4m3, e8m0 = _fp8_types()
     _req(h, "h", torch.bfloat16, 2)
     if isinstance(W_packed, torch.Tensor) and W_packed.dim() == 2:
         raise ValueError("W_packed must be in fragment order (quantize_weights_fp8, pack_weights_fp8)")
-    _req(W_packed, "W_packed", _E4M3, 1)
-    _req(W_scale, "W_scale", _E8M0, 2)
+    _req(W_packed, "W_packed", e4m3, 1)
+    _req(W_scale, "W_scale", e8m0, 2)
     B, D = h.shape
     _int32(B, D, V, vocab_offset)
     need = int(lib().fs_fp8_weights_bytes(V, D, 1))
