@@ -37,7 +37,7 @@ __device__ __forceinline__ int scale_byte(uint32_t amax) {
   const int e = static_cast<int>(amax >> 7) - 8 + ((amax & 0x7F) > 0x60);
   return amax == 0 ? 127 : max(e, 127 - 110);
 }
-// 2^e and 2^-e of a scale byte (17 to 248).
+// 2^e and 2^-e of a scale byte (17 to 247).
 __device__ __forceinline__ float scale_up(int byte) { return __int_as_float(byte << 23); }
 __device__ __forceinline__ float scale_down(int byte) { return __int_as_float((254 - byte) << 23); }
 
