@@ -4,7 +4,7 @@
 // compile in parallel.
 //
 // One block computes TA vocabulary rows by TB tokens; a wave holds MR x NT tiles of
-// 32 x 32 (v_mfma_scale_f32_32x32x64_f8f6f4, W as operand A).  Both operands go
+// 32 x 32 (v_mfma_scale_f32_32x32x64_f8f6f4, W as operand A; EXACT: below).  Both operands go
 // through LDS, staged by direct global->LDS loads in a ring of S slots of 128 k:
 // 128 bytes per row, as the 64 bf16 of the training products' slots, whose
 // staging (Tile) it shares.  A slot has two steps of 64 k, whose fragments are read
@@ -17,14 +17,15 @@
 // one block of 128).  Both live in LDS for the whole call of a block.
 //
 // Rounding.  The instruction aligns the products of eight neighbouring k to the
-// largest of them and keeps 13 bits below it; sums of such groups are fp32
-// (measured: bytes planted 12 binades below the largest of their eight keep their
+// largest of them and cuts each 13 bits below it, towards zero; sums of such groups are
+// fp32 (measured: bytes planted 12 binades below the largest of their eight keep their
 // first bit, two further none; those of other groups are exact).  On normal data that
-// is 1.5e-5 of a logit's spread, without a bias: a thousandth of what the values'
-// own four bits leave.
+// is 1.5e-5 of a logit's spread, a thousandth of what the values' own four bits leave.
+// Where the products of a logit share a sign (h along the row of W) nothing averages
+// it: such a logit comes out 1e-5 of it too small (7e-4 of 82, D = 1024 or 4096).
 // Exact products (EXACT) widen the same fragments to bf16, which holds four bits times a
-// power of two: four products of 16 k for one of 64, at half its rate.  Scores on few
-// entries take them (fs_fp8_tile_scores.hip).
+// power of two: four products of 16 k for one of 64, at half its rate.  Samples, logits in
+// fp32 and scores on few entries or of few rows take them (fs_fp8_tile_*.hip).
 #pragma once
 
 #include "fs_fp8.hpp"
