@@ -337,8 +337,10 @@ void grad_logits_kernel(GradArgs a) {
 }
 
 // dW of one slice: rows v of W, columns d, summed over the rows with a target.  SPLIT:
-// over one part of them, into the part's slab.
-template <class T, bool SPLIT>
+// over one part of them, into the part's slab.  NTS: stores that pass the caches (a kernel
+// of its own: the compiler joins the last stores of two branches, and the joined one has
+// lost the hint).
+template <class T, bool SPLIT, bool NTS>
 __global__ __launch_bounds__(T::kThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void grad_weights_kernel(GradArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char dyn_smem[];
@@ -389,17 +391,14 @@ void grad_weights_kernel(GradArgs a) {
   });
   const int v0 = b0 + T::wave_b(), c0 = a0 + T::wave_a();
   __bf16* out = a.dW + (static_cast<size_t>(a.v0) + v0) * a.D + c0;
-  auto packed = [&](auto m, auto n) FS_INLINE {
-    const f32x4 x = acc[m][n];
-    return pack_bf16(x[0], x[1], x[2], x[3]);
-  };
-  auto row = [&](int r) FS_INLINE { return out + static_cast<size_t>(r) * a.D; };
-  auto keep = [&](int r, int c) FS_INLINE { return v0 + r < a.nv && c0 + c < a.D; };
-  // Past the caches where every row starts a line; else lines are filled by two tiles
-  // (14 rows on 97002 x 2616: 124 us, past the caches 195; losses and dW of 64 rows on
-  // 128256 x 4096 497 us past them, 548 through them).
-  if (a.D % 64 == 0) T::template store_rows<true>(dyn_smem, packed, row, keep);
-  else T::template store_rows<false>(dyn_smem, packed, row, keep);
+  T::template store_rows<NTS>(
+      dyn_smem,
+      [&](auto m, auto n) FS_INLINE {
+        const f32x4 x = acc[m][n];
+        return pack_bf16(x[0], x[1], x[2], x[3]);
+      },
+      [&](int r) FS_INLINE { return out + static_cast<size_t>(r) * a.D; },
+      [&](int r, int c) FS_INLINE { return v0 + r < a.nv && c0 + c < a.D; });
 }
 
 // x + t * w for four consecutive columns of a row of W.
@@ -656,10 +655,10 @@ hipError_t launch_hidden(const GradArgs& a, hipStream_t stream) {
                               : launch_hidden<HiddenTile<256>::T>(a, stream);
 }
 
-template <class T, bool SPLIT = false>
+template <class T, bool SPLIT, bool NTS>
 hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
   static SmemRaised raised;
-  return launch_tiles(&grad_weights_kernel<T, SPLIT>, raised,
+  return launch_tiles(&grad_weights_kernel<T, SPLIT, NTS>, raised,
                       static_cast<int64_t>((a.nv + T::TB - 1) / T::TB) *
                           ((a.D + T::TA - 1) / T::TA) * (SPLIT ? a.w_splits : 1),
                       T::kThreads, T::kSmemBytes, a, stream);
@@ -670,11 +669,19 @@ hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
 // of the vocabulary 137 against 175 us, 2048 tokens 434 against 448 us; with
 // many rounds the tall blocks read less (2048 tokens on the whole of it 1793
 // against 1860 us, equal at 512).
+template <bool NTS>
 hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
-  if (a.w_splits > 1) return launch_weights<WeightsShort, true>(a, stream);
   const int64_t tall = static_cast<int64_t>((a.nv + 255) / 256) * ((a.D + 255) / 256);
-  return a.B > 512 && tall >= 16 * 256 ? launch_weights<WeightsTall>(a, stream)
-                                       : launch_weights<WeightsShort>(a, stream);
+  return a.B > 512 && tall >= 16 * 256 ? launch_weights<WeightsTall, false, NTS>(a, stream)
+                                       : launch_weights<WeightsShort, false, NTS>(a, stream);
+}
+
+// Past the caches where every row starts a line; else lines are filled by two tiles
+// (14 rows on 97002 x 2616: 124 us, past the caches 195; losses and dW of 64 rows on
+// 128256 x 4096 497 us past them, 548 through them).
+hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
+  if (a.w_splits > 1) return launch_weights<WeightsShort, true, false>(a, stream);
+  return a.D % 64 == 0 ? launch_weights<true>(a, stream) : launch_weights<false>(a, stream);
 }
 
 hipError_t run_grad(GradArgs& a, const GradPlan& p, hipStream_t s) {
