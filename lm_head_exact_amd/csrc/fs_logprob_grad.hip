@@ -676,12 +676,21 @@ hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
                                        : launch_weights<WeightsShort, false, NTS>(a, stream);
 }
 
-// Past the caches where every row starts a line; else lines are filled by two tiles
-// (14 rows on 97002 x 2616: 124 us, past the caches 195; losses and dW of 64 rows on
-// 128256 x 4096 497 us past them, 548 through them).
+// Past the caches where every row starts a line.  Else lines are filled by two tiles, and
+// few rows' dW is faster through the caches (a call, through and past them: 14 rows on
+// 97002 x 2616 305 and 340 us, 64 rows 321 and 340, 100 rows on 32000 x 2056 91 and 97).  A
+// longer product gains more from what a large dW would push out of them meanwhile (dW and
+// dh: 130 rows on 97002 x 2616 563 and 549, 300 rows 819 and 788; 300 rows on 32000 x 2056
+// 217 and 210; 1025 rows on 50000 x 1016 432 and 398; on 32000 x 1000 512 rows 135 and 137,
+// 2048 rows 412 and 393).
+bool weights_pass_caches(const GradArgs& a) {
+  return a.D % 64 == 0 ||
+         (a.B > 64 && a.B * static_cast<int64_t>(a.V) > (int64_t{1} << 34) / a.D);
+}
+
 hipError_t launch_weights(const GradArgs& a, hipStream_t stream) {
   if (a.w_splits > 1) return launch_weights<WeightsShort, true, false>(a, stream);
-  return a.D % 64 == 0 ? launch_weights<true>(a, stream) : launch_weights<false>(a, stream);
+  return weights_pass_caches(a) ? launch_weights<true>(a, stream) : launch_weights<false>(a, stream);
 }
 
 hipError_t run_grad(GradArgs& a, const GradPlan& p, hipStream_t s) {
