@@ -340,8 +340,8 @@ FS_API fs_status fs_sample_unfused(const void* h, const void* W, int32_t B, int3
  *
  * Weights and hidden states as e4m3 values (no infinities, largest 448) with a
  * scale for each block of 128 columns -- and of 128 rows, for W --, products in
- * 8 bits, sums in fp32: half the bytes of a decode step and up to twice the rate
- * of a batch.  A scale is the power of two 2^e with the least e >= -110 for which
+ * 8 bits, sums in fp32: half the bytes of a decode step, and up to twice the rate
+ * of a batch's bf16 logits and log-probabilities.  A scale is the power of two 2^e with the least e >= -110 for which
  * no finite entry of its block exceeds 448 * 2^e (e = 0 for a block of zeros),
  * stored as the byte e + 127 (e8m0); values are rounded to nearest even; entries
  * that are not finite become NaN.  The last block of a row or of the vocabulary
