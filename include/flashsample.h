@@ -367,7 +367,8 @@ FS_API fs_status fs_sample_unfused(const void* h, const void* W, int32_t B, int3
  *   workspace    >= fs_fp8_workspace_bytes(B, D, V) bytes (0 for invalid sizes);
  *                contents on entry ignored
  * NaN or infinite entries of h or W give NaN in the logits that they enter (for
- * the sampler undefined ids).  All calls are asynchronous on `stream`, allocate
+ * the sampler undefined ids); finite ones of 1.9375 * 2^127 or more round to 2^128 and
+ * may be infinite in the products.  All calls are asynchronous on `stream`, allocate
  * nothing, give equal bits for equal calls and may be captured into graphs; calls
  * that overlap need distinct workspaces and outputs.  Outputs and workspaces
  * overlap neither one another nor an input. */
